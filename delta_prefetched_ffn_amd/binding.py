@@ -26,6 +26,9 @@ REDUCE_ATOMIC, REDUCE_ORDERED = 0, 1
 REDUCES = {"atomic": REDUCE_ATOMIC, "ordered": REDUCE_ORDERED}
 LAYOUTS = {"slots": 0, "compact": 1}
 ACTS = {"relu": ACT_RELU, "silu": ACT_SILU}
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
+KV_HOST = -1
+KV_MODES = {"share": 0, "copy": 1}
 _NAMES = {0: "NP_OK", 1: "NP_EINVAL", 2: "NP_ECAPACITY", 3: "NP_ENOMEM", 4: "NP_EHIP",
           5: "NP_ESTATE", 6: "NP_EDEVICE"}
 
@@ -36,7 +39,10 @@ EXPORTS = ["np_layer_create", "np_layer_destroy", "np_layer_reset", "np_delta_as
            "np_layer_raise_error", "np_probe_read", "np_probe_read_set", "np_probe_copy", "np_decode_use_graphs", "np_layer_set_window",
            "np_sparse_ffn_acc", "np_layer_set_ffn_reduce", "np_layer_set_levels",
            "np_layer_set_layout", "np_layer_read_moves", "np_decode_set_staging",
-           "np_layer_set_planar", "np_sparse_ffn_noalloc"]
+           "np_layer_set_planar", "np_sparse_ffn_noalloc",
+           "np_kv_bytes", "np_kv_create", "np_kv_destroy", "np_kv_reset", "np_kv_extend", "np_kv_append",
+           "np_kv_attend", "np_kv_fork", "np_kv_trim", "np_kv_free", "np_kv_adopt", "np_kv_evict",
+           "np_kv_compact", "np_kv_read_pages", "np_kv_read_tokens", "np_kv_info"]
 
 
 class NPError(RuntimeError):
@@ -50,6 +56,12 @@ class LayerDesc(ctypes.Structure):
                 ("n_rows", ctypes.c_int32), ("n_centroids", ctypes.c_int32),
                 ("mask_mode", ctypes.c_int32), ("act", ctypes.c_int32), ("device", ctypes.c_int32),
                 ("masks", ctypes.c_void_p), ("row_store", ctypes.c_void_p)]
+
+
+class KVDesc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("n_layers", "n_heads", "n_kv_heads", "head_dim", "page_tokens", "n_pages",
+                                              "max_seqs", "max_pages", "device")] + \
+               [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
 
 
 @lru_cache(maxsize=1)
@@ -86,6 +98,22 @@ def lib() -> ctypes.CDLL:
         "np_decode_set_staging": [i64, i32],
         "np_layer_set_planar": [vp, i32],
         "np_sparse_ffn_noalloc": [vp, vp, vp, vp],
+        "np_kv_bytes": [vp, vp],
+        "np_kv_create": [vp, vp],
+        "np_kv_destroy": [vp],
+        "np_kv_reset": [vp],
+        "np_kv_extend": [vp, i32, vp, vp, vp],
+        "np_kv_append": [vp, i32, vp, vp, i32, vp, vp],
+        "np_kv_attend": [vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, i32, i32, vp],
+        "np_kv_fork": [vp, i32, i32, i32, i32, vp],
+        "np_kv_trim": [vp, i32, i32],
+        "np_kv_free": [vp, i32],
+        "np_kv_adopt": [vp, i32, vp, i32, i32, vp],
+        "np_kv_evict": [vp, i32, i32, i32, vp, vp],
+        "np_kv_compact": [vp, vp, vp],
+        "np_kv_read_pages": [vp, i32, vp, i32, vp, vp],
+        "np_kv_read_tokens": [vp, i32, i32, i32, i32, vp, vp],
+        "np_kv_info": [vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -234,6 +262,122 @@ class Layer:
         out = np.empty((s.size, self.n_rows, self.d_model), dtype=np.uint16)
         _check(lib().np_layer_read_rows(self.h, s.ctypes.data, s.size, out.ctypes.data))
         return out
+
+
+def kv_bytes(*, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
+             max_seqs: int = 1, max_pages: int = 1) -> tuple[int, int]:
+    """Bytes of a cache's pool: (codes, exps)."""
+    desc = KVDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, KV_HOST, None, None)
+    out = (ctypes.c_int64 * 2)()
+    _check(lib().np_kv_bytes(ctypes.byref(desc), out))
+    return out[0], out[1]
+
+
+class KVCache:
+    """An 8-bit key/value cache (np_kv). codes and exps are device pointers (ints) to the caller's pool of
+    kv_bytes() bytes; device KV_HOST (no pool) keeps the books only."""
+
+    def __init__(self, *, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
+                 max_seqs: int, max_pages: int, codes: int = 0, exps: int = 0, device: int = 0, keepalive=None):
+        desc = KVDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, device,
+                      codes or None, exps or None)
+        h = ctypes.c_void_p()
+        _check(lib().np_kv_create(ctypes.byref(desc), ctypes.byref(h)))
+        self.h = h
+        self.n_layers, self.n_heads, self.n_kv_heads, self.head_dim = n_layers, n_heads, n_kv_heads, head_dim
+        self.page_tokens, self.n_pages, self.max_seqs, self.max_pages = page_tokens, n_pages, max_seqs, max_pages
+        self._keepalive = keepalive
+
+    def close(self) -> None:
+        if self.h:
+            _check(lib().np_kv_destroy(self.h))
+            self.h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            if getattr(self, "h", None):
+                lib().np_kv_destroy(self.h)
+        except Exception:
+            pass
+
+    def reset(self) -> None:
+        _check(lib().np_kv_reset(self.h))
+
+    def extend(self, seqs, n_new, stream: int = 0) -> None:
+        """seqs[i] gets n_new[i] more tokens; they become the current tokens of append and attend."""
+        n = len(seqs)
+        if len(n_new) != n:
+            raise ValueError(f"extend: {n} sequences and {len(n_new)} counts")
+        a = ctypes.c_int32 * n
+        _check(lib().np_kv_extend(self.h, n, a(*seqs), a(*n_new), stream or None))
+
+    def append(self, layer: int, k_ptr: int, v_ptr: int, dtype: str, strides=None, stream: int = 0) -> None:
+        """Stores the current tokens' k, v [rows][n_kv_heads][head_dim]; strides (elements): k row, k head, v row, v head."""
+        st = None if strides is None else (ctypes.c_int64 * 4)(*strides)
+        rc = lib().np_kv_append(self.h, layer, k_ptr, v_ptr, DTYPES[dtype], st, stream or None)
+        if rc:
+            _check(rc)
+
+    def attend(self, layer: int, q_ptr: int, out_ptr: int, dtype: str, strides=None, *, scale: float, window: int = 0,
+               sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
+        """Attention of the current tokens: q, out [rows][n_heads][head_dim]; strides (elements): q row, q head, out row,
+        out head; window 0: every earlier token, else the last `window` and the first `sinks`."""
+        st = None if strides is None else (ctypes.c_int64 * 4)(*strides)
+        rc = lib().np_kv_attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], st, scale, window, sinks,
+                                stream or None)
+        if rc:
+            _check(rc)
+
+    def fork(self, src: int, dst: int, n_tokens: int, mode: str = "share", stream: int = 0) -> None:
+        """The empty sequence dst becomes the first n_tokens of src ("share": shared pages, copied on write; "copy")."""
+        _check(lib().np_kv_fork(self.h, src, dst, n_tokens, KV_MODES[mode], stream or None))
+
+    def trim(self, seq: int, n_tokens: int) -> None:
+        _check(lib().np_kv_trim(self.h, seq, n_tokens))
+
+    def free(self, seq: int) -> None:
+        _check(lib().np_kv_free(self.h, seq))
+
+    def adopt(self, seq: int, pages, n_tokens: int, stream: int = 0) -> None:
+        """The empty sequence seq becomes these pages of the pool, holding n_tokens tokens."""
+        p = np.ascontiguousarray(pages, dtype=np.int32)
+        _check(lib().np_kv_adopt(self.h, seq, p.ctypes.data, p.size, n_tokens, stream or None))
+
+    def evict(self, seq: int, window: int, sinks: int = 0, stream: int = 0) -> int:
+        """Drops the pages that no later query of this window sees; how many."""
+        n = ctypes.c_int32(0)
+        _check(lib().np_kv_evict(self.h, seq, window, sinks, ctypes.byref(n), stream or None))
+        return n.value
+
+    def compact(self, stream: int = 0) -> int:
+        """Moves the pages in use to the front of the pool; how many moved."""
+        n = ctypes.c_int32(0)
+        _check(lib().np_kv_compact(self.h, ctypes.byref(n), stream or None))
+        return n.value
+
+    def pages(self, seq: int) -> np.ndarray:
+        out = np.empty(self.max_pages, dtype=np.int32)
+        n = ctypes.c_int32(0)
+        _check(lib().np_kv_read_pages(self.h, seq, out.ctypes.data, out.size, ctypes.byref(n), None))
+        return out[: n.value].copy()
+
+    def tokens(self, seq: int) -> int:
+        n, t = ctypes.c_int32(0), ctypes.c_int32(0)
+        _check(lib().np_kv_read_pages(self.h, seq, None, 0, ctypes.byref(n), ctypes.byref(t)))
+        return t.value
+
+    def read_tokens(self, layer: int, seq: int, first: int = 0, n: int | None = None) -> tuple[np.ndarray, np.ndarray]:
+        """Keys and values fp32 [n][n_kv_heads][head_dim] of tokens [first, first + n) (host)."""
+        n = self.tokens(seq) - first if n is None else n
+        k = np.empty((max(n, 0), self.n_kv_heads, self.head_dim), dtype=np.float32)
+        v = np.empty_like(k)
+        _check(lib().np_kv_read_tokens(self.h, layer, seq, first, n, k.ctypes.data, v.ctypes.data))
+        return k, v
+
+    def info(self) -> dict:
+        out = (ctypes.c_int32 * 4)()
+        _check(lib().np_kv_info(self.h, out))
+        return dict(zip(["n_pages", "free", "shared", "current"], list(out)))
 
 
 def decode_step(layers, cids: np.ndarray, x_ptr: int, y_ptr: int, compute_stream: int = 0,

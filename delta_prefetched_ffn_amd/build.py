@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnp.so")
-SOURCES = ["np_api.hip", "k_delta.hip", "k_scatter.hip", "k_ffn.hip"]
+SOURCES = ["np_api.hip", "np_kv.hip", "k_delta.hip", "k_scatter.hip", "k_ffn.hip", "k_kv.hip", "k_attn.hip"]
+HEADERS = ["np_internal.hpp", "np_host.hpp", "kv_internal.hpp", "kv_device.hpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -64,8 +65,7 @@ def build_sanitized(force: bool = False) -> str:
     A process loading it needs the clang ASan runtime preloaded (sanitizer_runtime())."""
     obj_dir = os.path.dirname(SAN_LIB)
     os.makedirs(obj_dir, exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, "np_internal.hpp"),
-                                                      os.path.join(INCLUDE, "np.h")]
+    srcs = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, "np.h")]
     if not force and os.path.exists(SAN_LIB) and os.path.getmtime(SAN_LIB) >= max(map(os.path.getmtime, srcs)):
         return SAN_LIB
 

@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "np.h"
+#include "np_host.hpp"
 #include "np_internal.hpp"
 
 namespace np {
@@ -61,7 +62,9 @@ void setup_scratch(int dev) {
 }
 
 thread_local std::string g_err;
+}  // namespace
 
+namespace np {
 np_status fail(np_status st, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -72,26 +75,23 @@ np_status fail(np_status st, const char* fmt, ...) {
     return st;
 }
 
-#define NP_HIP(call)                                                                          \
-    do {                                                                                      \
-        hipError_t e_ = (call);                                                               \
-        if (e_ != hipSuccess) return fail(NP_EHIP, "%s failed: %s", #call, hipGetErrorString(e_)); \
-    } while (0)
-
-// Makes `dev` current for the scope and restores the previous device.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-        if (prev != dev) ok = hipSetDevice(dev) == hipSuccess;
+np_status check_io_ptr(const void* p, int dev, const char* what, const char* owner) {
+    hipPointerAttribute_t attr;
+    std::memset(&attr, 0, sizeof attr);
+    if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(NP_EINVAL, "%s is neither device memory nor pinned host memory", what);
     }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+    if (attr.type == hipMemoryTypeDevice) {
+        if (attr.device != dev) return fail(NP_EINVAL, "%s lives on device %d, the %s on device %d", what, attr.device, owner, dev);
+        return NP_OK;
     }
-};
+    if (attr.type == hipMemoryTypeHost && attr.devicePointer) return NP_OK;
+    return fail(NP_EINVAL, "%s (memory type %d) is not device memory or mapped pinned host memory", what, (int)attr.type);
+}
+}  // namespace np
 
+namespace {
 enum LayerState { kFresh = 0, kAssigned = 1, kScattered = 2 };
 constexpr size_t kCountsBytes = 8 * 4 + 2 * 8;  // int32 counts[8] + 2 x uint64 running sums (cleared by resets)
 constexpr size_t kCountsAlloc = kCountsBytes + 8;  // + the device address of the host error word
@@ -537,29 +537,9 @@ np_status enqueue_step_ffn(np_layer* L, const float* x, float* y, hipStream_t s,
     return enqueue_ffn(L, x, y, s, prm, layer, read_through_ok(L), y_holds_base, nullptr, pf, pf_fixed);
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // Error bits that a kernel of the layer raised since its last reset (read without synchronizing:
 // a kernel still running may add some later). Calls that enqueue work for the layer refuse it
 // with NP_EDEVICE while any are set.
-// x and y must be memory the layer's device can read and write: its own device memory or pinned
-// host memory mapped for it. A pageable host pointer (or another device's memory) would fault the
-// GPU instead of failing here.
-np_status check_io_ptr(const void* p, int dev, const char* what) {
-    hipPointerAttribute_t attr;
-    std::memset(&attr, 0, sizeof attr);
-    if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
-        (void)hipGetLastError();
-        return fail(NP_EINVAL, "%s is neither device memory nor pinned host memory", what);
-    }
-    if (attr.type == hipMemoryTypeDevice) {
-        if (attr.device != dev) return fail(NP_EINVAL, "%s lives on device %d, the layer on device %d", what, attr.device, dev);
-        return NP_OK;
-    }
-    if (attr.type == hipMemoryTypeHost && attr.devicePointer) return NP_OK;
-    return fail(NP_EINVAL, "%s (memory type %d) is not device memory or mapped pinned host memory", what, (int)attr.type);
-}
-
 np_status check_device_err(const np_layer* L, int index = -1) {
     const uint32_t bits = L->err_h ? __atomic_load_n(L->err_h, __ATOMIC_ACQUIRE) : 0u;
     if (!bits) return NP_OK;

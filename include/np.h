@@ -380,6 +380,170 @@ const char* np_last_error(void);
  * kernel on `stream` would: for testing the reporting without a failing kernel. */
 np_status np_layer_raise_error(np_layer* layer, int32_t bits, void* stream);
 
+/* ---- 8-bit key/value cache and the attention over it ----
+ *
+ * The attention of the decode steps that np_decode_step runs the FFNs of: keys
+ * and values of past tokens in 8 bits, in pages that sequences share, so that
+ * the cache leaves the device memory to the resident rows.
+ *
+ * Format. A pool of n_pages pages of page_tokens tokens, the same page number
+ * in every layer:
+ *   codes  uint8 [n_layers][n_pages][n_kv_heads][2][page_tokens / 16][S][1024]
+ *   exps   int8  [n_layers][n_pages][n_kv_heads][2]
+ * (fourth index of codes, last of exps: 0 K, 1 V; S = ceil(head_dim / 64)). A
+ * code is an e4m3 number (4 exponent bits, bias 7, 3 fraction bits, no
+ * infinity, 0x7f and 0xff NaN); the value is code * 2^exp, one exponent per
+ * page, head, and K or V (the quantisation block). 1024 bytes hold 16 tokens x
+ * 64 values: for K, byte (16 g + t) * 16 + b is token t, value 16 g + b; for
+ * V, byte (16 g + r) * 16 + 4 i + t is token 4 g + t, value 4 r + i.
+ * Values past head_dim are zero. Bytes of tokens that a sequence has not
+ * reached are unspecified.
+ *
+ * A sequence is a list of pages and a length: token j lies in its page
+ * j / page_tokens. The page lists live on the host (the library's, exact) and
+ * are mirrored on the device; pages are shared by reference count, and a
+ * shared page is copied before a sequence writes into it. New pages are the
+ * free pages with the lowest numbers.
+ *
+ * A step: np_kv_extend says which sequences get how many new tokens; then, for
+ * every layer, np_kv_append stores those tokens' keys and values and
+ * np_kv_attend computes their attention. Rows of k, v, q and out are the new
+ * tokens in the order of np_kv_extend: the first sequence's, then the
+ * second's. Calls of one cache must be ordered (one stream, or the caller's
+ * events) and are not thread-safe; different caches are independent. Calls
+ * that a graph captures replay with the sequences and lengths of the capture.
+ * After NP_EHIP from a call that changes the cache, np_kv_reset is needed
+ * (NP_ESTATE until then). Limits: 1 <= n_layers <= 1024, 1 <= n_kv_heads <=
+ * 1024, n_heads a multiple of it and <= 4096, head_dim a multiple of 8 in
+ * [8, 256], page_tokens 16, 32, 64 or 128, 1 <= n_pages <= 2^24,
+ * 1 <= max_seqs <= 4096, max_pages * page_tokens <= 2^28,
+ * max_seqs * max_pages <= 2^28. */
+typedef struct np_kv np_kv; /* opaque: one cache */
+
+typedef enum { NP_F32 = 0, NP_BF16 = 1, NP_F16 = 2 } np_dtype;
+typedef enum { NP_KV_SHARE = 0, NP_KV_COPY = 1 } np_kv_mode;
+
+/* desc.device of a cache without a device: it keeps the books (pages,
+ * lengths, every refusal) as another would and enqueues nothing; append,
+ * attend and read_tokens fail with NP_ESTATE. For schedulers that plan ahead. */
+#define NP_KV_HOST (-1)
+
+typedef struct np_kv_desc {
+    int32_t n_layers;
+    int32_t n_heads;     /* query heads                                      */
+    int32_t n_kv_heads;  /* key/value heads; n_heads / n_kv_heads share one  */
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t n_pages;     /* of the pool                                      */
+    int32_t max_seqs;    /* sequences 0 .. max_seqs - 1                      */
+    int32_t max_pages;   /* pages of one sequence at most                    */
+    int32_t device;      /* HIP device ordinal, or NP_KV_HOST                */
+    /* The pool, BORROWED: device memory of the sizes np_kv_bytes gives, codes
+     * 16-byte aligned, alive while the cache exists. The caller may save and
+     * restore it (np_kv_adopt). Not used with NP_KV_HOST. */
+    void* codes;
+    int8_t* exps;
+} np_kv_desc;
+
+/* Bytes of the pool: out2[0] of codes, out2[1] of exps. */
+np_status np_kv_bytes(const np_kv_desc* desc, int64_t* out2);
+
+/* A cache of empty sequences. The contents of the pool are kept. desc is
+ * copied. Errors: NP_EINVAL (a limit above, a pointer that the device cannot
+ * reach), NP_ENOMEM, NP_EHIP; *out is NULL on any error. */
+np_status np_kv_create(const np_kv_desc* desc, np_kv** out);
+
+/* Synchronizes the device and frees what the cache allocated (not the pool). */
+np_status np_kv_destroy(np_kv* kv);
+
+/* Every sequence empty, every page free; clears device errors. Enqueues
+ * nothing (it synchronizes only if there is an error to clear). */
+np_status np_kv_reset(np_kv* kv);
+
+/* Gives seqs[i] room for n_new[i] >= 0 more tokens (host arrays of n <= 128,
+ * the sequences distinct): their lengths grow, pages are taken, a last page
+ * that other sequences share is copied (all layers), and these tokens become
+ * the current ones of append and attend, until the next np_kv_extend or until
+ * trim, free, evict, fork (as dst) or adopt changes one of the sequences.
+ * Errors (nothing changed): NP_EINVAL, NP_ECAPACITY (max_pages, or too few
+ * free pages). */
+np_status np_kv_extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new, void* stream);
+
+/* Stores the current tokens' keys and values of one layer: k, v
+ * [rows][n_kv_heads][head_dim] of dtype, 16-byte aligned; strides (host, in
+ * elements, multiples of 16 bytes; NULL: contiguous) are k's row and head
+ * stride, then v's. Per block (page, head, K or V), with x the new values and
+ * the page's earlier tokens at exponent e0:
+ *   e = the smallest exponent in [-120, 120] with |x| <= 448 * 2^e, at least e0;
+ *   codes = x * 2^-e rounded to e4m3 (nearest even), and if e > e0 the earlier
+ *   codes * 2^(e0 - e) rounded again.
+ * Infinities are stored as +-448 * 2^e and NaN as NaN; neither enters e. A
+ * second call for the same tokens overwrites them, but e does not go down
+ * again for a page that holds earlier tokens.
+ * Errors: NP_EINVAL, NP_ESTATE (no current tokens), NP_EDEVICE. */
+np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t dtype, const int64_t* strides,
+                       void* stream);
+
+/* Attention of the current tokens over their own sequences. For the row at
+ * position i of its sequence and query head h, over the visible tokens j of
+ * key/value head h / (n_heads / n_kv_heads):
+ *   s_j = scale * q . k_j,   out = sum exp(s_j) v_j / sum exp(s_j).
+ * Token j is visible if j <= i, its page is held (np_kv_evict), and, with
+ * window > 0, i - j < window or j < sinks: a sliding window with a few first
+ * tokens that stay visible. A row without a visible token gives 0 (lse -inf).
+ * q, out [rows][n_heads][head_dim] of dtype, 16-byte aligned; strides as
+ * above: q's row and head stride, then out's (whose elements must not
+ * overlap). lse, fp32 [rows][n_heads], receives ln sum exp(s_j) (NULL: not).
+ * Sums and softmax statistics are fp32; K and V enter exactly (V scales of
+ * one head that lie more than 2^40 below the largest vanish); the weights
+ * exp(s_j) are rounded to fp16 for 16-bit dtypes and kept to 24 bits for
+ * NP_F32. Results are the same from run to run.
+ * Errors: NP_EINVAL (scale not positive and finite, a negative window), NP_ESTATE (no
+ * current tokens), NP_EDEVICE. */
+np_status np_kv_attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,
+                       const int64_t* strides, float scale, int32_t window, int32_t sinks, void* stream);
+
+/* Makes the empty sequence dst the first n_tokens of src: NP_KV_SHARE shares
+ * their pages (no copy now; whichever sequence first writes into a shared last
+ * page gets a copy of its own), NP_KV_COPY copies them. Errors: NP_EINVAL (dst
+ * not empty, n_tokens above src's, or inside a page that src has dropped),
+ * NP_ECAPACITY. */
+np_status np_kv_fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mode, void* stream);
+
+/* Shortens seq to n_tokens (rejected drafts) and gives back the pages past
+ * them; np_kv_free gives back all. Enqueues nothing: pages are used again by
+ * later calls of the same order. */
+np_status np_kv_trim(np_kv* kv, int32_t seq, int32_t n_tokens);
+np_status np_kv_free(np_kv* kv, int32_t seq);
+
+/* Makes the empty sequence seq the given pages (host, n_pages of them, each
+ * free; -1: a page of past tokens that was dropped) holding n_tokens tokens
+ * that the pool already contains: a restored or planned cache. Pages past the
+ * tokens stay reserved for the sequence. */
+np_status np_kv_adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens, void* stream);
+
+/* Gives back seq's pages whose tokens no later query sees with this window and
+ * these sinks (call it after the step's last attend). *n_freed (may be NULL):
+ * pages dropped. Without a window, attend does not see them either. */
+np_status np_kv_evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed, void* stream);
+
+/* Moves the pages in use to the front of the pool, so that pages [in use,
+ * n_pages) are free: the k-th page in use past the front (ascending) goes to
+ * the k-th free page of the front, in every layer. *n_moved (may be NULL). The
+ * current tokens stay. */
+np_status np_kv_compact(np_kv* kv, int32_t* n_moved, void* stream);
+
+/* The pages (host int32 [cap >= *n_pages], may be NULL) and length of seq. */
+np_status np_kv_read_pages(const np_kv* kv, int32_t seq, int32_t* pages, int32_t cap, int32_t* n_pages, int32_t* n_tokens);
+
+/* Tokens [first, first + n) of seq in one layer as fp32 [n][n_kv_heads][head_dim]
+ * on the host (k or v may be NULL; dropped tokens are 0). Synchronizes the device. */
+np_status np_kv_read_tokens(const np_kv* kv, int32_t layer, int32_t seq, int32_t first, int32_t n, float* k, float* v);
+
+/* out4 = {pages, free pages, pages shared by several sequences, sequences of
+ * the current step}. */
+np_status np_kv_info(const np_kv* kv, int32_t* out4);
+
 /* ---- measurement probes (roofline denominators and counter scaling) ---- */
 
 /* Streaming read of `bytes` (multiple of 16) at src (device or pinned host);

@@ -1,0 +1,450 @@
+"""The 8-bit key/value cache on the GPU against the fp64 definitions in tests/kv_reference.py: appended codes and exponents
+exactly, attention within bounds counted from its roundings."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import kv_reference as R
+from tests.harness import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+torch = None
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _torch():
+    global torch
+    torch = torch_mod()
+    assert torch.cuda.is_available()
+
+
+def tdt(name):
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+class Env:
+    """A cache, its pool (every byte NaN codes to begin with, so that nothing unwritten may matter) and its reference."""
+
+    def __init__(self, *, heads=4, kv=2, hd=64, page=16, pages=64, seqs=4, layers=1, max_pages=None, seed=0):
+        from delta_prefetched_ffn_amd import KVCache, kv_bytes
+        shape = dict(n_layers=layers, n_heads=heads, n_kv_heads=kv, head_dim=hd, page_tokens=page, n_pages=pages)
+        nc, ne = kv_bytes(**shape)
+        self.codes = torch.full((nc,), 0x7F, dtype=torch.uint8, device="cuda")
+        self.exps = torch.full((ne,), 100, dtype=torch.int8, device="cuda")
+        self.kv = KVCache(**shape, max_seqs=seqs, max_pages=max_pages or pages, codes=self.codes.data_ptr(), exps=self.exps.data_ptr(),
+                          keepalive=(self.codes, self.exps))
+        self.heads, self.nkv, self.hd, self.page, self.layers = heads, kv, hd, page, layers
+        self.ref = [[R.RefSeq(kv, hd, page) for _ in range(seqs)] for _ in range(layers)]
+        self.rng = np.random.default_rng(seed)
+        self.current = []
+
+    def stream(self):
+        return torch.cuda.current_stream().cuda_stream
+
+    def extend(self, seqs, new):
+        self.kv.extend(seqs, new, self.stream())
+        self.current = list(zip(seqs, new))
+
+    def rand(self, rows, n, dtype, scale=1.0):
+        x = torch.from_numpy((self.rng.standard_normal((rows, n, self.hd)) * scale).astype(np.float32)).to(tdt(dtype))
+        return x, x.double().numpy()
+
+    def append(self, k, v, dtype, layer=0, strides=None):
+        """k, v: (device tensor, fp64 values)."""
+        kd, vd = k[0].cuda(), v[0].cuda()
+        self.kv.append(layer, kd.data_ptr(), vd.data_ptr(), dtype, strides, self.stream())
+        row = 0
+        for s, n in self.current:
+            if n:
+                self.ref[layer][s].append(k[1][row:row + n], v[1][row:row + n])
+            row += n
+
+    def step(self, seqs, new, dtype="f32", layer=0, scale=1.0):
+        self.extend(seqs, new)
+        rows = sum(new)
+        if rows:
+            self.append(self.rand(rows, self.nkv, dtype, scale), self.rand(rows, self.nkv, dtype, scale), dtype, layer)
+
+    def check_tokens(self, seqs, layer=0):
+        for s in seqs:
+            k, v = self.kv.read_tokens(layer, s)
+            rk, rv = self.ref[layer][s].values()
+            np.testing.assert_array_equal(k, rk.astype(np.float32), err_msg=f"seq {s} K")
+            np.testing.assert_array_equal(v, rv.astype(np.float32), err_msg=f"seq {s} V")
+
+    def attend(self, dtype, layer=0, window=0, sinks=0, held=None, scale=None, q_scale=1.0, layout="plain", lse=True, q=None):
+        rows = sum(n for _, n in self.current)
+        scale = 1 / math.sqrt(self.hd) if scale is None else scale
+        qt, q64 = self.rand(rows, self.heads, dtype, q_scale) if q is None else q
+        H, hd = self.heads, self.hd
+        if layout == "plain":
+            qd, out, st = qt.cuda(), torch.full((rows, H, hd), 7.0, dtype=qt.dtype, device="cuda"), None
+        elif layout == "fused":       # q inside a wider projection output; out padded
+            wide = torch.zeros((rows, H + 3, hd), dtype=qt.dtype, device="cuda")
+            wide[:, 1:1 + H] = qt.cuda()
+            qd = wide[:, 1:1 + H]
+            hold = torch.full((rows, H, hd + 8), 7.0, dtype=qt.dtype, device="cuda")
+            out = hold[:, :, :hd]
+            st = (qd.stride(0), qd.stride(1), out.stride(0), out.stride(1))
+        else:                         # heads outermost
+            qd = qt.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+            out = torch.full((H, rows, hd), 7.0, dtype=qt.dtype, device="cuda").transpose(0, 1)
+            st = (qd.stride(0), qd.stride(1), out.stride(0), out.stride(1))
+        ls = torch.full((rows, H), 7.0, device="cuda") if lse else None
+        self.kv.attend(layer, qd.data_ptr(), out.data_ptr(), dtype, st, scale=scale, window=window, sinks=sinks,
+                       lse_ptr=ls.data_ptr() if lse else 0, stream=self.stream())
+        got = out.double().cpu().numpy()
+        if layout == "fused":
+            assert bool((hold[:, :, hd:] == 7.0).all()), "written past the head dimension"
+        row = 0
+        for s, n in self.current:
+            k, v = self.ref[layer][s].values()
+            want, wl, terms, mag = R.attention(q64[row:row + n], k, v, len(k) - n, scale, window, sinks, None if held is None else held.get(s))
+            g = got[row:row + n]
+            nan = np.isnan(want)
+            assert np.array_equal(np.isnan(g), nan), f"seq {s}: NaN in other places ({np.isnan(g).sum()} and {nan.sum()})"
+            tol = R.bound(want, terms, mag, len(k), hd, dtype)
+            err = np.abs(g - want)
+            bad = ~nan & ~(err <= tol)
+            assert not bad.any(), f"seq {s}: {bad.sum()} of {bad.size} off, worst {np.nanmax(np.where(bad, err / tol, 0)):.2f} bounds at {np.argwhere(bad)[0]}"
+            if lse:
+                gl = ls.double().cpu().numpy()[row:row + n]
+                fin = np.isfinite(wl)
+                assert np.array_equal(np.isneginf(gl), np.isneginf(wl)), f"seq {s}: lse of empty rows"
+                assert np.array_equal(np.isnan(gl), np.isnan(wl)), f"seq {s}: lse NaN"
+                assert (np.abs(gl - wl)[fin] <= R.lse_bound(wl, mag, len(k), hd)[fin]).all(), f"seq {s}: lse"
+            row += n
+        return out
+
+
+# ------------------------------------------------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("hd,page,kv", [(64, 16, 2), (128, 64, 3), (40, 32, 1), (80, 128, 2), (256, 16, 1), (200, 64, 2)])
+def test_append_is_exact(dtype, hd, page, kv):
+    e = Env(hd=hd, page=page, kv=kv, heads=kv, seed=hd + page)
+    # one token, a few, across pages, ragged batches with an empty member, ends at every place of a group of four
+    for seqs, new in (([0], [1]), ([0, 1], [2, 5]), ([2, 0, 1], [3 * page + 1, 0, page - 5]), ([0, 2], [page, 1]), ([1, 0], [2, 3])):
+        e.step(seqs, new, dtype, scale=float(e.rng.choice([0.01, 1.0, 300.0])))
+        e.check_tokens([0, 1, 2])
+
+
+def test_append_special_values():
+    e = Env(hd=64, page=16, kv=1, heads=1)
+    rng = e.rng
+
+    def put(x, y):
+        e.extend([0], [len(x)])
+        t = [torch.from_numpy(a.astype(np.float32).reshape(-1, 1, 64)) for a in (x, y)]
+        e.append((t[0], t[0].double().numpy()), (t[1], t[1].double().numpy()), "f32")
+        e.check_tokens([0])
+
+    z = np.zeros((1, 64))
+    put(z, z)                                                # a block of zeros: exponent -120
+    put(z + 1e-30, z - 1e-38)                                # tiny: codes of the smallest exponents
+    put(z + 448.0, np.nextafter(np.float32(448.0), np.float32(1e9)) + z)  # on and just above the border
+    x = rng.standard_normal((2, 64))
+    x[0, 3], x[1, 7], x[1, 9] = np.inf, np.nan, -np.inf
+    put(x, -x)
+    big = rng.standard_normal((3, 64)) * 1e30
+    put(big, z.repeat(3, 0))
+    put(z + 3.3e38, z - 3.3e38)                              # the largest exponents
+    # ties to even, borders between binades and subnormals at a known exponent (0)
+    v = np.concatenate([[448.0], np.arange(1, 32) * 2.0 ** -10, 1 + np.arange(32) / 16])
+    put(v.reshape(1, 64), -v.reshape(1, 64))
+
+
+def test_append_strided_rows_and_second_call():
+    e = Env(hd=80, page=32, kv=3, heads=3)
+    e.step([0], [37], "bf16")
+    e.extend([0, 1], [9, 40])
+    wide = torch.from_numpy(e.rng.standard_normal((49, 8, 80)).astype(np.float32)).bfloat16()
+    k, v = wide[:, 1:4], wide[:, 5:8]
+    dev = wide.cuda()
+    kd, vd = dev[:, 1:4], dev[:, 5:8]
+    for _ in range(3):   # a repeated call stores the same
+        e.kv.append(0, kd.data_ptr(), vd.data_ptr(), "bf16", (kd.stride(0), kd.stride(1), vd.stride(0), vd.stride(1)), e.stream())
+    row = 0
+    for s, n in e.current:
+        e.ref[0][s].append(k[row:row + n].double().numpy(), v[row:row + n].double().numpy())
+        row += n
+    e.check_tokens([0, 1])
+
+
+# ------------------------------------------------------------------------------------------------------------- attend
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,kv,hd,page", [(4, 4, 64, 16), (8, 2, 128, 64), (7, 1, 80, 32), (6, 3, 40, 128), (4, 1, 256, 16), (2, 2, 192, 64), (40, 1, 128, 32)])
+def test_attend_single_tokens(dtype, heads, kv, hd, page):
+    e = Env(heads=heads, kv=kv, hd=hd, page=page, pages=96, seed=heads * hd)
+    e.step([0, 1, 2], [1, page + 3, 300], dtype)
+    e.step([0, 1, 2], [1, 1, 1], dtype)
+    e.attend(dtype)
+    e.step([2, 0], [1, 1], dtype)
+    e.attend(dtype, layout="fused", q_scale=4.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,kv,hd,page,new,before", [
+    (4, 4, 64, 16, 33, 0), (4, 2, 128, 64, 200, 0), (6, 2, 128, 32, 97, 131), (7, 1, 80, 16, 64, 1), (2, 2, 40, 128, 150, 50),
+    (2, 1, 256, 16, 70, 5), (2, 1, 192, 32, 129, 0)])
+def test_attend_prompts(dtype, heads, kv, hd, page, new, before):
+    e = Env(heads=heads, kv=kv, hd=hd, page=page, pages=64, seed=new)
+    if before:
+        e.step([0, 1], [before, before // 2], dtype)
+    e.step([1, 0, 2], [new // 3, new, 0], dtype)
+    e.attend(dtype)
+    e.attend(dtype, layout="heads", q_scale=3.0, lse=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 0), (32, 4), (33, 33), (100, 16), (7, 200), (1000, 3), (64, 70)])
+@pytest.mark.parametrize("new", [1, 3, 90])
+def test_window_and_first_tokens(dtype, window, sinks, new):
+    e = Env(heads=4, kv=2, hd=64, page=32, pages=64, seed=window)
+    e.step([0, 1], [290, 20], dtype)
+    e.step([0, 1, 2], [new, max(1, new // 2), new], dtype)
+    e.attend(dtype, window=window, sinks=sinks)
+
+
+def test_long_sequence_is_split_and_joined():
+    e = Env(heads=2, kv=1, hd=128, page=64, pages=160, seqs=2)
+    e.step([0, 1], [9000, 37], "bf16")
+    e.step([0, 1], [1, 1], "bf16")
+    a = e.attend("bf16")
+    e.attend("bf16", window=4096, sinks=4)
+    e.attend("f32", q_scale=8.0)
+    q = e.rand(2, 2, "bf16")
+    runs = [e.attend("bf16", q=q).clone() for _ in range(4)]
+    assert all(torch.equal(r, runs[0]) for r in runs), "not the same from run to run"
+    assert a.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_scales_of_blocks_far_apart(dtype):
+    # Value blocks of very different magnitude, the large ones hardly weighted: the unit of the sums has to follow.
+    for page in (16, 64):
+        e = Env(heads=2, kv=1, hd=64, page=page, pages=32, seed=page)
+        mags = [1.0, 2.0 ** 6, 2.0 ** -9, 2.0 ** 8, 1e-3, 0.0, 5.0, 2.0 ** -14]
+        rows = page * len(mags)
+        e.extend([0], [rows])
+        k = e.rng.standard_normal((rows, 1, 64))
+        k[:, 0, 0] = np.repeat([-40 if m > 10 else 5 for m in mags], page)   # the large blocks get weight e^-5 or so
+        v = e.rng.standard_normal((rows, 1, 64)) * np.repeat(mags, page)[:, None, None]
+        kt, vt = (torch.from_numpy(x.astype(np.float32)) for x in (k, v))
+        e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+        q = np.zeros((rows, 2, 64), np.float32)
+        q[:, :, 0] = 1.0
+        q[:, :, 1:] = e.rng.standard_normal((rows, 2, 63)) * 0.1
+        qt = torch.from_numpy(q).to(tdt(dtype))
+        e.attend(dtype, q=(qt, qt.double().numpy()))
+        e.extend([0], [0])
+        e.extend([0], [1])
+        e.append(e.rand(1, 1, "f32"), e.rand(1, 1, "f32"), "f32")
+        e.attend(dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_scores_with_large_spread(dtype):
+    # The running maximum rises by more than the lazy step many times, and early tokens end with weight zero.
+    e = Env(heads=2, kv=2, hd=64, page=16, pages=32)
+    rows = 180
+    e.extend([0], [rows])
+    k = e.rng.standard_normal((rows, 2, 64)) * 0.1
+    k[:, :, 0] = np.linspace(-60, 60, rows)[:, None]
+    kt = torch.from_numpy(k.astype(np.float32))
+    e.append((kt, kt.double().numpy()), e.rand(rows, 2, "f32"), "f32")
+    q = e.rng.standard_normal((rows, 2, 64)).astype(np.float32)
+    q[:, 0, 0], q[:, 1, 0] = 30.0, -30.0
+    qt = torch.from_numpy(q).to(tdt(dtype))
+    e.attend(dtype, q=(qt, qt.double().numpy()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_nan_and_infinity_stay_with_the_rows_that_see_them(dtype, page):
+    e = Env(heads=2, kv=1, hd=64, page=page, pages=32)
+    e.step([0], [70], "f32")
+    e.extend([0], [60])
+    k, v = (e.rng.standard_normal((60, 1, 64)).astype(np.float32) for _ in range(2))
+    v[20, 0, 5] = np.nan          # seen by rows 20 .. 20 + window - 1 only
+    v[41, 0, 9] = -np.inf         # stored as the block's lowest value
+    k[30, 0, 0] = np.nan          # rows that see it are NaN
+    kt, vt = torch.from_numpy(k), torch.from_numpy(v)
+    e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    e.check_tokens([0])
+    e.attend(dtype, window=9)
+    e.attend(dtype)
+    e.attend(dtype, window=3, sinks=2)
+    q = e.rand(60, 2, dtype)
+    q[0][7, 1, 0] = float("inf")  # a row of its own: NaN or not by its own formula, the others untouched
+    q[0][9, 0, 3] = float("nan")
+    e.attend(dtype, window=20, q=(q[0], q[0].double().numpy()))
+
+
+def test_dropped_pages_and_rows_that_see_nothing():
+    e = Env(heads=4, kv=2, hd=64, page=16, pages=64)
+    e.step([0, 1], [200, 200], "bf16")
+    # a cache restored without its past: rows see only what is held
+    pages = e.kv.pages(0)
+    keep = 8
+    gone = np.array([-1] * keep + pages[keep:].tolist(), np.int32)
+    e.kv.free(0)
+    e.kv.adopt(0, gone, 200, e.stream())
+    held = {0: np.arange(1000) >= keep * 16}
+    e.ref[0][0].codes[:keep * 16] = np.nan
+    e.step([0, 1], [3, 2], "bf16")
+    e.attend("bf16", held=held)
+    e.attend("f32", held=held, window=130, sinks=20)
+    # nothing held but the new tokens' page, and they are hidden: window 1 with every page dropped
+    assert e.kv.evict(1, 16, 0, e.stream()) == 11
+    held[1] = np.arange(1000) >= 11 * 16
+    e.step([1], [1], "bf16")
+    e.attend("bf16", held=held)
+    # rows with no visible token at all
+    e.kv.free(2)
+    p = e.kv.pages(1)
+    e.kv.free(1)
+    e.kv.adopt(2, [-1] * len(p), len(p) * 16, e.stream())
+    e.extend([2, 0], [2, 1])
+    e.ref[0][2] = R.RefSeq(2, 64, 16)
+    e.ref[0][2].codes = np.full((len(p) * 16, 2, 2, 64), np.nan)
+    e.ref[0][2].exps = np.zeros((len(p), 2, 2), dtype=np.int64)
+    e.append(e.rand(3, 2, "bf16"), e.rand(3, 2, "bf16"), "bf16")
+    e.attend("bf16", held={2: np.arange(1000) >= len(p) * 16, 0: held[0]})
+
+
+def test_empty_rows_are_zero():
+    # adopt with every page dropped, then a step whose queries lie in the past: no visible token, output 0, lse -inf
+    from delta_prefetched_ffn_amd import KVCache
+    e = Env(heads=4, kv=2, hd=64, page=16, pages=8)
+    e.step([0], [16], "bf16")
+    e.kv.evict(0, 1, 0, e.stream())
+    e.kv.extend([0], [0], e.stream())
+    q = torch.zeros((1, 4, 64), device="cuda")
+    e.kv.attend(0, q.data_ptr(), q.data_ptr(), "f32", scale=1.0, stream=e.stream())   # no rows: nothing to do
+    # window 4 hides every held token of a page-wide gap: rows at the start of a page see only themselves
+    e.step([0], [1], "bf16")
+    e.attend("bf16", held={0: np.arange(17) >= 16})
+    torch.cuda.synchronize()
+    assert KVCache is not None
+
+
+# --------------------------------------------------------------------------------------------------------- pages, order
+
+@pytest.mark.parametrize("mode", ["share", "copy"])
+def test_forks_keep_their_own_tokens(mode):
+    e = Env(heads=4, kv=2, hd=80, page=32, pages=40, layers=3)
+
+    def both(seqs, new):
+        e.extend(seqs, new)
+        for layer in range(3):
+            e.append(e.rand(sum(new), 2, "f32"), e.rand(sum(new), 2, "f32"), "f32", layer)
+
+    both([0], [75])
+    for dst, n in ((1, 75), (2, 70), (3, 64)):
+        e.kv.fork(0, dst, n, mode, e.stream())
+        for layer in range(3):
+            r = e.ref[layer][dst]
+            r.codes, r.exps = e.ref[layer][0].codes[:n].copy(), e.ref[layer][0].exps[:-(-n // 32)].copy()
+    both([1, 0, 2, 3], [4, 1, 3, 2])
+    both([2, 3], [40, 1])
+    for layer in range(3):
+        e.check_tokens([0, 1, 2, 3], layer)
+        e.attend("f32", layer)
+    # shorter again, then packed: contents stay
+    e.kv.trim(0, 40)
+    e.kv.free(3)
+    for layer in range(3):
+        e.ref[layer][0].codes = e.ref[layer][0].codes[:40]
+        e.ref[layer][0].exps = e.ref[layer][0].exps[:2]
+    e.kv.compact(e.stream())
+    used = sorted({int(p) for s in (0, 1, 2) for p in e.kv.pages(s)})
+    assert used == list(range(len(used)))
+    for layer in range(3):
+        e.check_tokens([0, 1, 2], layer)
+    both([0, 2], [30, 1])
+    for layer in range(3):
+        e.check_tokens([0, 1, 2], layer)
+        e.attend("bf16", layer)
+
+
+def test_compact_moves_many_pages():
+    e = Env(heads=1, kv=1, hd=64, page=16, pages=1200, seqs=3, max_pages=600)
+    for _ in range(20):   # pages of three sequences interleaved
+        e.step([0, 1, 2], [480, 160, 7], "f16")
+    e.kv.free(0)
+    assert e.kv.compact(e.stream()) > 0
+    e.ref[0][0] = R.RefSeq(1, 64, 16)
+    e.check_tokens([1, 2])
+    e.step([2, 1], [1, 1], "f16")
+    e.attend("f16")
+
+
+def test_offsets_past_32_bits():
+    # A pool above 4 GiB whose last pages are the ones in use.
+    e = Env(heads=2, kv=2, hd=128, page=64, pages=140000)
+    assert e.codes.numel() > (1 << 32)
+    e.kv.adopt(0, list(range(139999, 139990, -1)), 0, e.stream())
+    e.step([0], [530], "bf16")
+    e.check_tokens([0])
+    e.step([0], [1], "bf16")
+    e.attend("bf16")
+    e.kv.fork(0, 1, 500, "copy", e.stream())
+    assert e.kv.compact(e.stream()) == 9
+    e.check_tokens([0])
+
+
+def test_another_stream_and_graph_replays():
+    e = Env(heads=4, kv=2, hd=128, page=32, pages=64)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        e.step([0, 1], [500, 90], "bf16")
+        e.step([0, 1], [1, 1], "bf16")
+        e.attend("bf16")
+        e.check_tokens([0, 1])
+        q = torch.randn((2, 4, 128), device="cuda").bfloat16()
+        k, v = (torch.randn((2, 2, 128), device="cuda").bfloat16() for _ in range(2))
+        out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st = torch.cuda.current_stream().cuda_stream
+        e.kv.append(0, k.data_ptr(), v.data_ptr(), "bf16", None, st)
+        e.kv.attend(0, q.data_ptr(), out.data_ptr(), "bf16", scale=0.1, stream=st)
+    for i in range(4):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, device="cuda"))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        e.kv.append(0, k.data_ptr(), v.data_ptr(), "bf16", None, e.stream())
+        e.kv.attend(0, q.data_ptr(), out.data_ptr(), "bf16", scale=0.1, stream=e.stream())
+        torch.cuda.synchronize()
+        assert torch.equal(got, out), i
+
+
+def test_refusals_with_a_device():
+    from delta_prefetched_ffn_amd import KVCache, NPError
+    from delta_prefetched_ffn_amd import binding as B
+    e = Env()
+    e.extend([0], [3])
+    host = np.zeros(4096, np.float32)
+    at = (host.ctypes.data + 15) // 16 * 16
+    x = torch.zeros(4096, device="cuda")
+    for call in (lambda: e.kv.append(0, at, x.data_ptr(), "f32"), lambda: e.kv.append(0, x.data_ptr(), at, "f32"),
+                 lambda: e.kv.attend(0, at, x.data_ptr(), "f32", scale=1.0), lambda: e.kv.attend(0, x.data_ptr(), at, "f32", scale=1.0),
+                 lambda: e.kv.attend(0, x.data_ptr(), x.data_ptr(), "f32", scale=1.0, lse_ptr=at),
+                 lambda: KVCache(n_layers=1, n_heads=1, n_kv_heads=1, head_dim=64, page_tokens=16, n_pages=1, max_seqs=1, max_pages=1, codes=at, exps=x.data_ptr()),
+                 lambda: KVCache(n_layers=1, n_heads=1, n_kv_heads=1, head_dim=64, page_tokens=16, n_pages=1, max_seqs=1, max_pages=1, codes=x.data_ptr(), exps=at),
+                 lambda: KVCache(n_layers=1, n_heads=1, n_kv_heads=1, head_dim=64, page_tokens=16, n_pages=1, max_seqs=1, max_pages=1),
+                 lambda: KVCache(n_layers=1, n_heads=1, n_kv_heads=1, head_dim=64, page_tokens=16, n_pages=1, max_seqs=1, max_pages=1, device=99, codes=x.data_ptr(), exps=x.data_ptr())):
+        with pytest.raises(NPError) as err:
+            call()
+        assert err.value.status == B.NP_EINVAL
+    e.append(e.rand(3, 2, "f32"), e.rand(3, 2, "f32"), "f32")   # still usable
+    e.check_tokens([0])
+    e.attend("f32")
