@@ -13,6 +13,8 @@
 // operand of the second product: two groups of 16 tokens fill its 32 k-slots, four per lane and
 // group, and the V tile's dword i of the lane's chunk holds exactly those four tokens of value
 // 4 r + i. So neither P nor V crosses lanes, and a lane's results are 16 consecutive values.
+#include <algorithm>
+
 #include "kv_device.hpp"
 
 namespace np {
@@ -57,20 +59,20 @@ struct Vec8<_Float16> {
 __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 __device__ inline f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// Eight e4m3 codes (two dwords) times 2^k (s = 2^k as a float) to eight 16-bit floats: exact in
+// Eight e4m3 codes (two dwords), each dword times its scale 2^k, to eight 16-bit floats: exact in
 // bf16, exact in fp16 while the product stays within its normal range.
 template <typename E>
-__device__ inline typename Vec8<E>::t widen(uint32_t a, uint32_t b, float s);
+__device__ inline typename Vec8<E>::t widen(uint32_t a, uint32_t b, float sa, float sb);
 template <>
-__device__ inline bf16x8 widen<__bf16>(uint32_t a, uint32_t b, float s) {
-    const bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false), y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
-    const bf16x2 z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false), w = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
+__device__ inline bf16x8 widen<__bf16>(uint32_t a, uint32_t b, float sa, float sb) {
+    const bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sa, false), y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sa, true);
+    const bf16x2 z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sb, false), w = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sb, true);
     return bf16x8{x[0], x[1], y[0], y[1], z[0], z[1], w[0], w[1]};
 }
 template <>
-__device__ inline f16x8 widen<_Float16>(uint32_t a, uint32_t b, float s) {
-    const f16x2 x = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, s, false), y = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, s, true);
-    const f16x2 z = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, s, false), w = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, s, true);
+__device__ inline f16x8 widen<_Float16>(uint32_t a, uint32_t b, float sa, float sb) {
+    const f16x2 x = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, sa, false), y = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, sa, true);
+    const f16x2 z = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, sb, false), w = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, sb, true);
     return f16x8{x[0], x[1], y[0], y[1], z[0], z[1], w[0], w[1]};
 }
 
@@ -90,8 +92,8 @@ __device__ inline void split(typename Vec8<E>::t* o, const float* x) {
         }
 }
 
-constexpr int kRows = 16;    // query rows of a tile
-constexpr int kPiece = 32;   // tokens of one step
+constexpr int kRows = kRowTile;      // query rows of a tile
+constexpr int kPiece = kPieceTokens;  // tokens of one step
 // P's values reach 2^kLazy before the running maximum is raised, so most steps rescale nothing.
 constexpr float kLazy = 8.0f;
 // O is kept in units of 2^unit; a block's V codes are widened times 2^(ev - unit). Within
@@ -115,12 +117,53 @@ __device__ inline Pieces pieces_of(int pos_lo, int pos_hi, int window, int sinks
     return p;
 }
 
-constexpr int kWaves = 4;
+// Adds a part (maximum mp, sum lp, values v) to a row's join at the maximum mm >= mp. A part that
+// saw no token (mp = -inf, lp = 0) adds nothing, whatever mm is.
+__device__ inline void join(f32x4& x, float& ll, float mm, float mp, float lp, f32x4 v) {
+    if (mp == -__builtin_inff() && lp == 0.0f) return;
+    const float f = mp == mm ? 1.0f : __builtin_amdgcn_exp2f(mp - mm);
+    ll += f * lp;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] += f * v[j];
+}
 
-// Few rows: one workgroup per (row tile, split of the key axis, kv head). Its four waves take every
-// fourth piece of the split and are joined through LDS at the end; splits are joined by k_attn_join.
-template <typename T, int NS>
-__global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
+// Four values of a finished row (query token and head of the group: r), and its lse.
+template <typename T>
+__device__ inline void store_row(const AttnArgs& a, int row0, int group, int h, int r, int d, f32x4 x, float ll, float mm) {
+    const bool none = mm == -__builtin_inff() && ll == 0.0f;  // no visible token: 0
+    const int t = r / group, head = h * group + r - t * group;
+    T* const out = static_cast<T*>(a.out) + (int64_t)(row0 + t) * a.o_row + (int64_t)head * a.o_head + d;
+    const float inv = none ? 0.0f : 1.0f / ll;
+    T y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = (T)(x[j] * inv);
+    __builtin_memcpy(__builtin_assume_aligned(out, 4 * sizeof(T)), y, sizeof y);
+    if (a.lse && d == 0)
+        a.lse[(int64_t)(row0 + t) * a.kv.n_heads + head] =
+            none ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(ll)) * 0.69314718055994531f;
+}
+
+// Partial results pass between dies: stores and loads that bypass the die's own cache.
+__device__ inline void put2(float* p, float x, float y) {
+    const uint64_t w = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline f32x2 get2(const float* p) {
+    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return f32x2{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+
+// Few rows: one workgroup of W waves per (row tile, split of the key axis, kv head). Its waves take
+// every W-th piece of the split and are joined through LDS; the workgroup that finishes a row tile
+// last joins the splits, in their order (so the result does not depend on which one that is).
+//
+// Bound by the cache's bytes (4 * group products per byte). A wave asks for a piece's K and V (8 KiB
+// at head_dim 128) a step ahead; page numbers and exponents of its next 32 pieces are fetched by its
+// lanes in two loads, so a piece's address needs no memory round trip of its own. Measured, at 1, 4
+// and 56 pieces a wave (32 heads x 4 Ki tokens; 8 x 8 heads x 4 Ki; 24 x 8 heads x 4 .. 32 Ki): 4
+// waves 15.2, 18.7 and 196 us, 8 waves 13.5, 18.5 and 192 us, 16 waves 15.7, 20.3 and 210 us.
+template <typename T, int NS, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_rows(AttnArgs a) {
     typedef Kind<T> Kd;
     typedef typename Kd::Q Q;
     typedef typename Kd::P P;
@@ -128,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
     typedef typename Vec8<P>::t P8;
     const KvView& kv = a.kv;
     const int b = find_item(a.b, blockIdx.x), h = blockIdx.y;
-    const int item = (int)blockIdx.x - a.b.item0[b], rt = item / a.splits, sp = item - rt * a.splits;
+    const int splits = a.b.splits[b], item = (int)blockIdx.x - a.b.item0[b], rt = item / splits, sp = item - rt * splits;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int group = kv.n_heads / kv.n_kv, rows = a.b.fresh[b] * group, r0 = rt * kRows;
     const int row = r0 + col;  // (query token, head of the group)
@@ -137,24 +180,52 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
     const int before = a.b.before[b], pos = before + tq;
     const int pos_lo = before + r0 / group, pos_hi = before + min(r0 + kRows - 1, rows - 1) / group;
     const Pieces pc = pieces_of(pos_lo, pos_hi, a.window, a.sinks);
-    const int u0 = (int)((int64_t)pc.total * sp / a.splits), u1 = (int)((int64_t)pc.total * (sp + 1) / a.splits);
-
-    Q8 q[NS][2][Kd::kQ];
-#pragma unroll
-    for (int c = 0; c < NS; ++c)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const int d = c * 64 + quad * 16 + f * 8;
-            float x[8] = {};
-            if (real && d < kv.hd)
-                load_row<8>(x, static_cast<const T*>(a.q) + (int64_t)(a.b.row0[b] + tq) * a.q_row + (int64_t)head * a.q_head + d);
-            split<Q, Kd::kQ>(q[c][f], x);
-        }
+    const int share = pc.total / splits, more = pc.total - share * splits;
+    const int u0 = sp * share + min(sp, more), u1 = u0 + share + (sp < more ? 1 : 0);
 
     const uint8_t* const codes = kv.codes + a.layer * kv.layer_bytes;
     const int8_t* const exps = kv.exps + (int64_t)a.layer * kv.n_pages * kv.n_kv * 2;
     const int side_bytes = (1 << kv.page_shift) * kv.slabs * kTileDims;
     const int seq = a.b.seq[b];
+
+    // The wave's pieces are u0 + wave + n * W, n < count. Lane i: page and exponents of group i % 2 of
+    // piece (n & ~31) + i / 2.
+    const int count = u1 - u0 > wave ? (u1 - u0 - wave + W - 1) / W : 0;
+    const auto token_of = [&](int n) { return pc[u0 + wave + n * W] * kPiece; };
+    int ahead_page = -1, ahead_exps = 0;
+    const auto fetch_pages = [&](int n0) {
+        const int n = n0 + (lane >> 1), t = n < count ? token_of(n) + 16 * (lane & 1) : pos_hi + 1;
+        ahead_page = t <= pos_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
+    };
+    const auto fetch_exps = [&] {
+        ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(ahead_page, 0) * kv.n_kv + h) * 2);
+    };
+    // The q tile goes through LDS, one operand (c, f) per wave: all waves share it, and 16 waves at
+    // 128 registers have none left for it. Its trip runs beside the first page numbers'.
+    extern __shared__ float s_mem[];
+    Q8* const s_q = reinterpret_cast<Q8*>(s_mem);  // [NS][2][kQ][64 lanes]
+    fetch_pages(0);
+    for (int cf = wave; cf < 2 * NS; cf += W) {
+        const int d = (cf >> 1) * 64 + quad * 16 + (cf & 1) * 8;
+        const T* const qrow = static_cast<const T*>(a.q) + (int64_t)(a.b.row0[b] + tq) * a.q_row + (int64_t)head * a.q_head + d;
+        u32x4 raw[sizeof(T) / 2];
+#pragma unroll
+        for (int w = 0; w < (int)sizeof(T) / 2; ++w) {
+            raw[w] = u32x4{0, 0, 0, 0};
+            if (real && d < kv.hd) raw[w] = reinterpret_cast<const u32x4*>(qrow)[w];
+        }
+        if constexpr (sizeof(T) == 2) {
+            s_q[cf * 64 + lane] = __builtin_bit_cast(Q8, raw[0]);
+        } else {
+            float x[8];
+            __builtin_memcpy(x, raw, sizeof x);
+            Q8 t[Kd::kQ];
+            split<Q, Kd::kQ>(t, x);
+#pragma unroll
+            for (int n = 0; n < Kd::kQ; ++n) s_q[(cf * Kd::kQ + n) * 64 + lane] = t[n];
+        }
+    }
+    __syncthreads();
 
     f32x4 o[NS][4];
 #pragma unroll
@@ -166,53 +237,86 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
     int unit = 0, top = 0;  // o is in units of 2^unit
     bool begun = false;
 
-    for (int u = u0 + wave; u < u1; u += kWaves) {
-        const int tok = pc[u] * kPiece;
-        u32x4 k[2][NS], v[2][NS];
-        float kf[2];
-        int ev[2];
+    // K of the next piece is asked for once this one's products have read K, V once they have read V:
+    // a wave always has loads in flight and holds one piece only. The last piece's "next" loads read
+    // one line of the pool's start, so that their number is the same in every turn (the wait for K or
+    // V counts the loads behind it).
+    u32x4 k[2][NS], v[2][NS];
+    const uint8_t* at[2];  // of the piece whose K was asked for last
+    int lane16 = lane * 16;
+    const auto locate = [&](int n) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            // A group that is not held (or lies past the last position) reads page 0: its tokens are
+            // hidden below like any other hidden token.
+            const int page = max(0, __builtin_amdgcn_readlane(ahead_page, (n & 31) * 2 + g)), t = token_of(n) + 16 * g;
+            at[g] = codes + page * kv.page_bytes + (int64_t)h * 2 * side_bytes +
+                    (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes);
+        }
+    };
+    const auto load_k = [&] {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int c = 0; c < NS; ++c) k[g][c] = *reinterpret_cast<const u32x4*>(at[g] + c * kTileBytes + lane16);
+    };
+    const auto load_v = [&] {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int c = 0; c < NS; ++c) v[g][c] = *reinterpret_cast<const u32x4*>(at[g] + side_bytes + c * kTileBytes + lane16);
+    };
+    fetch_exps();
+    locate(0);
+    if (!count) lane16 = 0;
+    load_k();
+    load_v();
+    for (int n = 0; n < count; ++n) {
+        const int tok = token_of(n);
         bool held[2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int t = tok + 16 * g;
-            const int page = t <= pos_hi ? __builtin_amdgcn_readfirstlane(page_of(kv, seq, t >> kv.page_shift)) : -1;
-            held[g] = page >= 0;
-            kf[g] = 0.0f;
-            ev[g] = unit;
-            if (held[g]) {
-                const int8_t* const e = exps + ((int64_t)page * kv.n_kv + h) * 2;
-                kf[g] = a.scale2 * pow2i(max(-126, (int)e[0]));
-                ev[g] = max(-126, (int)e[1]);
-                const uint8_t* const p = codes + page * kv.page_bytes + (int64_t)h * 2 * side_bytes +
-                                         (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes) + lane * 16;
-#pragma unroll
-                for (int c = 0; c < NS; ++c) {
-                    k[g][c] = *reinterpret_cast<const u32x4*>(p + c * kTileBytes);
-                    v[g][c] = *reinterpret_cast<const u32x4*>(p + side_bytes + c * kTileBytes);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < NS; ++c) k[g][c] = v[g][c] = u32x4{0, 0, 0, 0};
-            }
-        }
-        if (!held[0] && !held[1]) continue;
+        for (int g = 0; g < 2; ++g) held[g] = __builtin_amdgcn_readlane(ahead_page, (n & 31) * 2 + g) >= 0;
 
-        float s[8];  // tokens tok + 16 (k / 4) + 4 quad + k % 4
+        f32x4 acc[2];  // raw scores of tokens tok + 16 g + 4 quad + j
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            f32x4 acc = {0, 0, 0, 0};
+            acc[g] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < NS; ++c)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const Q8 kk = widen<Q>(k[g][c][2 * f], k[g][c][2 * f + 1], 1.0f);
+                    const Q8 kk = widen<Q>(k[g][c][2 * f], k[g][c][2 * f + 1], 1.0f, 1.0f);
 #pragma unroll
-                    for (int n = 0; n < Kd::kQ; ++n) acc = mfma(kk, q[c][f][n], acc);
+                    for (int t = 0; t < Kd::kQ; ++t) acc[g] = mfma(kk, s_q[((c * 2 + f) * Kd::kQ + t) * 64 + lane], acc[g]);
                 }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[4 * g + j] = acc[j] * kf[g];
         }
+        __builtin_amdgcn_sched_barrier(0);
+        float kf[2];
+        int ev[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int e = __builtin_amdgcn_readlane(ahead_exps, (n & 31) * 2 + g);
+            kf[g] = a.scale2 * pow2i(max(-126, (int)(int8_t)e));
+            ev[g] = max(-126, (int)(int8_t)(e >> 8));
+        }
+        if (n + 1 < count) {
+            if ((n & 31) == 31) {
+                fetch_pages(n + 1);
+                fetch_exps();
+                asm volatile("" : "+v"(ahead_exps));  // waited for here, in this branch
+            }
+            locate(n + 1);
+        } else {
+            at[0] = at[1] = codes;
+            lane16 = 0;
+        }
+        load_k();
 
+        float s[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[4 * g + j] = acc[g][j] * kf[g];
         // Visibility: a piece that every row of the tile sees whole needs no comparisons.
         const bool whole = held[0] && held[1] && tok + kPiece - 1 <= pos_lo &&
                            (!a.window || tok > pos_hi - a.window || tok + kPiece <= a.sinks);
@@ -252,11 +356,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
             l += p[k8];
         }
 
-        // Normally one pass; two where the groups' V scales lie too far apart for one unit.
-        const bool near = !held[0] || !held[1] || (ev[0] - ev[1] <= kNear + kFar && ev[1] - ev[0] <= kNear + kFar);
-        for (int pass = 0; pass < (near ? 1 : 2); ++pass) {
-            const int e0 = near ? held[0] ? ev[0] : ev[1] : ev[pass], e1 = near ? held[1] ? ev[1] : ev[0] : ev[pass];
-            const int lo_e = min(e0, e1), hi_e = max(e0, e1);
+        // O += V^T P^T. Both groups at once, or one at a time where their V scales lie too far apart for
+        // one unit (the other group's codes are then out of the product: they would overflow).
+        const auto fit_unit = [&](int ea, int eb) {
+            const int lo_e = min(ea, eb), hi_e = max(ea, eb);
             if (!begun) {
                 unit = top = min(hi_e, lo_e + kFar);
                 begun = true;
@@ -271,57 +374,74 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
                     for (int i = 0; i < 4; ++i) o[c][i] *= f;
                 unit = to;
             }
-            float pp[8];
+        };
+        const int e0 = held[0] ? ev[0] : ev[1], e1 = held[1] ? ev[1] : ev[0];
+        const bool near = e0 - e1 <= kNear + kFar && e1 - e0 <= kNear + kFar;
+        // NaN codes of tokens that a row does not see must not reach it: 0 * NaN is NaN. Tokens that no row
+        // of the tile sees (often bytes never written) are cleared here; the path below keeps real NaN
+        // values from the rows that do not see them.
+        bool clean = true;
+        if (!whole) {
+            uint32_t bad = 0;
 #pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) pp[k8] = near || (k8 >> 2) == pass ? p[k8] : 0.0f;
-            P8 pv[Kd::kP];
-            split<P, Kd::kP>(pv, pp);
-            // Of two passes each takes one group: the other's codes are out (they would overflow at this unit).
+            for (int g = 0; g < 2; ++g) {
+                uint32_t some = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = tok + 16 * g + 4 * quad + j;
+                    if (held[g] && t <= pos_hi && (!a.window || pos_lo - t < a.window || t < a.sinks)) some |= 0xffu << (8 * j);
+                }
+#pragma unroll
+                for (int c = 0; c < NS; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[g][c][i] &= some;
+                        bad |= nan_bytes(v[g][c][i]);
+                    }
+            }
+            clean = !__any(bad != 0);
+        }
+        if (clean && near) {
+            fit_unit(e0, e1);
             const float f0 = pow2i(max(-126, e0 - unit)), f1 = pow2i(max(-126, e1 - unit));
-            const uint32_t in0 = near || pass == 0 ? ~0u : 0u, in1 = near || pass == 1 ? ~0u : 0u;
+            P8 pv[Kd::kP];
+            split<P, Kd::kP>(pv, p);
 #pragma unroll
             for (int c = 0; c < NS; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t w0 = v[0][c][i] & in0, w1 = v[1][c][i] & in1;
-                    uint32_t bad = 0;
-                    if (!whole) {
-                        // NaN codes of tokens that a row does not see (values that were NaN, or bytes never
-                        // written) must not reach it: 0 * NaN is NaN. They are taken out of the product and
-                        // given back below to the rows that do see them.
-                        const uint32_t n0 = nan_bytes(w0) >> 7, n1 = nan_bytes(w1) >> 7;
-                        bad = n0 | n1;
-                        w0 &= ~(n0 * 255u);
-                        w1 &= ~(n1 * 255u);
-                        if (__any(bad)) {
-                            const P8 ones = widen<P>(n0 * 0x38u, n1 * 0x38u, 1.0f);  // 0x38 is 1.0
-                            float see[8];
+                    const P8 vv = widen<P>(v[0][c][i], v[1][c][i], f0, f1);
 #pragma unroll
-                            for (int k8 = 0; k8 < 8; ++k8) see[k8] = vis >> k8 & 1 ? 1.0f : 0.0f;
-                            P8 sv[1];
-                            split<P, 1>(sv, see);
-                            const f32x4 hit = mfma(ones, sv[0], f32x4{0, 0, 0, 0});
+                    for (int t = 0; t < Kd::kP; ++t) o[c][i] = mfma(vv, pv[t], o[c][i]);
+                }
+        } else {
+        // Row by row, each with the codes of the tokens it sees and, of two far scales, one at a time.
+        for (int turn = 0; turn < (near ? kRows : 2 * kRows); ++turn) {
+            const int r = turn & (kRows - 1), pass = turn / kRows;
+            const int ea = near ? e0 : pass ? e1 : e0, eb = near ? e1 : ea;
+            fit_unit(ea, eb);
+            const float f0 = pow2i(max(-126, ea - unit)), f1 = pow2i(max(-126, eb - unit));
+            const uint32_t vr = __shfl(vis, quad * 16 + r);
+            uint32_t in[2] = {0, 0};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (hit[j] > 0.0f) o[c][i][j] = __builtin_nanf("");
-                        }
-                    }
-                    // widen's dwords: four tokens of group 0, four of group 1
-                    P8 vv;
-                    if (f0 == f1) {
-                        vv = widen<P>(w0, w1, f0);
-                    } else {
-                        const P8 x0 = widen<P>(w0, w0, f0), x1 = widen<P>(w1, w1, f1);
+            for (int k8 = 0; k8 < 8; ++k8)
+                if ((vr >> k8 & 1) && (near || (k8 >> 2) == pass)) in[k8 >> 2] |= 0xffu << (8 * (k8 & 3));
+            P8 pv[Kd::kP];
+            split<P, Kd::kP>(pv, p);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            vv[j] = x0[j];
-                            vv[4 + j] = x1[j];
-                        }
-                    }
+            for (int c = 0; c < NS; ++c)
 #pragma unroll
-                    for (int n = 0; n < Kd::kP; ++n) o[c][i] = mfma(vv, pv[n], o[c][i]);
+                for (int i = 0; i < 4; ++i) {
+                    const P8 vv = widen<P>(v[0][c][i] & in[0], v[1][c][i] & in[1], f0, f1);
+                    f32x4 x = o[c][i];
+#pragma unroll
+                    for (int t = 0; t < Kd::kP; ++t) x = mfma(vv, pv[t], x);
+                    if (col == r) o[c][i] = x;
+                    __builtin_amdgcn_sched_barrier(0);  // this path must not cost registers
                 }
         }
+        }
+        load_v();
     }
 
     // Join the waves: rows' maximum, sum and O in true units.
@@ -329,116 +449,117 @@ __global__ __launch_bounds__(64 * kWaves) void k_attn_rows(AttnArgs a) {
     l += __shfl_xor(l, 32);
     seen = (__ballot(seen) >> col & 0x0001000100010001ull) != 0;
     if (seen && m == -__builtin_inff()) l = __builtin_nanf("");  // every visible score is -inf: 0 / 0
-    constexpr int D = NS * 64;
-    __shared__ float s_o[kWaves][kRows][D + 4], s_m[kWaves][kRows], s_l[kWaves][kRows];
+    constexpr int D = NS * 64, DS = D + 4;
+    __syncthreads();  // the q tile is done with
+    const int cap = a.row_cap;
+    float* const s_m = s_mem;  // [W][cap]
+    float* const s_l = s_m + W * cap;
+    float* const s_o = s_l + W * cap;  // [W][cap][DS]
+    const int tile_rows = min(kRows, rows - r0);
     const float back = pow2i(max(-126, min(127, unit)));
+    if (col < tile_rows) {
+        float* const dst = s_o + (wave * cap + col) * DS + quad * 16;
 #pragma unroll
-    for (int c = 0; c < NS; ++c)
+        for (int c = 0; c < NS; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s_o[wave][col][c * 64 + quad * 16 + 4 * j + i] = o[c][i][j] * back;
-    if (quad == 0) {
-        s_m[wave][col] = m;
-        s_l[wave][col] = l;
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4*>(dst + c * 64 + 4 * j) = f32x4{o[c][0][j], o[c][1][j], o[c][2][j], o[c][3][j]} * back;
+        if (quad == 0) {
+            s_m[wave * cap + col] = m;
+            s_l[wave * cap + col] = l;
+        }
     }
     __syncthreads();
-    const int D4 = kv.hd / 4;
-    for (int k = threadIdx.x; k < kRows * D4; k += 64 * kWaves) {
+    const int D4 = kv.hd / 4, n_out = tile_rows * D4;
+    const int64_t first = ((int64_t)(a.b.part0[b] + rt * splits) * kv.n_kv + h), step = kv.n_kv;
+    const int PS = cap * (D + 2);
+    for (int k = threadIdx.x; k < n_out; k += 64 * W) {
         const int r = k / D4, d = (k - r * D4) * 4;
-        if (r0 + r >= rows) break;
-        float mm = s_m[0][r], ll = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][r]);
+        float mm = s_m[r], ll = 0.0f;
+#pragma unroll 4
+        for (int w = 1; w < W; ++w) mm = fmaxf(mm, s_m[w * cap + r]);
         f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = s_m[w][r] == mm ? 1.0f : __builtin_amdgcn_exp2f(s_m[w][r] - mm);
-            if (s_l[w][r] == 0.0f && f == 1.0f && s_m[w][r] == -__builtin_inff()) continue;  // saw nothing
-            ll += f * s_l[w][r];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] += f * s_o[w][r][d + j];
-        }
-        const bool none = mm == -__builtin_inff() && ll == 0.0f;  // no visible token: 0
-        const int t = (r0 + r) / group, hd = h * group + (r0 + r) - t * group;
-        if (a.splits == 1) {
-            T* const out = static_cast<T*>(a.out) + (int64_t)(a.b.row0[b] + t) * a.o_row + (int64_t)hd * a.o_head + d;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) out[j] = (T)(none ? 0.0f : x[j] / ll);
-            if (a.lse && d == 0)
-                a.lse[(int64_t)(a.b.row0[b] + t) * kv.n_heads + hd] = none ? -__builtin_inff() : (mm + log2f(ll)) * 0.69314718055994531f;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) join(x, ll, mm, s_m[w * cap + r], s_l[w * cap + r], *reinterpret_cast<const f32x4*>(s_o + (w * cap + r) * DS + d));
+        if (splits == 1) {
+            store_row<T>(a, a.b.row0[b], group, h, r0 + r, d, x, ll, mm);
         } else {
-            float* const part = a.part + (((int64_t)blockIdx.x * kv.n_kv + h) * kRows + r) * (D + 2);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[2 + d + j] = x[j];
-            if (d == 0) {
-                part[0] = mm;
-                part[1] = ll;
-            }
+            // Past the caches of this die, to where the joining workgroup reads.
+            float* const part = a.part + (first + sp * step) * PS + r * (D + 2);
+            put2(part + 2 + d, x[0], x[1]);
+            put2(part + 4 + d, x[2], x[3]);
+            if (d == 0) put2(part, mm, ll);
         }
     }
-}
-
-// Joins the splits of a row tile, in order: one workgroup per (row tile, kv head).
-template <typename T>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    const KvView& kv = a.kv;
-    const int first = (int)blockIdx.x * a.splits;
-    const int b = find_item(a.b, first), h = blockIdx.y;
-    const int rt = (first - a.b.item0[b]) / a.splits;
-    const int group = kv.n_heads / kv.n_kv, rows = a.b.fresh[b] * group, r0 = rt * kRows, D = kv.slabs * 64, D4 = kv.hd / 4;
-    for (int k = threadIdx.x; k < kRows * D4; k += 256) {
+    if (splits == 1) return;
+    // Each wave's stores are done (acknowledged where every die sees them) before the count rises.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint32_t* const s_last = reinterpret_cast<uint32_t*>(s_mem);
+    if (threadIdx.x == 0) s_last[0] = atomicInc(a.arrived + first, (uint32_t)splits - 1);  // back to 0 with the last
+    __syncthreads();
+    if (s_last[0] != (uint32_t)splits - 1) return;
+    for (int k = threadIdx.x; k < n_out; k += 64 * W) {
         const int r = k / D4, d = (k - r * D4) * 4;
-        if (r0 + r >= rows) break;
-        const int64_t stride = (int64_t)kv.n_kv * kRows * (D + 2);
-        const float* const p = a.part + (((int64_t)first * kv.n_kv + h) * kRows + r) * (D + 2);
+        const float* const p = a.part + first * PS + r * (D + 2);
         float mm = -__builtin_inff(), ll = 0.0f;
-        for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, p[s * stride]);
         f32x4 x = {0, 0, 0, 0};
-        for (int s = 0; s < a.splits; ++s) {
-            const float ms = p[s * stride], ls = p[s * stride + 1];
-            if (ms == -__builtin_inff() && ls == 0.0f) continue;  // saw nothing
-            const float f = ms == mm ? 1.0f : __builtin_amdgcn_exp2f(ms - mm);
-            ll += f * ls;
+        constexpr int U = 4;  // splits in flight
+        for (int s0 = 0; s0 < splits; s0 += U) {
+            f32x2 ml[U], xa[U], xb[U];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] += f * p[s * stride + 2 + d + j];
+            for (int i = 0; i < U; ++i) {
+                const float* const q = p + min(s0 + i, splits - 1) * step * PS;
+                ml[i] = get2(q);
+                xa[i] = get2(q + 2 + d);
+                xb[i] = get2(q + 4 + d);
+            }
+            float m1 = mm;
+#pragma unroll
+            for (int i = 0; i < U; ++i) m1 = fmaxf(m1, ml[i][0]);
+            if (m1 != mm) {
+                const float f = __builtin_amdgcn_exp2f(mm - m1);
+                x *= f;
+                ll *= f;
+                mm = m1;
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (s0 + i < splits) join(x, ll, mm, ml[i][0], ml[i][1], f32x4{xa[i][0], xa[i][1], xb[i][0], xb[i][1]});
         }
-        const bool none = mm == -__builtin_inff() && ll == 0.0f;
-        const int t = (r0 + r) / group, hd = h * group + (r0 + r) - t * group;
-        T* const out = static_cast<T*>(a.out) + (int64_t)(a.b.row0[b] + t) * a.o_row + (int64_t)hd * a.o_head + d;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out[j] = (T)(none ? 0.0f : x[j] / ll);
-        if (a.lse && d == 0)
-            a.lse[(int64_t)(a.b.row0[b] + t) * kv.n_heads + hd] = none ? -__builtin_inff() : (mm + log2f(ll)) * 0.69314718055994531f;
+        store_row<T>(a, a.b.row0[b], group, h, r0 + r, d, x, ll, mm);
     }
 }
 
-template <typename T>
+template <typename T, int NS>
 hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
+    constexpr int W = kAttnWaves;
     const dim3 grid(a.b.item0[a.b.n], a.kv.n_kv);
-    switch (a.kv.slabs) {
-        case 1: k_attn_rows<T, 1><<<grid, 64 * kWaves, 0, s>>>(a); break;
-        case 2: k_attn_rows<T, 2><<<grid, 64 * kWaves, 0, s>>>(a); break;
-        case 3: k_attn_rows<T, 3><<<grid, 64 * kWaves, 0, s>>>(a); break;
-        default: k_attn_rows<T, 4><<<grid, 64 * kWaves, 0, s>>>(a); break;
-    }
+    constexpr size_t kRowLds = (size_t)W * (2 + NS * 64 + 4) * sizeof(float);
+    const size_t lds = std::max(kRowLds * a.row_cap, sizeof(bf16x8) * 64 * 2 * NS * Kind<T>::kQ);
+    static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_rows<T, NS, W>),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kRowLds * kRows));
+    if (ready != hipSuccess) return ready;
+    k_attn_rows<T, NS, W><<<grid, 64 * W, lds, s>>>(a);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t attn_as(const AttnArgs& a, hipStream_t s) {
+    switch (a.kv.slabs) {
+        case 1: return rows_as<T, 1>(a, s);
+        case 2: return rows_as<T, 2>(a, s);
+        case 3: return rows_as<T, 3>(a, s);
+        default: return rows_as<T, 4>(a, s);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s) {
-    if (dtype == kF32) return rows_as<float>(a, s);
-    if (dtype == kBF16) return rows_as<__bf16>(a, s);
-    return rows_as<_Float16>(a, s);
-}
-
-hipError_t launch_attn_join(const AttnArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid(a.b.item0[a.b.n] / a.splits, a.kv.n_kv);
-    if (dtype == kF32) k_attn_join<float><<<grid, 256, 0, s>>>(a);
-    else if (dtype == kBF16) k_attn_join<__bf16><<<grid, 256, 0, s>>>(a);
-    else k_attn_join<_Float16><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
+    if (dtype == kF32) return attn_as<float>(a, s);
+    if (dtype == kBF16) return attn_as<__bf16>(a, s);
+    return attn_as<_Float16>(a, s);
 }
 
 }  // namespace np

@@ -32,16 +32,11 @@ __device__ inline int find_item(const KvBatch& b, int item) {
     return __builtin_amdgcn_readfirstlane(c);
 }
 
-// The page of table entry `index` of sequence `seq`; -1 where it was dropped. An entry outside the
-// pool (the host never writes one) raises kErrBadPage and counts as dropped.
+// The page of table entry `index` of sequence `seq`; -1 where it was dropped (a number outside the
+// pool, which the host never writes, counts as dropped too: no address is made of it).
 __device__ inline int page_of(const KvView& kv, int seq, int index) {
     const int p = kv.table[(int64_t)seq * kv.max_pages + index];
-    if (p < -1 || p >= kv.n_pages) {
-        atomicOr(kv.err, kErrBadPage);
-        __hip_atomic_store(kv.err_host, (uint32_t)kErrBadPage, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-        return -1;
-    }
-    return p;
+    return p < kv.n_pages ? p : -1;
 }
 
 // N consecutive values of a caller's row, as fp32 (N = 4 or 8; the address is aligned to

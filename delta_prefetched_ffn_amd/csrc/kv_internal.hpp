@@ -13,9 +13,6 @@ constexpr int kMaxPageTokens = 128;
 constexpr int kMaxBatch = 128;        // sequences of one np_kv_extend
 constexpr int kMaxSeqTokens = 1 << 28;
 
-// Device error bits of a cache.
-constexpr int kErrBadPage = 1;  // a page table entry of a token in use lies outside the pool
-
 // The code tile: 16 tokens x 64 values = 1024 bytes, laid out in the lane order of the 16x16x32
 // matrix instructions so that a wave reads a tile as 64 consecutive 16-byte chunks, each lane's
 // chunk being exactly its operand (np.h gives the byte order).
@@ -28,8 +25,6 @@ struct KvView {
     uint8_t* codes;        // [layers][pages][kv heads][2][page_tokens / 16][slabs][1024]
     int8_t* exps;          // [layers][pages][kv heads][2]
     const int32_t* table;  // [max_seqs][max_pages] page of each sequence position, -1: dropped
-    int32_t* err;          // device error bits
-    uint32_t* err_host;    // the same in pinned host memory (device address)
     int64_t page_bytes;    // codes of one page of one layer
     int64_t layer_bytes;   // codes of one layer
     int32_t n_pages, max_pages;
@@ -47,6 +42,10 @@ struct KvBatch {
     int32_t fresh[kMaxBatch];   // new tokens
     int32_t row0[kMaxBatch];
     int32_t item0[kMaxBatch + 1];
+    // Attention only: pieces of the key axis per row tile, and the sequence's first partial result
+    // (in units of one item of every kv head; sequences with one piece have none).
+    int32_t splits[kMaxBatch];
+    int32_t part0[kMaxBatch];
 };
 
 struct AppendArgs {
@@ -68,10 +67,20 @@ struct AttnArgs {
     int32_t window;      // 0: none
     int32_t sinks;
     int32_t layer;
-    int32_t splits;      // pieces of the key axis per row tile
-    float* part;         // [item][kv head][16][64 slabs + 2] partial results (splits > 1)
+    int32_t row_cap;     // rows of the largest tile in this launch (LDS is sized for it)
+    float* part;         // [partial][kv head][row_cap][64 slabs + 2] partial results
+    uint32_t* arrived;   // [partial][kv head] splits done (at the tile's first partial), 0 between launches
     KvBatch b;  // item = one (row tile, split) of one sequence
 };
+static_assert(sizeof(AttnArgs) <= 4096 && sizeof(AppendArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+// Attention over few rows: how many partial results (workgroups that share a row tile with others)
+// one launch may have, and how many rows these may have together; the waves of a workgroup.
+constexpr int kAttnWaves = 8;
+constexpr int kRowTile = 16;
+constexpr int kPieceTokens = 32;
+constexpr int kMaxPartials = 8192;
+constexpr int kMaxPartialRows = 32768;
 
 // Page table entries (seq, index0 + k) = page0 + k * step for k < count; step 0 repeats page0.
 constexpr int kTableRuns = 200;
@@ -101,6 +110,5 @@ hipError_t launch_kv_append(const AppendArgs& a, int dtype, hipStream_t s);
 hipError_t launch_kv_table(const TableArgs& a, hipStream_t s);
 hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s);
-hipError_t launch_attn_join(const AttnArgs& a, int dtype, hipStream_t s);
 
 }  // namespace np

@@ -19,11 +19,13 @@ using namespace np;
 
 namespace {
 
-// Attention over few rows splits the key axis until about this many workgroups are in flight.
-constexpr int kTargetWgs = 1024;
-constexpr int kRowTile = 16;
-constexpr int kPieceTokens = 32;
-constexpr int kMinPieces = 8;  // pieces of a split
+// Attention over few rows splits the key axis into workgroups for every compute unit: one each while
+// a wave then has at most kFewPieces pieces (each further workgroup costs the launch a join), two
+// each beyond (one's start and join hide behind the other's stream). Measured at 1, 4 and 56 pieces a
+// wave: 256 workgroups 13.5, 18.5 and 216 us, 512 workgroups 20.7, 23.0 and 192 us, 1024 workgroups
+// 20.7, 33.3 and 193 us.
+constexpr int kCus = 256;
+constexpr int kFewPieces = 16;
 
 struct Seq {
     std::vector<int32_t> pages;  // -1: dropped
@@ -44,9 +46,7 @@ struct np_kv {
     bool broken = false;            // a launch failed in the middle of a call
     int32_t* table = nullptr;
     float* part = nullptr;
-    int32_t* err = nullptr;
-    uint32_t* err_h = nullptr;
-    uint32_t* err_hd = nullptr;
+    uint32_t* arrived = nullptr;
 
     bool host_only() const { return desc.device == NP_KV_HOST; }
     int pt() const { return desc.page_tokens; }
@@ -97,8 +97,6 @@ struct np_kv {
         v.codes = static_cast<uint8_t*>(desc.codes);
         v.exps = desc.exps;
         v.table = table;
-        v.err = err;
-        v.err_host = err_hd;
         v.page_bytes = page_bytes;
         v.layer_bytes = layer_bytes;
         v.n_pages = desc.n_pages;
@@ -113,8 +111,7 @@ struct np_kv {
     ~np_kv() {
         if (table) (void)hipFree(table);
         if (part) (void)hipFree(part);
-        if (err) (void)hipFree(err);
-        if (err_h) (void)hipHostFree(err_h);
+        if (arrived) (void)hipFree(arrived);
     }
 };
 
@@ -201,8 +198,6 @@ np_status check_tail(const np_kv* kv, int32_t seq, int32_t n_tokens) {
 np_status check_kv(const np_kv* kv) {
     if (!kv) return fail(NP_EINVAL, "kv must not be NULL");
     if (kv->broken) return fail(NP_ESTATE, "an earlier call failed in the middle: call np_kv_reset");
-    const uint32_t bits = kv->err_h ? __atomic_load_n(kv->err_h, __ATOMIC_ACQUIRE) : 0u;
-    if (bits) return fail(NP_EDEVICE, "a kernel of the cache reported error bits 0x%x (np_kv_reset clears them)", bits);
     return NP_OK;
 }
 
@@ -294,19 +289,14 @@ np_status create(const np_kv_desc* desc, np_kv** out) {
         if ((st = check_io_ptr(D.codes, D.device, "codes", "cache")) != NP_OK) return st;
         if ((st = check_io_ptr(D.exps, D.device, "exps", "cache")) != NP_OK) return st;
         const size_t table_bytes = (size_t)D.max_seqs * D.max_pages * sizeof(int32_t);
-        const size_t part_bytes = (size_t)kTargetWgs * kRowTile * (kv->slabs * kTileDims + 2) * sizeof(float);
-        void* p = nullptr;
+        const size_t part_bytes = (size_t)kMaxPartialRows * (kv->slabs * kTileDims + 2) * sizeof(float);
         if (hipMalloc((void**)&kv->table, table_bytes) != hipSuccess || hipMalloc((void**)&kv->part, part_bytes) != hipSuccess ||
-            hipMalloc((void**)&kv->err, sizeof(int32_t)) != hipSuccess ||
-            hipHostMalloc(&p, sizeof(uint32_t), hipHostMallocDefault) != hipSuccess) {
+            hipMalloc((void**)&kv->arrived, kMaxPartials * sizeof(uint32_t)) != hipSuccess) {
             (void)hipGetLastError();
             return fail(NP_ENOMEM, "cannot allocate the page table (%zu bytes) and scratch (%zu bytes)", table_bytes, part_bytes);
         }
-        kv->err_h = static_cast<uint32_t*>(p);
-        *kv->err_h = 0;
-        NP_HIP(hipHostGetDevicePointer((void**)&kv->err_hd, kv->err_h, 0));
         NP_HIP(hipMemset(kv->table, 0xff, table_bytes));
-        NP_HIP(hipMemset(kv->err, 0, sizeof(int32_t)));
+        NP_HIP(hipMemset(kv->arrived, 0, kMaxPartials * sizeof(uint32_t)));
         NP_HIP(hipDeviceSynchronize());
     }
     *out = kv;
@@ -444,19 +434,46 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.sinks = sinks;
     a.layer = layer;
     a.part = kv->part;
-    const int group = D.n_heads / D.n_kv_heads;
-    int64_t tiles = 0, pieces = 1;
-    for (size_t i = 0; i < kv->b_seq.size(); ++i) {
-        const int64_t f = kv->b_fresh[i], len = kv->b_before[i] + f;
-        tiles += (f * group + kRowTile - 1) / kRowTile;
-        if (f) pieces = std::max(pieces, (window ? std::min(len, (int64_t)window + sinks + f) : len) / kPieceTokens + 1);
+    a.arrived = kv->arrived;
+    const int group = D.n_heads / D.n_kv_heads, n = (int)kv->b_seq.size();
+    if (rows * group > 1 << 28) return fail(NP_EINVAL, "%lld query rows in one call are too many", (long long)rows * group);
+    // Pieces of a sequence's last row tile (the most of its tiles), and of all tiles together.
+    const auto tiles = [&](int i) { return (kv->b_fresh[i] * group + kRowTile - 1) / kRowTile; };
+    const auto pieces = [&](int i) {
+        const int64_t len = (int64_t)kv->b_before[i] + kv->b_fresh[i];
+        const int64_t span = std::min<int64_t>(kv->b_fresh[i], (kRowTile - 1) / group + 1);  // positions of a row tile
+        return (window ? std::min(len, (int64_t)window + span + std::min<int64_t>(sinks, len) + kPieceTokens) : len) / kPieceTokens + 1;
+    };
+    int64_t all = 0;
+    a.row_cap = 1;
+    for (int i = 0; i < n; ++i) {
+        all += pieces(i) * tiles(i) * D.n_kv_heads;
+        a.row_cap = std::max(a.row_cap, std::min(kRowTile, kv->b_fresh[i] * group));
     }
-    if (tiles * 64 > 1 << 30) return fail(NP_EINVAL, "%lld query rows in one call are too many", (long long)rows * group);
-    a.splits = (int32_t)std::max<int64_t>(1, std::min(kTargetWgs / (tiles * D.n_kv_heads), pieces / kMinPieces));
-    fill_batch(kv, a.b, [&](int i) { return (kv->b_fresh[i] * group + kRowTile - 1) / kRowTile * a.splits; });
+    // Pieces of a workgroup: one per wave at least, else so many that the launch is not a few workgroups
+    // more than its turns hold (they would be a turn of their own).
+    const int64_t most = kCus * (all > (int64_t)kCus * kAttnWaves * kFewPieces ? 2 : 1);
+    const auto splits = [&](int i, int64_t per) { return (pieces(i) + per - 1) / per; };
+    int64_t per = std::max<int64_t>(kAttnWaves, all / most);
+    for (;; per += per / 16 + 1) {
+        int64_t wgs = 0, least = 0;
+        for (int i = 0; i < n; ++i) {
+            wgs += tiles(i) * splits(i, per) * D.n_kv_heads;
+            least += tiles(i) * D.n_kv_heads;
+        }
+        if (wgs <= std::max(most, least)) break;
+    }
+    int64_t partials = 0;
+    for (int i = 0; i < n; ++i) {
+        int64_t sp = std::max<int64_t>(1, splits(i, per));
+        if ((partials + tiles(i) * sp) * D.n_kv_heads > std::min(kMaxPartials, kMaxPartialRows / a.row_cap)) sp = 1;
+        a.b.splits[i] = (int32_t)sp;
+        a.b.part0[i] = (int32_t)partials;
+        if (sp > 1) partials += tiles(i) * sp;
+    }
+    fill_batch(kv, a.b, [&](int i) { return tiles(i) * a.b.splits[i]; });
     DeviceGuard g(D.device);
     NP_HIP(launch_attn(a, dtype, s));
-    if (a.splits > 1) NP_HIP(launch_attn_join(a, dtype, s));
     return NP_OK;
 }
 
@@ -681,13 +698,6 @@ np_status np_kv_destroy(np_kv* kv) {
 np_status np_kv_reset(np_kv* kv) {
     if (!kv) return fail(NP_EINVAL, "kv must not be NULL");
     return guarded([&] {
-        if (!kv->host_only() && (kv->broken || *kv->err_h)) {
-            DeviceGuard g(kv->desc.device);
-            NP_HIP(hipDeviceSynchronize());
-            NP_HIP(hipMemset(kv->err, 0, sizeof(int32_t)));
-            NP_HIP(hipDeviceSynchronize());
-            __atomic_store_n(kv->err_h, 0u, __ATOMIC_RELEASE);
-        }
         kv->broken = false;
         kv->clear();
         return NP_OK;

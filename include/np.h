@@ -456,8 +456,7 @@ np_status np_kv_create(const np_kv_desc* desc, np_kv** out);
 /* Synchronizes the device and frees what the cache allocated (not the pool). */
 np_status np_kv_destroy(np_kv* kv);
 
-/* Every sequence empty, every page free; clears device errors. Enqueues
- * nothing (it synchronizes only if there is an error to clear). */
+/* Every sequence empty, every page free. Enqueues nothing. */
 np_status np_kv_reset(np_kv* kv);
 
 /* Gives seqs[i] room for n_new[i] >= 0 more tokens (host arrays of n <= 128,
@@ -480,7 +479,7 @@ np_status np_kv_extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t*
  * Infinities are stored as +-448 * 2^e and NaN as NaN; neither enters e. A
  * second call for the same tokens overwrites them, but e does not go down
  * again for a page that holds earlier tokens.
- * Errors: NP_EINVAL, NP_ESTATE (no current tokens), NP_EDEVICE. */
+ * Errors: NP_EINVAL, NP_ESTATE (no current tokens). */
 np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t dtype, const int64_t* strides,
                        void* stream);
 
@@ -499,7 +498,7 @@ np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, i
  * exp(s_j) are rounded to fp16 for 16-bit dtypes and kept to 24 bits for
  * NP_F32. Results are the same from run to run.
  * Errors: NP_EINVAL (scale not positive and finite, a negative window), NP_ESTATE (no
- * current tokens), NP_EDEVICE. */
+ * current tokens). */
 np_status np_kv_attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,
                        const int64_t* strides, float scale, int32_t window, int32_t sinks, void* stream);
 
