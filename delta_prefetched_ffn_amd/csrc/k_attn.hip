@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     };
     // The q tile goes through LDS, one operand (c, f) per wave: all waves share it, and 16 waves at
     // 128 registers have none left for it. Its trip runs beside the first page numbers'.
-    extern __shared__ float s_mem[];
+    extern __shared__ __attribute__((aligned(128))) float s_mem[];
     Q8* const s_q = reinterpret_cast<Q8*>(s_mem);  // [NS][2][kQ][64 lanes]
     fetch_pages(0);
     for (int cf = wave; cf < 2 * NS; cf += W) {
@@ -531,6 +531,327 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     }
 }
 
+// Waves of a workgroup for many rows: 8, two to a SIMD at 256 registers, where q, O and the scores fit;
+// 4 at 512 registers for fp32 (three summands of q) and the longest heads.
+template <typename T, int NS>
+constexpr int kTileWaves = NS * (sizeof(T) == 4 ? 3 : 1) <= 3 ? 8 : 4;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+__device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+
+// Many rows: one workgroup of W waves per (32 W rows, kv head), 32 rows a wave, 64 tokens a step.
+//
+// Bound by the matrix units, with the exponentials next (per 64 tokens a wave has 32 products of
+// 32x32x16, 1024 clocks, and 32 exponentials a lane, 512). So what is not theirs is kept off the
+// waves: codes are widened to 16 bits once per workgroup, by the wave that moved them into LDS (every
+// wave reads them all, 1 KiB of consecutive operands at a time), with V's scale folded into that
+// conversion; the products are transposed as above, so P needs no trip through LDS; and the next
+// step's codes are asked for before this step's products. The workgroups of one kv head have numbers
+// that leave them on one die (its cache then holds the head's K and V), the longest rows first.
+//
+// Operand slots: S^T lane (half, row) holds tokens 8 (i / 4) + 4 half + i % 4, i < 16, of a 32-token
+// block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
+// V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho / 2) + 2 vt +
+// rho % 2: then a lane ends with eight consecutive values of its row.
+template <typename T, int NS, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_tile(AttnArgs a) {
+    typedef Kind<T> Kd;
+    typedef typename Kd::Q Q;
+    typedef typename Kd::P P;
+    typedef typename Vec8<Q>::t Q8;
+    typedef typename Vec8<P>::t P8;
+    constexpr int KS = NS * 4;               // 16-value steps of a head
+    constexpr int kSide = 64 * NS * 64;      // values of a step's K (or V)
+    constexpr int kUnits = 8 * NS / W;       // 1 KiB code tiles a wave moves per step
+    const KvView& kv = a.kv;
+    const int item_all = blockIdx.x / kv.n_kv, h = blockIdx.x - item_all * kv.n_kv;
+    const int b = find_item(a.b, item_all);
+    const int rt = a.b.item0[b + 1] - 1 - item_all;  // the last rows first
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    const int group = kv.n_heads / kv.n_kv, rows = a.b.fresh[b] * group, r0 = rt * 32 * W, w0 = r0 + 32 * wave;
+    const int row = w0 + col;
+    const bool real = row < rows;
+    const int tq = row / group, head = h * group + row - tq * group;
+    const int before = a.b.before[b], pos = before + tq;
+    const int wg_lo = before + r0 / group, wg_hi = before + min(r0 + 32 * W - 1, rows - 1) / group;
+    const int pos_lo = before + min(w0, rows - 1) / group, pos_hi = before + min(w0 + 31, rows - 1) / group;
+    const int seq = a.b.seq[b];
+    const uint8_t* const codes = kv.codes + a.layer * kv.layer_bytes;
+    const int8_t* const exps = kv.exps + (int64_t)a.layer * kv.n_pages * kv.n_kv * 2;
+    const int side_bytes = (1 << kv.page_shift) * kv.slabs * kTileDims;
+
+    // Steps of 64 tokens: the first tokens' steps, then those of the window.
+    const int lo = a.window ? max(0, wg_lo - a.window + 1) : 0;
+    const int n_sink = (min(a.sinks, lo) + 63) / 64, first = max(n_sink, lo / 64), steps = n_sink + wg_hi / 64 + 1 - first;
+    const auto token_of = [&](int n) { return (n < n_sink ? n : first + n - n_sink) * 64; };
+
+    // Lane i: page and exponents of group i % 4 of step (n & ~15) + i / 4.
+    int ahead_page = -1, ahead_exps = 0;
+    const auto fetch = [&](int n0) {
+        const int n = n0 + (lane >> 2), t = n < steps ? token_of(n) + 16 * (lane & 3) : wg_hi + 1;
+        ahead_page = t <= wg_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
+        ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(ahead_page, 0) * kv.n_kv + h) * 2);
+        asm volatile("" : "+v"(ahead_exps));  // waited for here
+    };
+    fetch(0);
+
+    Q8 q[KS][Kd::kQ];
+    {
+        const T* const qrow = static_cast<const T*>(a.q) + (int64_t)(a.b.row0[b] + tq) * a.q_row + (int64_t)head * a.q_head;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int d = k * 16 + half * 8;
+            float x[8] = {};
+            if (real && d < kv.hd) load_row<8>(x, qrow + d);
+            split<Q, Kd::kQ>(q[k], x);
+        }
+    }
+
+    extern __shared__ __attribute__((aligned(128))) float s_mem[];
+    Q* const s_k = reinterpret_cast<Q*>(s_mem);                // [2][2 blocks][KS][2 halves][32 tokens][8]
+    P* const s_v = reinterpret_cast<P*>(s_mem) + 2 * kSide;    // [2][4 groups][2 NS][2 halves][32 rho][8]
+    // Per step buffer: the groups' K factors and V units, a bit per token of held groups, whether a V
+    // code is NaN, and then, per value, the tokens where it is.
+    __shared__ float s_kf[2][4];
+    __shared__ int s_unit[2][4];
+    __shared__ uint64_t s_held[2];
+    __shared__ int s_has_nan[2];
+    __shared__ unsigned long long s_nan[2][NS * 64];
+
+    // What this wave moves in a step: tiles wave + j W of [side][group][slab].
+    u32x4 part[kUnits];
+    const auto ask = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int tile = wave + j * W, side = tile / (4 * NS), g = tile / NS & 3, c = tile % NS;
+            const int page = max(0, __builtin_amdgcn_readlane(ahead_page, (n & 15) * 4 + g)), t = token_of(n) + 16 * g;
+            const uint8_t* const p = codes + page * kv.page_bytes + (int64_t)(2 * h + side) * side_bytes +
+                                     ((int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * kv.slabs + c) * kTileBytes;
+            part[j] = reinterpret_cast<const u32x4*>(p)[lane];
+        }
+    };
+    int v_unit = 0, v_top = 0;
+    bool begun = false;
+    const auto put = [&](int n, int buf) {
+        // The V units of the step's groups, in order (every wave works out the same).
+        int ev[4], un[4];
+        uint64_t held = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int from = (n & 15) * 4 + g, e = __builtin_amdgcn_readlane(ahead_exps, from);
+            ev[g] = max(-126, (int)(int8_t)(e >> 8));
+            if (__builtin_amdgcn_readlane(ahead_page, from) >= 0) {
+                held |= 0xffffull << (16 * g);
+                v_top = begun ? max(v_top, ev[g]) : ev[g];
+                if (!begun || ev[g] > v_unit + kNear || ev[g] < v_unit - kFar) v_unit = max(ev[g], v_top - kDrop);
+                begun = true;
+            }
+            un[g] = v_unit;
+            if (threadIdx.x == 0) {
+                // Never 0: a hidden score is -inf, and stays it times this.
+                s_kf[buf][g] = fmaxf(a.scale2 * pow2i(max(-126, (int)(int8_t)e)), 1.2e-38f);
+                s_unit[buf][g] = v_unit;
+            }
+        }
+        if (threadIdx.x == 0) s_held[buf] = held;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int tile = wave + j * W, side = tile / (4 * NS), g = tile / NS & 3, c = tile % NS;
+            if (side == 0) {
+                Q8* const d = reinterpret_cast<Q8*>(s_k + buf * kSide) + ((g >> 1) * KS + c * 4 + (lane >> 4)) * 64 + (g & 1) * 16 + (lane & 15);
+                d[0] = widen<Q>(part[j][0], part[j][1], 1.0f, 1.0f);
+                d[32] = widen<Q>(part[j][2], part[j][3], 1.0f, 1.0f);
+                continue;
+            }
+            const int e = g < 2 ? (g ? ev[1] : ev[0]) : g == 2 ? ev[2] : ev[3], u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+            const int quad = lane >> 4, t = token_of(n) + 16 * g + 4 * quad, r = lane & 15;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bad |= nan_bytes(part[j][i]);
+            if (__any(bad != 0)) {
+                // NaN codes must not reach rows that do not see their token (0 * NaN is NaN): they leave the
+                // product, and a note of them gives them back to the rows that do. Tokens that nobody sees
+                // (dropped, or past the last position: often bytes never written) leave no note.
+                const bool live = (held >> (16 * g) & 1) != 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t nb = nan_bytes(part[j][i]);
+                    uint64_t at = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if ((nb >> (8 * k + 7) & 1) && live && t + k <= wg_hi) at |= 1ull << (16 * g + 4 * quad + k);
+                    if (at) {
+                        atomicOr(&s_nan[buf][64 * c + 4 * r + i], (unsigned long long)at);
+                        s_has_nan[buf] = 1;
+                    }
+                    part[j][i] &= ~((nb >> 7) * 255u);
+                }
+            }
+            const float f = pow2i(max(-126, min(127, e - u)));
+            // value 4 r + i: tile vt = i / 2, rho = 2 r + i % 2; half quad % 2, slots 4 (quad / 2) ..
+            u32x2* const d = reinterpret_cast<u32x2*>(s_v + buf * kSide) + ((g * NS + c) * 2 * 64 + (quad & 1) * 32 + 2 * r) * 2 + (quad >> 1);
+            const u32x4 xw = __builtin_bit_cast(u32x4, widen<P>(part[j][0], part[j][1], f, f));
+            const u32x4 yw = __builtin_bit_cast(u32x4, widen<P>(part[j][2], part[j][3], f, f));
+            d[0] = u32x2{xw[0], xw[1]};
+            d[2] = u32x2{xw[2], xw[3]};
+            d[128] = u32x2{yw[0], yw[1]};
+            d[130] = u32x2{yw[2], yw[3]};
+        }
+    };
+
+    f32x16 o[2 * NS];
+#pragma unroll
+    for (int i = 0; i < 2 * NS; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;  // l: this lane's tokens only
+    bool seen = false;
+    int unit = 0;
+
+    for (int i = threadIdx.x; i < 2 * NS * 64; i += 64 * W) s_nan[0][i] = 0;
+    if (threadIdx.x < 2) s_has_nan[threadIdx.x] = 0;
+    ask(0);
+    __syncthreads();
+    put(0, 0);
+    for (int n = 0; n < steps; ++n) {
+        const int buf = n & 1, tok = token_of(n);
+        __syncthreads();
+        const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[buf]) != 0;
+        if (n + 1 < steps) {
+            if (((n + 1) & 15) == 0) fetch(n + 1);
+            ask(n + 1);
+        }
+        const bool any = tok <= pos_hi && (!a.window || tok + 63 > pos_lo - a.window || tok < a.sinks) && w0 < rows;
+        if (any) {
+            f32x16 s[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+            const Q8* const kt = reinterpret_cast<const Q8*>(s_k + buf * kSide) + lane;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const Q8 kk = kt[(t * KS + k) * 64];
+#pragma unroll
+                    for (int x = 0; x < Kd::kQ; ++x) s[t] = mfma(kk, q[k][x], s[t]);
+                }
+            float kf[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) kf[g] = s_kf[buf][g];
+            const uint64_t held = s_held[buf];
+            const bool whole = held == ~0ull && tok + 63 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + 64 <= a.sinks);
+            uint64_t vis = ~0ull;  // of the row, a bit per token
+            if (!whole) {
+                const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+                vis = below(pos - tok + 1) & held;
+                if (a.window) vis &= ~below(pos - a.window + 1 - tok) | below(a.sinks - tok);
+                const uint64_t mine = vis >> (4 * half);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int bit = 8 * (i >> 2) + (i & 3);
+                    const int keep = (int)((uint32_t)(mine >> (bit & 32)) << (31 - (bit & 31))) >> 31;
+                    s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & keep) | (0xff800000u & ~keep));
+                }
+            }
+            seen |= vis != 0;
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float x = s[g >> 1][8 * (g & 1)];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) x = fmaxf(x, s[g >> 1][8 * (g & 1) + j]);
+                mx = fmaxf(mx, x * kf[g]);
+            }
+            if (__any(mx > m + kLazy)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                const float m1 = fmaxf(m, mx);
+                const float f = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+                m = m1;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
+            }
+            const float m0 = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float p[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g >> 1][8 * (g & 1) + j], kf[g], -m0));
+                    l += p[j];
+                }
+                P8 pv[Kd::kP];
+                split<P, Kd::kP>(pv, p);
+                const int un = __builtin_amdgcn_readfirstlane(s_unit[buf][g]);
+                if (un != unit) {
+                    const float f = pow2i(max(-126, min(127, unit - un)));
+#pragma unroll
+                    for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
+                    unit = un;
+                }
+                const P8* const vt = reinterpret_cast<const P8*>(s_v + buf * kSide) + g * NS * 2 * 64 + lane;
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) {
+                    const P8 vv = vt[i * 64];
+#pragma unroll
+                    for (int x = 0; x < Kd::kP; ++x) o[i] = mfma(vv, pv[x], o[i]);
+                }
+            }
+            if (has_nan) {
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int rho = 8 * (j >> 2) + 4 * half + (j & 3);
+                        if (s_nan[buf][64 * (i >> 1) + 4 * (rho >> 1) + 2 * (i & 1) + (rho & 1)] & vis) o[i][j] = __builtin_nanf("");
+                    }
+            }
+        }
+        if (n + 1 < steps) put(n + 1, buf ^ 1);
+        if (has_nan) {  // cleared for the step after the next, which writes it behind the next barrier
+            __syncthreads();
+            for (int i = threadIdx.x; i < NS * 64; i += 64 * W) s_nan[buf][i] = 0;
+            if (threadIdx.x == 0) s_has_nan[buf] = 0;
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    seen = (__ballot(seen) >> col & 0x0000000100000001ull) != 0;
+    if (!real) return;
+    // Every visible score -inf: 0 / 0. No visible token: 0.
+    const float inv = !seen ? 0.0f : m == -__builtin_inff() ? __builtin_nanf("") : 1.0f / l;
+    const float back = pow2i(max(-126, min(127, unit)));
+    T* const out = static_cast<T*>(a.out) + (int64_t)(a.b.row0[b] + tq) * a.o_row + (int64_t)head * a.o_head;
+#pragma unroll
+    for (int c = 0; c < NS; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 64 * c + 16 * i + 8 * half;
+            if (d >= kv.hd) continue;
+            T y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = (T)(seen ? o[2 * c + (e >> 1 & 1)][4 * i + 2 * (e >> 2) + (e & 1)] * back * inv : 0.0f);
+            __builtin_memcpy(__builtin_assume_aligned(out + d, 16), y, sizeof y);
+        }
+    if (a.lse && half == 0)
+        a.lse[(int64_t)(a.b.row0[b] + tq) * kv.n_heads + head] =
+            !seen ? -__builtin_inff() : m == -__builtin_inff() ? __builtin_nanf("") : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+}
+
+template <typename T, int NS>
+hipError_t tile_as(const AttnArgs& a, hipStream_t s) {
+    constexpr int W = kTileWaves<T, NS>;
+    constexpr int kLds = 4 * 64 * NS * 64 * 2;  // two steps of K and V, 16 bits a value
+    static const hipError_t ready =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tile<T, NS, W>), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (ready != hipSuccess) return ready;
+    k_attn_tile<T, NS, W><<<(unsigned)a.b.item0[a.b.n] * a.kv.n_kv, 64 * W, kLds, s>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T, int NS>
 hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
     constexpr int W = kAttnWaves;
@@ -547,14 +868,24 @@ hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t attn_as(const AttnArgs& a, hipStream_t s) {
     switch (a.kv.slabs) {
-        case 1: return rows_as<T, 1>(a, s);
-        case 2: return rows_as<T, 2>(a, s);
-        case 3: return rows_as<T, 3>(a, s);
-        default: return rows_as<T, 4>(a, s);
+        case 1: return a.part ? rows_as<T, 1>(a, s) : tile_as<T, 1>(a, s);
+        case 2: return a.part ? rows_as<T, 2>(a, s) : tile_as<T, 2>(a, s);
+        case 3: return a.part ? rows_as<T, 3>(a, s) : tile_as<T, 3>(a, s);
+        default: return a.part ? rows_as<T, 4>(a, s) : tile_as<T, 4>(a, s);
     }
 }
 
 }  // namespace
+
+int attn_tile_rows(int dtype, int slabs) {
+    const bool f32 = dtype == kF32;
+    switch (slabs) {
+        case 1: return 32 * (f32 ? kTileWaves<float, 1> : kTileWaves<__bf16, 1>);
+        case 2: return 32 * (f32 ? kTileWaves<float, 2> : kTileWaves<__bf16, 2>);
+        case 3: return 32 * (f32 ? kTileWaves<float, 3> : kTileWaves<__bf16, 3>);
+        default: return 32 * (f32 ? kTileWaves<float, 4> : kTileWaves<__bf16, 4>);
+    }
+}
 
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s) {
     if (dtype == kF32) return attn_as<float>(a, s);

@@ -27,6 +27,9 @@ namespace {
 constexpr int kCus = 256;
 constexpr int kFewPieces = 16;
 
+// Rows (query tokens x heads of a group) of a sequence from which its attention runs in large tiles.
+constexpr int kManyRows = 128;
+
 struct Seq {
     std::vector<int32_t> pages;  // -1: dropped
     int32_t tokens = 0;
@@ -437,8 +440,18 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.arrived = kv->arrived;
     const int group = D.n_heads / D.n_kv_heads, n = (int)kv->b_seq.size();
     if (rows * group > 1 << 28) return fail(NP_EINVAL, "%lld query rows in one call are too many", (long long)rows * group);
+    DeviceGuard g(D.device);
+    // Sequences of many rows (prompts) go to the matrix units in large tiles, the others below.
+    const auto many = [&](int i) { return (int64_t)kv->b_fresh[i] * group >= kManyRows; };
+    const int tile_rows = attn_tile_rows(dtype, kv->slabs);
+    fill_batch(kv, a.b, [&](int i) { return many(i) ? (kv->b_fresh[i] * group + tile_rows - 1) / tile_rows : 0; });
+    if (a.b.item0[n] > 0) {
+        a.part = nullptr;
+        NP_HIP(launch_attn(a, dtype, s));
+        a.part = kv->part;
+    }
     // Pieces of a sequence's last row tile (the most of its tiles), and of all tiles together.
-    const auto tiles = [&](int i) { return (kv->b_fresh[i] * group + kRowTile - 1) / kRowTile; };
+    const auto tiles = [&](int i) { return many(i) ? 0 : (kv->b_fresh[i] * group + kRowTile - 1) / kRowTile; };
     const auto pieces = [&](int i) {
         const int64_t len = (int64_t)kv->b_before[i] + kv->b_fresh[i];
         const int64_t span = std::min<int64_t>(kv->b_fresh[i], (kRowTile - 1) / group + 1);  // positions of a row tile
@@ -448,8 +461,9 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.row_cap = 1;
     for (int i = 0; i < n; ++i) {
         all += pieces(i) * tiles(i) * D.n_kv_heads;
-        a.row_cap = std::max(a.row_cap, std::min(kRowTile, kv->b_fresh[i] * group));
+        if (tiles(i)) a.row_cap = std::max(a.row_cap, std::min(kRowTile, kv->b_fresh[i] * group));
     }
+    if (!all) return NP_OK;
     // Pieces of a workgroup: one per wave at least, else so many that the launch is not a few workgroups
     // more than its turns hold (they would be a turn of their own).
     const int64_t most = kCus * (all > (int64_t)kCus * kAttnWaves * kFewPieces ? 2 : 1);
@@ -472,7 +486,6 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
         if (sp > 1) partials += tiles(i) * sp;
     }
     fill_batch(kv, a.b, [&](int i) { return tiles(i) * a.b.splits[i]; });
-    DeviceGuard g(D.device);
     NP_HIP(launch_attn(a, dtype, s));
     return NP_OK;
 }
