@@ -586,12 +586,18 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     const int n_sink = (min(a.sinks, lo) + 63) / 64, first = max(n_sink, lo / 64), steps = n_sink + wg_hi / 64 + 1 - first;
     const auto token_of = [&](int n) { return (n < n_sink ? n : first + n - n_sink) * 64; };
 
-    // Lane i: page and exponents of group i % 4 of step (n & ~15) + i / 4.
-    int ahead_page = -1, ahead_exps = 0;
-    const auto fetch = [&](int n0) {
+    // Lane i: group i % 4 of step (n & ~15) + i / 4: its K codes' address (page 0 where it is not held or
+    // past the last position), exponents, and whether it is held.
+    uint64_t ahead_at = 0;
+    int ahead_exps = 0;
+    bool ahead_held = false;
+    const auto fetch = [&](int n0) __attribute__((always_inline)) {
         const int n = n0 + (lane >> 2), t = n < steps ? token_of(n) + 16 * (lane & 3) : wg_hi + 1;
-        ahead_page = t <= wg_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
-        ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(ahead_page, 0) * kv.n_kv + h) * 2);
+        const int page = t <= wg_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
+        ahead_held = page >= 0;
+        ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(page, 0) * kv.n_kv + h) * 2);
+        ahead_at = reinterpret_cast<uint64_t>(codes + max(page, 0) * kv.page_bytes + (int64_t)2 * h * side_bytes +
+                                              (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes));
         asm volatile("" : "+v"(ahead_exps));  // waited for here
     };
     fetch(0);
@@ -621,40 +627,44 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 
     // What this wave moves in a step: tiles wave + j W of [side][group][slab].
     u32x4 part[kUnits];
-    const auto ask = [&](int n) {
+    const auto ask = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
-            const int tile = wave + j * W, side = tile / (4 * NS), g = tile / NS & 3, c = tile % NS;
-            const int page = max(0, __builtin_amdgcn_readlane(ahead_page, (n & 15) * 4 + g)), t = token_of(n) + 16 * g;
-            const uint8_t* const p = codes + page * kv.page_bytes + (int64_t)(2 * h + side) * side_bytes +
-                                     ((int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * kv.slabs + c) * kTileBytes;
-            part[j] = reinterpret_cast<const u32x4*>(p)[lane];
+            const int tile = wave + j * W, side = tile / (4 * NS), from = (n & 15) * 4 + (tile / NS & 3), c = tile % NS;
+            const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(ahead_at >> 32), from) << 32 |
+                                (uint32_t)__builtin_amdgcn_readlane((int)ahead_at, from);
+            typedef const __attribute__((address_space(1))) u32x4 chunk;
+            part[j] = reinterpret_cast<chunk*>(at + side * side_bytes + c * kTileBytes)[lane];
         }
     };
     int v_unit = 0, v_top = 0;
     bool begun = false;
-    const auto put = [&](int n, int buf) {
-        // The V units of the step's groups, in order (every wave works out the same).
-        int ev[4], un[4];
-        uint64_t held = 0;
+    const auto put = [&](int n, int buf) __attribute__((always_inline)) {
+        // The V units of the step's groups, in order (every wave works out the same). Mostly all four are
+        // held and near the unit.
+        const int from = (n & 15) * 4, my_ev = max(-126, (int)(int8_t)(ahead_exps >> 8));
+        const uint32_t holds = (uint32_t)(__ballot(ahead_held) >> from) & 15;
+        const bool fits = my_ev <= v_unit + kNear && my_ev >= v_unit - kFar;
+        int un[4] = {v_unit, v_unit, v_unit, v_unit};
+        if (!begun || ((uint32_t)(__ballot(ahead_held && !fits) >> from) & 15)) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int from = (n & 15) * 4 + g, e = __builtin_amdgcn_readlane(ahead_exps, from);
-            ev[g] = max(-126, (int)(int8_t)(e >> 8));
-            if (__builtin_amdgcn_readlane(ahead_page, from) >= 0) {
-                held |= 0xffffull << (16 * g);
-                v_top = begun ? max(v_top, ev[g]) : ev[g];
-                if (!begun || ev[g] > v_unit + kNear || ev[g] < v_unit - kFar) v_unit = max(ev[g], v_top - kDrop);
-                begun = true;
-            }
-            un[g] = v_unit;
-            if (threadIdx.x == 0) {
-                // Never 0: a hidden score is -inf, and stays it times this.
-                s_kf[buf][g] = fmaxf(a.scale2 * pow2i(max(-126, (int)(int8_t)e)), 1.2e-38f);
-                s_unit[buf][g] = v_unit;
+            for (int g = 0; g < 4; ++g) {
+                const int e = __builtin_amdgcn_readlane(my_ev, from + g);
+                if (holds >> g & 1) {
+                    v_top = begun ? max(v_top, e) : e;
+                    if (!begun || e > v_unit + kNear || e < v_unit - kFar) v_unit = max(e, v_top - kDrop);
+                    begun = true;
+                }
+                un[g] = v_unit;
             }
         }
-        if (threadIdx.x == 0) s_held[buf] = held;
+        if (wave == 0 && lane >> 2 == (n & 15)) {
+            // K's factor is never 0: a hidden score is -inf, and stays it times this.
+            const int g = lane & 3;
+            s_kf[buf][g] = fmaxf(a.scale2 * pow2i(max(-126, (int)(int8_t)ahead_exps)), 1.2e-38f);
+            s_unit[buf][g] = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+            if (g == 0) s_held[buf] = (holds & 1 ? 0xffffull : 0) | (holds & 2 ? 0xffffull << 16 : 0) | (holds & 4 ? 0xffffull << 32 : 0) | (holds & 8 ? 0xffffull << 48 : 0);
+        }
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
             const int tile = wave + j * W, side = tile / (4 * NS), g = tile / NS & 3, c = tile % NS;
@@ -664,7 +674,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                 d[32] = widen<Q>(part[j][2], part[j][3], 1.0f, 1.0f);
                 continue;
             }
-            const int e = g < 2 ? (g ? ev[1] : ev[0]) : g == 2 ? ev[2] : ev[3], u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+            const int e = __builtin_amdgcn_readlane(my_ev, from + g), u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
             const int quad = lane >> 4, t = token_of(n) + 16 * g + 4 * quad, r = lane & 15;
             uint32_t bad = 0;
 #pragma unroll
@@ -673,7 +683,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                 // NaN codes must not reach rows that do not see their token (0 * NaN is NaN): they leave the
                 // product, and a note of them gives them back to the rows that do. Tokens that nobody sees
                 // (dropped, or past the last position: often bytes never written) leave no note.
-                const bool live = (held >> (16 * g) & 1) != 0;
+                const bool live = (holds >> g & 1) != 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t nb = nan_bytes(part[j][i]);
@@ -714,21 +724,28 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     ask(0);
     __syncthreads();
     put(0, 0);
+    if (steps > 1) ask(1);
     for (int n = 0; n < steps; ++n) {
         const int buf = n & 1, tok = token_of(n);
         __syncthreads();
         const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[buf]) != 0;
-        if (n + 1 < steps) {
-            if (((n + 1) & 15) == 0) fetch(n + 1);
-            ask(n + 1);
-        }
+        // Of the two waves of a SIMD one widens before its first products and one behind them: while one
+        // keeps the matrix unit, the other has the vector unit.
+        const auto move = [&]() __attribute__((always_inline)) {
+            if (n + 1 >= steps) return;
+            put(n + 1, buf ^ 1);
+            if (n + 2 >= steps) return;
+            if (((n + 2) & 15) == 0) fetch(n + 2);
+            ask(n + 2);
+        };
+        if (W == 4 || wave < W / 2) move();
         const bool any = tok <= pos_hi && (!a.window || tok + 63 > pos_lo - a.window || tok < a.sinks) && w0 < rows;
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
         if (any) {
-            f32x16 s[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
             const Q8* const kt = reinterpret_cast<const Q8*>(s_k + buf * kSide) + lane;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -738,6 +755,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 #pragma unroll
                     for (int x = 0; x < Kd::kQ; ++x) s[t] = mfma(kk, q[k][x], s[t]);
                 }
+        }
+        if (W != 4 && wave >= W / 2) move();
+        if (any) {
             float kf[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) kf[g] = s_kf[buf][g];
@@ -810,7 +830,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                     }
             }
         }
-        if (n + 1 < steps) put(n + 1, buf ^ 1);
         if (has_nan) {  // cleared for the step after the next, which writes it behind the next barrier
             __syncthreads();
             for (int i = threadIdx.x; i < NS * 64; i += 64 * W) s_nan[buf][i] = 0;
