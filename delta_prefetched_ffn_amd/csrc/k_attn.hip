@@ -554,6 +554,21 @@ __device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amd
 // block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
 // V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho / 2) + 2 vt +
 // rho % 2: then a lane ends with eight consecutive values of its row.
+// x, but made where it stands: what rare paths compute from the lane is not kept in registers across
+// the loop for them.
+__device__ inline int here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// x, computed before what follows in the program: the compiler moves arithmetic across barriers.
+template <typename V>
+__device__ inline V settled(V x) {
+    u32x4 w = __builtin_bit_cast(u32x4, x);
+    asm volatile("" : "+v"(w));
+    return __builtin_bit_cast(V, w);
+}
+
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_tile(AttnArgs a) {
     typedef Kind<T> Kd;
@@ -563,6 +578,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     typedef typename Vec8<P>::t P8;
     constexpr int KS = NS * 4;               // 16-value steps of a head
     constexpr int kSide = 64 * NS * 64;      // values of a step's K (or V)
+    constexpr bool kShift = W == 8;          // two waves to a SIMD, in opposite phases
     constexpr int kUnits = 8 * NS / W;       // 1 KiB code tiles a wave moves per step
     const KvView& kv = a.kv;
     const int item_all = blockIdx.x / kv.n_kv, h = blockIdx.x - item_all * kv.n_kv;
@@ -577,6 +593,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     const int wg_lo = before + r0 / group, wg_hi = before + min(r0 + 32 * W - 1, rows - 1) / group;
     const int pos_lo = before + min(w0, rows - 1) / group, pos_hi = before + min(w0 + 31, rows - 1) / group;
     const int seq = a.b.seq[b];
+    const float scale2 = a.scale2;
     const uint8_t* const codes = kv.codes + a.layer * kv.layer_bytes;
     const int8_t* const exps = kv.exps + (int64_t)a.layer * kv.n_pages * kv.n_kv * 2;
     const int side_bytes = (1 << kv.page_shift) * kv.slabs * kTileDims;
@@ -592,7 +609,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     int ahead_exps = 0;
     bool ahead_held = false;
     const auto fetch = [&](int n0) __attribute__((always_inline)) {
-        const int n = n0 + (lane >> 2), t = n < steps ? token_of(n) + 16 * (lane & 3) : wg_hi + 1;
+        const int own = here(lane), n = n0 + (own >> 2), t = n < steps ? token_of(n) + 16 * (own & 3) : wg_hi + 1;
         const int page = t <= wg_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
         ahead_held = page >= 0;
         ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(page, 0) * kv.n_kv + h) * 2);
@@ -617,20 +634,32 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     extern __shared__ __attribute__((aligned(128))) float s_mem[];
     Q* const s_k = reinterpret_cast<Q*>(s_mem);                // [2][2 blocks][KS][2 halves][32 tokens][8]
     P* const s_v = reinterpret_cast<P*>(s_mem) + 2 * kSide;    // [2][4 groups][2 NS][2 halves][32 rho][8]
-    // Per step buffer: the groups' K factors and V units, a bit per token of held groups, whether a V
-    // code is NaN, and then, per value, the tokens where it is.
+    // Per step: the groups' K factors, a bit per token of held groups, the groups' V units; whether a V
+    // code is NaN and, per value, the tokens where it is.
     __shared__ float s_kf[2][4];
-    __shared__ int s_unit[2][4];
     __shared__ uint64_t s_held[2];
-    __shared__ int s_has_nan[2];
-    __shared__ unsigned long long s_nan[2][NS * 64];
+    __shared__ int s_unit[2][4];
+    __shared__ int s_has_nan[4];
+    __shared__ unsigned long long s_nan[4][NS * 64];
+    __shared__ uint32_t s_bad[32 * W][2 * NS];  // per row, a bit per value: it is NaN
 
-    // What this wave moves in a step: tiles wave + j W of [side][group][slab].
+    // What this wave moves in a step: kUnits of the code tiles [side][group][slab]. In opposite phases
+    // the first waves move K, the others V.
+    const bool second = kShift && wave >= W / 2;
+    const bool moves_k = !kShift || !second, moves_v = !kShift || second;
+    const auto tile_at = [&](int j, int& side, int& g, int& c) __attribute__((always_inline)) {
+        const int tile = kShift ? (second ? 4 * NS : 0) + (wave & 3) + 4 * j : wave + W * j;
+        side = tile / (4 * NS);
+        g = tile / NS & 3;
+        c = tile % NS;
+    };
     u32x4 part[kUnits];
     const auto ask = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
-            const int tile = wave + j * W, side = tile / (4 * NS), from = (n & 15) * 4 + (tile / NS & 3), c = tile % NS;
+            int side, g, c;
+            tile_at(j, side, g, c);
+            const int from = (n & 15) * 4 + g;
             const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(ahead_at >> 32), from) << 32 |
                                 (uint32_t)__builtin_amdgcn_readlane((int)ahead_at, from);
             typedef const __attribute__((address_space(1))) u32x4 chunk;
@@ -639,74 +668,87 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     };
     int v_unit = 0, v_top = 0;
     bool begun = false;
-    const auto put = [&](int n, int buf) __attribute__((always_inline)) {
-        // The V units of the step's groups, in order (every wave works out the same). Mostly all four are
-        // held and near the unit.
-        const int from = (n & 15) * 4, my_ev = max(-126, (int)(int8_t)(ahead_exps >> 8));
+    const auto put = [&](int n) __attribute__((always_inline)) {
+        const int buf = n & 1, from = (n & 15) * 4, my_ev = max(-126, (int)(int8_t)(ahead_exps >> 8));
         const uint32_t holds = (uint32_t)(__ballot(ahead_held) >> from) & 15;
-        const bool fits = my_ev <= v_unit + kNear && my_ev >= v_unit - kFar;
-        int un[4] = {v_unit, v_unit, v_unit, v_unit};
-        if (!begun || ((uint32_t)(__ballot(ahead_held && !fits) >> from) & 15)) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int e = __builtin_amdgcn_readlane(my_ev, from + g);
-                if (holds >> g & 1) {
-                    v_top = begun ? max(v_top, e) : e;
-                    if (!begun || e > v_unit + kNear || e < v_unit - kFar) v_unit = max(e, v_top - kDrop);
-                    begun = true;
-                }
-                un[g] = v_unit;
-            }
-        }
         if (wave == 0 && lane >> 2 == (n & 15)) {
             // K's factor is never 0: a hidden score is -inf, and stays it times this.
-            const int g = lane & 3;
-            s_kf[buf][g] = fmaxf(a.scale2 * pow2i(max(-126, (int)(int8_t)ahead_exps)), 1.2e-38f);
-            s_unit[buf][g] = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
-            if (g == 0) s_held[buf] = (holds & 1 ? 0xffffull : 0) | (holds & 2 ? 0xffffull << 16 : 0) | (holds & 4 ? 0xffffull << 32 : 0) | (holds & 8 ? 0xffffull << 48 : 0);
+            s_kf[buf][lane & 3] = fmaxf(scale2 * pow2i(max(-126, (int)(int8_t)ahead_exps)), 1.2e-38f);
+            if ((lane & 3) == 0) s_held[buf] = (holds & 1 ? 0xffffull : 0) | (holds & 2 ? 0xffffull << 16 : 0) | (holds & 4 ? 0xffffull << 32 : 0) | (holds & 8 ? 0xffffull << 48 : 0);
         }
+        if (moves_v) {
+            // The V units of the step's groups, in order (every wave works out the same). Mostly all are near
+            // the unit, and it stays.
+            const bool fits = my_ev <= v_unit + kNear && my_ev >= v_unit - kFar;
+            int un[4] = {v_unit, v_unit, v_unit, v_unit};
+            if (!begun || ((uint32_t)(__ballot(ahead_held && !fits) >> from) & 15)) {
 #pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-            const int tile = wave + j * W, side = tile / (4 * NS), g = tile / NS & 3, c = tile % NS;
-            if (side == 0) {
+                for (int g = 0; g < 4; ++g) {
+                    const int e = __builtin_amdgcn_readlane(my_ev, from + g);
+                    if (holds >> g & 1) {
+                        v_top = begun ? max(v_top, e) : e;
+                        if (!begun || e > v_unit + kNear || e < v_unit - kFar) v_unit = max(e, v_top - kDrop);
+                        begun = true;
+                    }
+                    un[g] = v_unit;
+                }
+            }
+            if (wave == (kShift ? W / 2 : 0) && lane < 4) s_unit[buf][lane] = lane < 2 ? (lane ? un[1] : un[0]) : lane == 2 ? un[2] : un[3];
+            // The notes of the step before the last are done with.
+            if (s_has_nan[(n + 2) & 3]) {
+                for (int i = threadIdx.x & (W * 32 - 1); i < NS * 64; i += W * 32) s_nan[(n + 2) & 3][i] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                int side, g, c;
+                tile_at(j, side, g, c);
+                if (side == 0) continue;
+                const int e = __builtin_amdgcn_readlane(my_ev, from + g), u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+                const int quad = lane >> 4, r = lane & 15;
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad |= nan_bytes(part[j][i]);
+                if (__any(bad != 0)) {
+                    // NaN codes must not reach rows that do not see their token (0 * NaN is NaN): they leave
+                    // the product, and a note of them gives them back to the rows that do. Tokens that nobody
+                    // sees (dropped, or past the last position: often bytes never written) leave no note.
+                    const bool live = (holds >> g & 1) != 0;
+                    const int own = here(lane), place = 16 * g + 4 * (own >> 4), t = token_of(n) + place;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t nb = nan_bytes(part[j][i]);
+                        uint64_t at = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if ((nb >> (8 * k + 7) & 1) && live && t + k <= wg_hi) at |= 1ull << (place + k);
+                        if (at) {
+                            atomicOr(&s_nan[n & 3][64 * c + 4 * (own & 15) + i], (unsigned long long)at);
+                            s_has_nan[n & 3] = 1;
+                        }
+                        part[j][i] &= ~((nb >> 7) * 255u);
+                    }
+                }
+                const float f = pow2i(max(-126, min(127, e - u)));
+                // value 4 r + i: tile vt = i / 2, rho = 2 r + i % 2; half quad % 2, slots 4 (quad / 2) ..
+                u32x2* const d = reinterpret_cast<u32x2*>(s_v + buf * kSide) + ((g * NS + c) * 2 * 64 + (quad & 1) * 32 + 2 * r) * 2 + (quad >> 1);
+                const u32x4 xw = __builtin_bit_cast(u32x4, widen<P>(part[j][0], part[j][1], f, f));
+                const u32x4 yw = __builtin_bit_cast(u32x4, widen<P>(part[j][2], part[j][3], f, f));
+                d[0] = u32x2{xw[0], xw[1]};
+                d[2] = u32x2{xw[2], xw[3]};
+                d[128] = u32x2{yw[0], yw[1]};
+                d[130] = u32x2{yw[2], yw[3]};
+            }
+        }
+        if (moves_k) {
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) {
+                int side, g, c;
+                tile_at(j, side, g, c);
+                if (side != 0) continue;
                 Q8* const d = reinterpret_cast<Q8*>(s_k + buf * kSide) + ((g >> 1) * KS + c * 4 + (lane >> 4)) * 64 + (g & 1) * 16 + (lane & 15);
                 d[0] = widen<Q>(part[j][0], part[j][1], 1.0f, 1.0f);
                 d[32] = widen<Q>(part[j][2], part[j][3], 1.0f, 1.0f);
-                continue;
             }
-            const int e = __builtin_amdgcn_readlane(my_ev, from + g), u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
-            const int quad = lane >> 4, t = token_of(n) + 16 * g + 4 * quad, r = lane & 15;
-            uint32_t bad = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bad |= nan_bytes(part[j][i]);
-            if (__any(bad != 0)) {
-                // NaN codes must not reach rows that do not see their token (0 * NaN is NaN): they leave the
-                // product, and a note of them gives them back to the rows that do. Tokens that nobody sees
-                // (dropped, or past the last position: often bytes never written) leave no note.
-                const bool live = (holds >> g & 1) != 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t nb = nan_bytes(part[j][i]);
-                    uint64_t at = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if ((nb >> (8 * k + 7) & 1) && live && t + k <= wg_hi) at |= 1ull << (16 * g + 4 * quad + k);
-                    if (at) {
-                        atomicOr(&s_nan[buf][64 * c + 4 * r + i], (unsigned long long)at);
-                        s_has_nan[buf] = 1;
-                    }
-                    part[j][i] &= ~((nb >> 7) * 255u);
-                }
-            }
-            const float f = pow2i(max(-126, min(127, e - u)));
-            // value 4 r + i: tile vt = i / 2, rho = 2 r + i % 2; half quad % 2, slots 4 (quad / 2) ..
-            u32x2* const d = reinterpret_cast<u32x2*>(s_v + buf * kSide) + ((g * NS + c) * 2 * 64 + (quad & 1) * 32 + 2 * r) * 2 + (quad >> 1);
-            const u32x4 xw = __builtin_bit_cast(u32x4, widen<P>(part[j][0], part[j][1], f, f));
-            const u32x4 yw = __builtin_bit_cast(u32x4, widen<P>(part[j][2], part[j][3], f, f));
-            d[0] = u32x2{xw[0], xw[1]};
-            d[2] = u32x2{xw[2], xw[3]};
-            d[128] = u32x2{yw[0], yw[1]};
-            d[130] = u32x2{yw[2], yw[3]};
         }
     };
 
@@ -719,123 +761,148 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     bool seen = false;
     int unit = 0;
 
-    for (int i = threadIdx.x; i < 2 * NS * 64; i += 64 * W) s_nan[0][i] = 0;
-    if (threadIdx.x < 2) s_has_nan[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 4 * NS * 64; i += 64 * W) s_nan[0][i] = 0;
+    for (int i = threadIdx.x; i < 64 * W * NS; i += 64 * W) s_bad[0][i] = 0;
+    if (threadIdx.x < 4) s_has_nan[threadIdx.x] = 0;
     ask(0);
     __syncthreads();
-    put(0, 0);
+    put(0);
     if (steps > 1) ask(1);
-    for (int n = 0; n < steps; ++n) {
-        const int buf = n & 1, tok = token_of(n);
-        __syncthreads();
-        const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[buf]) != 0;
-        // Of the two waves of a SIMD one widens before its first products and one behind them: while one
-        // keeps the matrix unit, the other has the vector unit.
-        const auto move = [&]() __attribute__((always_inline)) {
-            if (n + 1 >= steps) return;
-            put(n + 1, buf ^ 1);
-            if (n + 2 >= steps) return;
-            if (((n + 2) & 15) == 0) fetch(n + 2);
-            ask(n + 2);
-        };
-        if (W == 4 || wave < W / 2) move();
-        const bool any = tok <= pos_hi && (!a.window || tok + 63 > pos_lo - a.window || tok < a.sinks) && w0 < rows;
-        f32x16 s[2];
+    // A wave's step n: between barriers the softmax of step n and the move of step n + 1, then the
+    // products of K(n + 1) and of V(n). The two waves of a SIMD are half a step apart, so one has the matrix
+    // unit while the other has the vector unit. The second half's V(n + 1) takes the buffer that
+    // everybody's products of V(n - 1) are done with, the first half's K(n + 1) that of K(n - 1).
+    P8 pv[4][Kd::kP];
+    uint64_t vis = 0;
+    f32x16 s[2];
+    const auto scores = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
-        if (any) {
-            const Q8* const kt = reinterpret_cast<const Q8*>(s_k + buf * kSide) + lane;
+        const Q8* const kt = reinterpret_cast<const Q8*>(s_k + (n & 1) * kSide) + lane;
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const Q8 kk = kt[(t * KS + k) * 64];
+            for (int t = 0; t < 2; ++t) {
+                const Q8 kk = kt[(t * KS + k) * 64];
 #pragma unroll
-                    for (int x = 0; x < Kd::kQ; ++x) s[t] = mfma(kk, q[k][x], s[t]);
-                }
+                for (int x = 0; x < Kd::kQ; ++x) s[t] = mfma(kk, q[k][x], s[t]);
+            }
+        // Operands come from LDS four products ahead.
+        constexpr int kMfma = 0x8, kDsRead = 0x100;  // classes of the scheduler
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KS - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, Kd::kQ, 0);
+            __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
         }
-        if (W != 4 && wave >= W / 2) move();
-        if (any) {
-            float kf[4];
+        __builtin_amdgcn_sched_group_barrier(kMfma, 4 * Kd::kQ, 0);
+    };
+    __syncthreads();
+    if (second) __syncthreads();
+    scores(0);
+    for (int n = 0; n < steps; ++n) {
+        const int buf = n & 1, tok = token_of(n);
+        __syncthreads();
+        float kf[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) kf[g] = s_kf[buf][g];
-            const uint64_t held = s_held[buf];
-            const bool whole = held == ~0ull && tok + 63 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + 64 <= a.sinks);
-            uint64_t vis = ~0ull;  // of the row, a bit per token
-            if (!whole) {
-                const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
-                vis = below(pos - tok + 1) & held;
-                if (a.window) vis &= ~below(pos - a.window + 1 - tok) | below(a.sinks - tok);
-                const uint64_t mine = vis >> (4 * half);
+        for (int g = 0; g < 4; ++g) kf[g] = s_kf[buf][g];
+        const uint64_t held = s_held[buf];
+        int un[4];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int bit = 8 * (i >> 2) + (i & 3);
-                    const int keep = (int)((uint32_t)(mine >> (bit & 32)) << (31 - (bit & 31))) >> 31;
-                    s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & keep) | (0xff800000u & ~keep));
-                }
+        for (int g = 0; g < 4; ++g) un[g] = __builtin_amdgcn_readfirstlane(s_unit[buf][g]);
+        const bool same = un[0] == unit && un[1] == unit && un[2] == unit && un[3] == unit;
+        const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[n & 3]) != 0;
+        const bool whole = held == ~0ull && tok + 63 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + 64 <= a.sinks);
+        vis = ~0ull;  // of the row, a bit per token
+        if (!whole) {
+            const auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+            vis = below(pos - tok + 1) & held;
+            if (a.window) vis &= ~below(pos - a.window + 1 - tok) | below(a.sinks - tok);
+            const uint64_t mine = vis >> (4 * half);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int bit = 8 * (i >> 2) + (i & 3);
+                const int keep = (int)((uint32_t)(mine >> (bit & 32)) << (31 - (bit & 31))) >> 31;
+                s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & keep) | (0xff800000u & ~keep));
             }
-            seen |= vis != 0;
-            float mx = -__builtin_inff();
+        }
+        seen |= vis != 0;
+        float mx = -__builtin_inff();
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float x = s[g >> 1][8 * (g & 1)];
+        for (int g = 0; g < 4; ++g) {
+            float x = s[g >> 1][8 * (g & 1)];
 #pragma unroll
-                for (int j = 1; j < 8; ++j) x = fmaxf(x, s[g >> 1][8 * (g & 1) + j]);
-                mx = fmaxf(mx, x * kf[g]);
+            for (int j = 1; j < 8; ++j) x = fmaxf(x, s[g >> 1][8 * (g & 1) + j]);
+            mx = fmaxf(mx, x * kf[g]);
+        }
+        if (__any(mx > m + kLazy)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float m1 = fmaxf(m, mx);
+            const float f = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
+        }
+        const float m0 = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float p[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g >> 1][8 * (g & 1) + j], kf[g], -m0));
+                l += p[j];
             }
-            if (__any(mx > m + kLazy)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32));
-                const float m1 = fmaxf(m, mx);
-                const float f = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-                m = m1;
-                l *= f;
+            split<P, Kd::kP>(pv[g], p);
+#pragma unroll
+            for (int x = 0; x < Kd::kP; ++x) pv[g][x] = settled(pv[g][x]);  // in this phase, not behind the barrier
+        }
+        if (n + 1 < steps) {
+            put(n + 1);
+            if (n + 2 < steps) {
+                if (((n + 2) & 15) == 0) fetch(n + 2);
+                ask(n + 2);
+            }
+        }
+        __syncthreads();
+        // Behind the last step the scores are of no use (its K buffer holds an old step), but cost no branch.
+        scores(n + 1);
+        const P8* const vt = reinterpret_cast<const P8*>(s_v + buf * kSide) + lane;
+        P8 vv[2][2 * NS];  // a group's operands, asked for a group ahead
+#pragma unroll
+        for (int i = 0; i < 2 * NS; ++i) vv[0][i] = vt[i * 64];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            if (un[g] != unit) {
+                const float f = pow2i(max(-126, min(127, unit - un[g])));
 #pragma unroll
                 for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
+                unit = un[g];
             }
-            const float m0 = m == -__builtin_inff() ? 0.0f : m;
+            if (g < 3) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float p[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g >> 1][8 * (g & 1) + j], kf[g], -m0));
-                    l += p[j];
-                }
-                P8 pv[Kd::kP];
-                split<P, Kd::kP>(pv, p);
-                const int un = __builtin_amdgcn_readfirstlane(s_unit[buf][g]);
-                if (un != unit) {
-                    const float f = pow2i(max(-126, min(127, unit - un)));
-#pragma unroll
-                    for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
-                    unit = un;
-                }
-                const P8* const vt = reinterpret_cast<const P8*>(s_v + buf * kSide) + g * NS * 2 * 64 + lane;
-#pragma unroll
-                for (int i = 0; i < 2 * NS; ++i) {
-                    const P8 vv = vt[i * 64];
-#pragma unroll
-                    for (int x = 0; x < Kd::kP; ++x) o[i] = mfma(vv, pv[x], o[i]);
-                }
+                for (int i = 0; i < 2 * NS; ++i) vv[(g + 1) & 1][i] = vt[((g + 1) * 2 * NS + i) * 64];
             }
-            if (has_nan) {
 #pragma unroll
-                for (int i = 0; i < 2 * NS; ++i)
+            for (int i = 0; i < 2 * NS; ++i)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int rho = 8 * (j >> 2) + 4 * half + (j & 3);
-                        if (s_nan[buf][64 * (i >> 1) + 4 * (rho >> 1) + 2 * (i & 1) + (rho & 1)] & vis) o[i][j] = __builtin_nanf("");
-                    }
-            }
+                for (int x = 0; x < Kd::kP; ++x) o[i] = mfma(vv[g & 1][i], pv[g][x], o[i]);
         }
-        if (has_nan) {  // cleared for the step after the next, which writes it behind the next barrier
-            __syncthreads();
-            for (int i = threadIdx.x; i < NS * 64; i += 64 * W) s_nan[buf][i] = 0;
-            if (threadIdx.x == 0) s_has_nan[buf] = 0;
+        if (has_nan) {
+            // Which values of this row meet a NaN: kept aside, for the end.
+            const unsigned long long* const notes = s_nan[n & 3] + here(half) * 32 * NS;
+#pragma unroll 1
+            for (int w = 0; w < NS; ++w) {
+                uint32_t word = 0;
+#pragma unroll 1
+                for (int d = 0; d < 32; ++d) word |= (notes[32 * w + d] & vis) ? 1u << d : 0u;
+                s_bad[wave * 32 + col][half * NS + w] |= word;
+            }
         }
     }
+    if (kShift && !second) __syncthreads();
 
     l += __shfl_xor(l, 32);
     seen = (__ballot(seen) >> col & 0x0000000100000001ull) != 0;
@@ -850,9 +917,13 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         for (int i = 0; i < 4; ++i) {
             const int d = 64 * c + 16 * i + 8 * half;
             if (d >= kv.hd) continue;
+            const uint32_t bad = s_bad[wave * 32 + col][d >> 5] >> (d & 31);
             T y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = (T)(seen ? o[2 * c + (e >> 1 & 1)][4 * i + 2 * (e >> 2) + (e & 1)] * back * inv : 0.0f);
+            for (int e = 0; e < 8; ++e) {
+                const float x = seen ? o[2 * c + (e >> 1 & 1)][4 * i + 2 * (e >> 2) + (e & 1)] * back * inv : 0.0f;
+                y[e] = (T)(bad >> e & 1 ? __builtin_nanf("") : x);
+            }
             __builtin_memcpy(__builtin_assume_aligned(out + d, 16), y, sizeof y);
         }
     if (a.lse && half == 0)
