@@ -552,8 +552,9 @@ __device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amd
 //
 // Operand slots: S^T lane (half, row) holds tokens 8 (i / 4) + 4 half + i % 4, i < 16, of a 32-token
 // block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
-// V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho / 2) + 2 vt +
-// rho % 2: then a lane ends with eight consecutive values of its row.
+// V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho % 16) + 2 vt +
+// rho / 16: then the lanes that widen V write without bank conflicts, and a lane ends with runs of 16
+// consecutive values of its row.
 // x, but made where it stands: what rare paths compute from the lane is not kept in registers across
 // the loop for them.
 __device__ inline int here(int x) {
@@ -667,7 +668,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         }
     };
     int v_unit = 0, v_top = 0;
-    bool begun = false;
+    bool begun = false, nan_met = false;  // nan_met: some step so far had a NaN
     const auto put = [&](int n) __attribute__((always_inline)) {
         const int buf = n & 1, from = (n & 15) * 4, my_ev = max(-126, (int)(int8_t)(ahead_exps >> 8));
         const uint32_t holds = (uint32_t)(__ballot(ahead_held) >> from) & 15;
@@ -695,7 +696,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
             if (wave == (kShift ? W / 2 : 0) && lane < 4) s_unit[buf][lane] = lane < 2 ? (lane ? un[1] : un[0]) : lane == 2 ? un[2] : un[3];
             // The notes of the step before the last are done with.
-            if (s_has_nan[(n + 2) & 3]) {
+            if (nan_met) {
                 for (int i = threadIdx.x & (W * 32 - 1); i < NS * 64; i += W * 32) s_nan[(n + 2) & 3][i] = 0;
             }
 #pragma unroll
@@ -729,14 +730,14 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                     }
                 }
                 const float f = pow2i(max(-126, min(127, e - u)));
-                // value 4 r + i: tile vt = i / 2, rho = 2 r + i % 2; half quad % 2, slots 4 (quad / 2) ..
-                u32x2* const d = reinterpret_cast<u32x2*>(s_v + buf * kSide) + ((g * NS + c) * 2 * 64 + (quad & 1) * 32 + 2 * r) * 2 + (quad >> 1);
+                // value 4 r + i: tile vt = i / 2, rho = r + 16 (i % 2); half quad % 2, slots 4 (quad / 2) ..
+                u32x2* const d = reinterpret_cast<u32x2*>(s_v + buf * kSide) + ((g * NS + c) * 2 * 64 + (quad & 1) * 32 + r) * 2 + (quad >> 1);
                 const u32x4 xw = __builtin_bit_cast(u32x4, widen<P>(part[j][0], part[j][1], f, f));
                 const u32x4 yw = __builtin_bit_cast(u32x4, widen<P>(part[j][2], part[j][3], f, f));
                 d[0] = u32x2{xw[0], xw[1]};
-                d[2] = u32x2{xw[2], xw[3]};
+                d[32] = u32x2{xw[2], xw[3]};
                 d[128] = u32x2{yw[0], yw[1]};
-                d[130] = u32x2{yw[2], yw[3]};
+                d[160] = u32x2{yw[2], yw[3]};
             }
         }
         if (moves_k) {
@@ -775,33 +776,38 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     P8 pv[4][Kd::kP];
     uint64_t vis = 0;
     f32x16 s[2];
-    const auto scores = [&](int n) __attribute__((always_inline)) {
+    // The products of K(n) (S = 0 first) and of V(n - 1), interleaved: a sum's next product is issued
+    // when the last one's result is there. Operands come from LDS a few products ahead.
+    const auto products = [&](int n, bool first) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
         const Q8* const kt = reinterpret_cast<const Q8*>(s_k + (n & 1) * kSide) + lane;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Q8 kk = kt[(t * KS + k) * 64];
-#pragma unroll
-                for (int x = 0; x < Kd::kQ; ++x) s[t] = mfma(kk, q[k][x], s[t]);
-            }
-        // Operands come from LDS four products ahead.
+        const P8* const vt = reinterpret_cast<const P8*>(s_v + (~n & 1) * kSide) + lane;
         constexpr int kMfma = 0x8, kDsRead = 0x100;  // classes of the scheduler
-        __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
 #pragma unroll
-        for (int i = 0; i < 2 * KS - 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(kMfma, Kd::kQ, 0);
+        for (int k = 0; k < 2 * KS; ++k) {  // 2 KS = 8 NS products of each kind
+            const Q8 kk = kt[((k & 1) * KS + (k >> 1)) * 64];
+#pragma unroll
+            for (int x = 0; x < Kd::kQ; ++x) s[k & 1] = mfma(kk, q[k >> 1][x], s[k & 1]);
+            if (first) continue;
+            const P8 vv = vt[k * 64];
+#pragma unroll
+            for (int x = 0; x < Kd::kP; ++x) o[k % (2 * NS)] = mfma(vv, pv[k / (2 * NS)][x], o[k % (2 * NS)]);
+        }
+        constexpr int kAhead = 4;
+        __builtin_amdgcn_sched_group_barrier(kDsRead, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < (first ? 2 : 4) * KS - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, Kd::kQ, 0);  // kQ = kP
             __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(kMfma, 4 * Kd::kQ, 0);
+        __builtin_amdgcn_sched_group_barrier(kMfma, kAhead * Kd::kQ, 0);
     };
     __syncthreads();
     if (second) __syncthreads();
-    scores(0);
+    products(0, true);
     for (int n = 0; n < steps; ++n) {
         const int buf = n & 1, tok = token_of(n);
         __syncthreads();
@@ -814,6 +820,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         for (int g = 0; g < 4; ++g) un[g] = __builtin_amdgcn_readfirstlane(s_unit[buf][g]);
         const bool same = un[0] == unit && un[1] == unit && un[2] == unit && un[3] == unit;
         const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[n & 3]) != 0;
+        nan_met |= has_nan;
         const bool whole = held == ~0ull && tok + 63 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + 64 <= a.sinks);
         vis = ~0ull;  // of the row, a bit per token
         if (!whole) {
@@ -867,29 +874,31 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
         }
         __syncthreads();
-        // Behind the last step the scores are of no use (its K buffer holds an old step), but cost no branch.
-        scores(n + 1);
-        const P8* const vt = reinterpret_cast<const P8*>(s_v + buf * kSide) + lane;
-        P8 vv[2][2 * NS];  // a group's operands, asked for a group ahead
+        if (un[0] != unit || un[1] != unit || un[2] != unit || un[3] != unit) {
+            // A change of unit. If not all groups share the new one, their products are made here, one
+            // group after the other, and the weights below are zero.
+            const bool one = un[0] == un[1] && un[0] == un[2] && un[0] == un[3];
+            const P8* const vt = reinterpret_cast<const P8*>(s_v + buf * kSide) + lane;
 #pragma unroll
-        for (int i = 0; i < 2 * NS; ++i) vv[0][i] = vt[i * 64];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (un[g] != unit) {
+            for (int g = 0; g < 4; ++g) {
                 const float f = pow2i(max(-126, min(127, unit - un[g])));
-#pragma unroll
-                for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
                 unit = un[g];
+#pragma unroll
+                for (int i = 0; i < 2 * NS; ++i) {
+                    o[i] *= f;
+                    if (!one) {
+#pragma unroll
+                        for (int x = 0; x < Kd::kP; ++x) o[i] = mfma(vt[(g * 2 * NS + i) * 64], pv[g][x], o[i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);  // a rare path that must not cost registers
+                }
+#pragma unroll
+                for (int x = 0; x < Kd::kP; ++x)
+                    if (!one) pv[g][x] = __builtin_bit_cast(P8, u32x4{0, 0, 0, 0});
             }
-            if (g < 3) {
-#pragma unroll
-                for (int i = 0; i < 2 * NS; ++i) vv[(g + 1) & 1][i] = vt[((g + 1) * 2 * NS + i) * 64];
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * NS; ++i)
-#pragma unroll
-                for (int x = 0; x < Kd::kP; ++x) o[i] = mfma(vv[g & 1][i], pv[g][x], o[i]);
         }
+        // Behind the last step the scores are of no use (its K buffer holds an old step), but cost no branch.
+        products(n + 1, false);
         if (has_nan) {
             // Which values of this row meet a NaN: kept aside, for the end.
             const unsigned long long* const notes = s_nan[n & 3] + here(half) * 32 * NS;
@@ -914,14 +923,16 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 #pragma unroll
     for (int c = 0; c < NS; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = 64 * c + 16 * i + 8 * half;
+        for (int i = 0; i < 4; ++i) {  // eight values: run i / 2, its half i % 2
+            const int d = 64 * c + 32 * (i >> 1) + 16 * half + 8 * (i & 1);
             if (d >= kv.hd) continue;
             const uint32_t bad = s_bad[wave * 32 + col][d >> 5] >> (d & 31);
             T y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = seen ? o[2 * c + (e >> 1 & 1)][4 * i + 2 * (e >> 2) + (e & 1)] * back * inv : 0.0f;
+                // d + e = 64 c + 4 rho' + 2 vt + hi with rho' = 8 (i / 2) + 4 half + j, rho = rho' + 16 hi
+                const int j = 2 * (i & 1) + (e >> 2), vt = e >> 1 & 1, hi = e & 1;
+                const float x = seen ? o[2 * c + vt][4 * ((i >> 1) + 2 * hi) + j] * back * inv : 0.0f;
                 y[e] = (T)(bad >> e & 1 ? __builtin_nanf("") : x);
             }
             __builtin_memcpy(__builtin_assume_aligned(out + d, 16), y, sizeof y);
