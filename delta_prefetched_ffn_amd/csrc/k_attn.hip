@@ -637,9 +637,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     P* const s_v = reinterpret_cast<P*>(s_mem) + 2 * kSide;    // [2][4 groups][2 NS][2 halves][32 rho][8]
     // Per step: the groups' K factors, a bit per token of held groups, the groups' V units; whether a V
     // code is NaN and, per value, the tokens where it is.
-    __shared__ float s_kf[2][4];
+    __shared__ __attribute__((aligned(16))) float s_kf[2][4];
     __shared__ uint64_t s_held[2];
-    __shared__ int s_unit[2][4];
+    __shared__ __attribute__((aligned(16))) int s_unit[2][4];
     __shared__ int s_has_nan[4];
     __shared__ unsigned long long s_nan[4][NS * 64];
     __shared__ uint32_t s_bad[32 * W][2 * NS];  // per row, a bit per value: it is NaN
@@ -807,20 +807,15 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     };
     __syncthreads();
     if (second) __syncthreads();
+    f32x4 kf = *reinterpret_cast<const f32x4*>(s_kf[0]);
+    uint64_t held = s_held[0];
     products(0, true);
     for (int n = 0; n < steps; ++n) {
         const int buf = n & 1, tok = token_of(n);
         __syncthreads();
-        float kf[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) kf[g] = s_kf[buf][g];
-        const uint64_t held = s_held[buf];
-        int un[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) un[g] = __builtin_amdgcn_readfirstlane(s_unit[buf][g]);
-        const bool same = un[0] == unit && un[1] == unit && un[2] == unit && un[3] == unit;
-        const bool has_nan = __builtin_amdgcn_readfirstlane(s_has_nan[n & 3]) != 0;
-        nan_met |= has_nan;
+        // Read here, used behind the exponentials.
+        const int has_nan_v = s_has_nan[n & 3];
+        const u32x4 un_v = *reinterpret_cast<const u32x4*>(s_unit[buf]);
         const bool whole = held == ~0ull && tok + 63 <= pos_lo && (!a.window || tok > pos_hi - a.window || tok + 64 <= a.sinks);
         vis = ~0ull;  // of the row, a bit per token
         if (!whole) {
@@ -874,6 +869,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
         }
         __syncthreads();
+        int un[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) un[g] = __builtin_amdgcn_readfirstlane((int)un_v[g]);
+        const bool has_nan = __builtin_amdgcn_readfirstlane(has_nan_v) != 0;
+        nan_met |= has_nan;
         if (un[0] != unit || un[1] != unit || un[2] != unit || un[3] != unit) {
             // A change of unit. If not all groups share the new one, their products are made here, one
             // group after the other, and the weights below are zero.
@@ -898,6 +898,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
         }
         // Behind the last step the scores are of no use (its K buffer holds an old step), but cost no branch.
+        kf = *reinterpret_cast<const f32x4*>(s_kf[buf ^ 1]);  // of step n + 1
+        held = s_held[buf ^ 1];
         products(n + 1, false);
         if (has_nan) {
             // Which values of this row meet a NaN: kept aside, for the end.
