@@ -108,8 +108,8 @@ def lib() -> ctypes.CDLL:
         "np_kv_fork": [vp, i32, i32, i32, i32, vp],
         "np_kv_trim": [vp, i32, i32],
         "np_kv_free": [vp, i32],
-        "np_kv_adopt": [vp, i32, vp, i32, i32, vp],
-        "np_kv_evict": [vp, i32, i32, i32, vp, vp],
+        "np_kv_adopt": [vp, i32, vp, i32, i32],
+        "np_kv_evict": [vp, i32, i32, i32, vp],
         "np_kv_compact": [vp, vp, vp],
         "np_kv_read_pages": [vp, i32, vp, i32, vp, vp],
         "np_kv_read_tokens": [vp, i32, i32, i32, i32, vp, vp],
@@ -339,14 +339,14 @@ class KVCache:
         _check(lib().np_kv_free(self.h, seq))
 
     def adopt(self, seq: int, pages, n_tokens: int, stream: int = 0) -> None:
-        """The empty sequence seq becomes these pages of the pool, holding n_tokens tokens."""
+        """The empty sequence seq becomes these pages of the pool, holding n_tokens tokens (nothing is enqueued)."""
         p = np.ascontiguousarray(pages, dtype=np.int32)
-        _check(lib().np_kv_adopt(self.h, seq, p.ctypes.data, p.size, n_tokens, stream or None))
+        _check(lib().np_kv_adopt(self.h, seq, p.ctypes.data, p.size, n_tokens))
 
     def evict(self, seq: int, window: int, sinks: int = 0, stream: int = 0) -> int:
-        """Drops the pages that no later query of this window sees; how many."""
+        """Drops the pages that no later query of this window sees; how many (nothing is enqueued)."""
         n = ctypes.c_int32(0)
-        _check(lib().np_kv_evict(self.h, seq, window, sinks, ctypes.byref(n), stream or None))
+        _check(lib().np_kv_evict(self.h, seq, window, sinks, ctypes.byref(n)))
         return n.value
 
     def compact(self, stream: int = 0) -> int:

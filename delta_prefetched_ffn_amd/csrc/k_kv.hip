@@ -141,10 +141,9 @@ hipError_t append_as(const AppendArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-__global__ __launch_bounds__(256) void k_kv_table(TableArgs a) {
-    const TableRun r = a.run[blockIdx.x];
-    for (int k = threadIdx.x; k < r.count; k += 256)
-        a.table[(int64_t)r.seq * a.max_pages + r.index0 + k] = r.page0 < 0 ? -1 : r.page0 + k;
+__global__ __launch_bounds__(kTableEntries) void k_kv_table(TableArgs a) {
+    const int k = threadIdx.x;
+    if (k < a.n) a.table[a.at[k]] = a.page[k];
 }
 
 // Page copies, every layer at once: blockIdx.z = pair, blockIdx.y = layer, blockIdx.x = piece of
@@ -176,7 +175,7 @@ hipError_t launch_kv_append(const AppendArgs& a, int dtype, hipStream_t s) {
 }
 
 hipError_t launch_kv_table(const TableArgs& a, hipStream_t s) {
-    k_kv_table<<<a.n, 256, 0, s>>>(a);
+    k_kv_table<<<1, kTableEntries, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -82,15 +82,12 @@ constexpr int kPieceTokens = 32;
 constexpr int kMaxPartials = 8192;
 constexpr int kMaxPartialRows = 32768;
 
-// Page table entries (seq, index0 + k) = page0 + k * step for k < count; step 0 repeats page0.
-constexpr int kTableRuns = 200;
-struct TableRun {
-    int32_t seq, index0, count, page0;
-};
+// Page table entries to write: table[at[k]] = page[k], k < n.
+constexpr int kTableEntries = 480;
 struct TableArgs {
     int32_t* table;
-    int32_t max_pages, n;
-    TableRun run[kTableRuns];
+    int32_t n;
+    int32_t at[kTableEntries], page[kTableEntries];
 };
 
 constexpr int kCopyPairs = 448;

@@ -33,6 +33,7 @@ constexpr int kManyRows = 128;
 struct Seq {
     std::vector<int32_t> pages;  // -1: dropped
     int32_t tokens = 0;
+    int32_t stale_lo = 0, stale_hi = 0;  // entries that the device's page table does not have yet
 };
 
 }  // namespace
@@ -45,6 +46,7 @@ struct np_kv {
     std::vector<uint64_t> free_w;   // bit set: free
     int32_t n_free = 0;
     std::vector<Seq> seqs;
+    std::vector<int32_t> stale;     // sequences with such entries
     std::vector<int32_t> b_seq, b_before, b_fresh;  // the current batch (np_kv_extend); empty: none
     bool broken = false;            // a launch failed in the middle of a call
     int32_t* table = nullptr;
@@ -79,6 +81,19 @@ struct np_kv {
         free_w[p >> 6] |= 1ull << (p & 63);
         ++n_free;
     }
+    // Entries [lo, hi) of a sequence have changed.
+    void touch(int32_t seq, int32_t lo, int32_t hi) {
+        Seq& q = seqs[seq];
+        if (lo >= hi) return;
+        if (q.stale_lo == q.stale_hi) {
+            stale.push_back(seq);
+            q.stale_lo = lo;
+            q.stale_hi = hi;
+        } else {
+            q.stale_lo = std::min(q.stale_lo, lo);
+            q.stale_hi = std::max(q.stale_hi, hi);
+        }
+    }
     void drop_batch_of(int32_t seq) {
         if (std::find(b_seq.begin(), b_seq.end(), seq) != b_seq.end()) drop_batch();
     }
@@ -92,7 +107,12 @@ struct np_kv {
         free_w.assign((desc.n_pages + 63) / 64, ~0ull);
         if (desc.n_pages & 63) free_w.back() = (1ull << (desc.n_pages & 63)) - 1;
         n_free = desc.n_pages;
-        seqs.assign(desc.max_seqs, Seq());
+        for (Seq& q : seqs) {
+            q.pages.clear();
+            q.tokens = q.stale_lo = q.stale_hi = 0;
+        }
+        seqs.resize(desc.max_seqs);
+        stale.clear();
         drop_batch();
     }
     KvView view() const {
@@ -148,41 +168,34 @@ np_status copy_pages(np_kv* kv, const std::vector<Move>& moves, hipStream_t s) {
     return NP_OK;
 }
 
-// Collects page table entries as runs of consecutive pages and writes them in order on a stream.
-struct TableWriter {
-    std::vector<TableRun> runs;
-    void set(int32_t seq, int32_t index, int32_t page) {
-        if (!runs.empty()) {
-            TableRun& r = runs.back();
-            if (r.seq == seq && r.index0 + r.count == index &&
-                (r.page0 < 0 ? page < 0 : page == r.page0 + r.count)) {
-                ++r.count;
-                return;
+// Writes the entries that changed since the last flush, as they are now, to the device's page table.
+np_status flush_table(np_kv* kv, hipStream_t s) {
+    TableArgs a;
+    a.table = kv->table;
+    a.n = 0;
+    const auto launch = [&]() -> np_status {
+        const hipError_t e = a.n ? launch_kv_table(a, s) : hipSuccess;
+        a.n = 0;
+        if (e == hipSuccess) return NP_OK;
+        kv->broken = true;
+        return fail(NP_EHIP, "page table update failed: %s", hipGetErrorString(e));
+    };
+    for (const int32_t q : kv->stale) {
+        Seq& seq = kv->seqs[q];
+        const int32_t end = std::min<int32_t>(seq.stale_hi, (int32_t)seq.pages.size());
+        for (int32_t i = seq.stale_lo; i < end && !kv->host_only(); ++i) {
+            a.at[a.n] = q * kv->desc.max_pages + i;
+            a.page[a.n] = seq.pages[i];
+            if (++a.n == kTableEntries) {
+                const np_status st = launch();
+                if (st != NP_OK) return st;
             }
         }
-        runs.push_back({seq, index, 1, page});
+        seq.stale_lo = seq.stale_hi = 0;
     }
-    void set_all(const np_kv* kv, int32_t seq) {
-        const std::vector<int32_t>& p = kv->seqs[seq].pages;
-        for (size_t i = 0; i < p.size(); ++i) set(seq, (int32_t)i, p[i]);
-    }
-    np_status flush(np_kv* kv, hipStream_t s) const {
-        if (runs.empty() || kv->host_only()) return NP_OK;
-        TableArgs a;
-        a.table = kv->table;
-        a.max_pages = kv->desc.max_pages;
-        for (size_t i = 0; i < runs.size(); i += kTableRuns) {
-            a.n = (int32_t)std::min<size_t>(kTableRuns, runs.size() - i);
-            std::copy(runs.begin() + i, runs.begin() + i + a.n, a.run);
-            const hipError_t e = launch_kv_table(a, s);
-            if (e != hipSuccess) {
-                kv->broken = true;
-                return fail(NP_EHIP, "page table update failed: %s", hipGetErrorString(e));
-            }
-        }
-        return NP_OK;
-    }
-};
+    kv->stale.clear();
+    return launch();
+}
 
 np_status check_seq(const np_kv* kv, int32_t seq, const char* what) {
     if (seq < 0 || seq >= kv->desc.max_seqs)
@@ -342,7 +355,6 @@ np_status extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new
     // From here on nothing is refused. A page given up by a copy is still held by another sequence,
     // so copies read pages that nothing writes.
     std::vector<Move> moves;
-    TableWriter table;
     kv->drop_batch();
     for (int i = 0; i < n; ++i) {
         Seq& q = kv->seqs[seqs[i]];
@@ -355,19 +367,17 @@ np_status extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new
             moves.push_back({at, p});
             kv->release(at);
             at = p;
-            table.set(seqs[i], q.tokens / pt, p);
+            kv->touch(seqs[i], q.tokens / pt, q.tokens / pt + 1);
         }
         q.tokens += n_new[i];
-        while ((int)q.pages.size() < kv->pages_for(q.tokens)) {
-            const int32_t p = kv->take();
-            table.set(seqs[i], (int32_t)q.pages.size(), p);
-            q.pages.push_back(p);
-        }
+        const int32_t had = (int32_t)q.pages.size();
+        while ((int)q.pages.size() < kv->pages_for(q.tokens)) q.pages.push_back(kv->take());
+        kv->touch(seqs[i], had, (int32_t)q.pages.size());
     }
-    if (kv->host_only()) return NP_OK;
+    if (kv->host_only()) return flush_table(kv, s);
     DeviceGuard g(kv->desc.device);
     if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
-    return table.flush(kv, s);
+    return flush_table(kv, s);
 }
 
 np_status append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t dtype, const int64_t* strides, hipStream_t s) {
@@ -519,15 +529,13 @@ np_status fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mo
             ++kv->refs[p];
         }
     }
-    if (kv->host_only()) return NP_OK;
+    kv->touch(dst, 0, n);
+    if (moves.empty() || kv->host_only()) return NP_OK;
     DeviceGuard g(kv->desc.device);
-    if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
-    TableWriter table;
-    table.set_all(kv, dst);
-    return table.flush(kv, s);
+    return copy_pages(kv, moves, s);
 }
 
-np_status adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens, hipStream_t s) {
+np_status adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens) {
     np_status st = check_kv(kv);
     if (st != NP_OK) return st;
     if ((st = check_seq(kv, seq, "sequence")) != NP_OK) return st;
@@ -551,20 +559,16 @@ np_status adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, i
     kv->drop_batch_of(seq);
     for (int32_t p : q.pages)
         if (p >= 0) kv->take_page(p);
-    if (kv->host_only()) return NP_OK;
-    DeviceGuard g(kv->desc.device);
-    TableWriter table;
-    table.set_all(kv, seq);
-    return table.flush(kv, s);
+    kv->touch(seq, 0, n_pages);
+    return NP_OK;
 }
 
-np_status evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed, hipStream_t s) {
+np_status evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed) {
     np_status st = check_kv(kv);
     if (st != NP_OK) return st;
     if ((st = check_seq(kv, seq, "sequence")) != NP_OK) return st;
     if (window < 1 || sinks < 0) return fail(NP_EINVAL, "window=%d must be positive and sinks=%d not negative", window, sinks);
     Seq& q = kv->seqs[seq];
-    TableWriter table;
     // Tokens [sinks, tokens - window] are visible to no later query: whole pages of them go.
     const int64_t end = (int64_t)q.tokens - window + 1;
     int32_t freed = 0;
@@ -574,14 +578,11 @@ np_status evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* 
         kv->release(p);
         p = -1;
         ++freed;
-        table.set(seq, (int32_t)i, -1);
+        kv->touch(seq, (int32_t)i, (int32_t)i + 1);
     }
     if (n_freed) *n_freed = freed;
-    if (!freed) return NP_OK;
-    kv->drop_batch_of(seq);
-    if (kv->host_only()) return NP_OK;
-    DeviceGuard g(kv->desc.device);
-    return table.flush(kv, s);
+    if (freed) kv->drop_batch_of(seq);
+    return NP_OK;
 }
 
 np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
@@ -599,13 +600,12 @@ np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
     }
     if (n_moved) *n_moved = (int32_t)moves.size();
     if (moves.empty()) return NP_OK;
-    TableWriter table;
     for (int32_t q = 0; q < kv->desc.max_seqs; ++q) {
         std::vector<int32_t>& pages = kv->seqs[q].pages;
         for (size_t i = 0; i < pages.size(); ++i)
             if (pages[i] >= live) {
                 pages[i] = to[pages[i]];
-                table.set(q, (int32_t)i, pages[i]);
+                kv->touch(q, (int32_t)i, (int32_t)i + 1);
             }
     }
     for (const Move& m : moves) {
@@ -617,7 +617,7 @@ np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
     if (kv->host_only()) return NP_OK;
     DeviceGuard g(kv->desc.device);
     if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
-    return table.flush(kv, s);
+    return kv->b_seq.empty() ? NP_OK : flush_table(kv, s);  // the current step goes on with the new pages
 }
 
 float e4m3_value(uint8_t b) {
@@ -752,12 +752,12 @@ np_status np_kv_trim(np_kv* kv, int32_t seq, int32_t n_tokens) {
 
 np_status np_kv_free(np_kv* kv, int32_t seq) { return np_kv_trim(kv, seq, 0); }
 
-np_status np_kv_adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens, void* stream) {
-    return guarded([&] { return adopt(kv, seq, pages, n_pages, n_tokens, (hipStream_t)stream); });
+np_status np_kv_adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens) {
+    return guarded([&] { return adopt(kv, seq, pages, n_pages, n_tokens); });
 }
 
-np_status np_kv_evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed, void* stream) {
-    return guarded([&] { return evict(kv, seq, window, sinks, n_freed, (hipStream_t)stream); });
+np_status np_kv_evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed) {
+    return guarded([&] { return evict(kv, seq, window, sinks, n_freed); });
 }
 
 np_status np_kv_compact(np_kv* kv, int32_t* n_moved, void* stream) {

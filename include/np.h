@@ -401,9 +401,10 @@ np_status np_layer_raise_error(np_layer* layer, int32_t bits, void* stream);
  *
  * A sequence is a list of pages and a length: token j lies in its page
  * j / page_tokens. The page lists live on the host (the library's, exact) and
- * are mirrored on the device; pages are shared by reference count, and a
- * shared page is copied before a sequence writes into it. New pages are the
- * free pages with the lowest numbers.
+ * are mirrored on the device (np_kv_extend writes what changed); pages are
+ * shared by reference count, and a shared page is copied before a sequence
+ * writes into it. New pages are the free pages with the lowest numbers. Calls
+ * without a stream argument enqueue nothing.
  *
  * A step: np_kv_extend says which sequences get how many new tokens; then, for
  * every layer, np_kv_append stores those tokens' keys and values and
@@ -510,21 +511,22 @@ np_status np_kv_attend(np_kv* kv, int32_t layer, const void* q, void* out, float
 np_status np_kv_fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mode, void* stream);
 
 /* Shortens seq to n_tokens (rejected drafts) and gives back the pages past
- * them; np_kv_free gives back all. Enqueues nothing: pages are used again by
- * later calls of the same order. */
+ * them; np_kv_free gives back all. NP_EINVAL if n_tokens is above seq's length
+ * or inside a page that seq has dropped. */
 np_status np_kv_trim(np_kv* kv, int32_t seq, int32_t n_tokens);
 np_status np_kv_free(np_kv* kv, int32_t seq);
 
 /* Makes the empty sequence seq the given pages (host, n_pages of them, each
  * free; -1: a page of past tokens that was dropped) holding n_tokens tokens
  * that the pool already contains: a restored or planned cache. Pages past the
- * tokens stay reserved for the sequence. */
-np_status np_kv_adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens, void* stream);
+ * tokens stay reserved for the sequence. NP_EINVAL for a page out of range,
+ * in use or given twice. */
+np_status np_kv_adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, int32_t n_tokens);
 
 /* Gives back seq's pages whose tokens no later query sees with this window and
  * these sinks (call it after the step's last attend). *n_freed (may be NULL):
  * pages dropped. Without a window, attend does not see them either. */
-np_status np_kv_evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed, void* stream);
+np_status np_kv_evict(np_kv* kv, int32_t seq, int32_t window, int32_t sinks, int32_t* n_freed);
 
 /* Moves the pages in use to the front of the pool, so that pages [in use,
  * n_pages) are free: the k-th page in use past the front (ascending) goes to
