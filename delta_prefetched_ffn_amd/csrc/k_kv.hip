@@ -19,6 +19,16 @@ __device__ inline int exp_for(float a) {
     return max(-120, min(120, e));
 }
 
+__device__ inline float block_max(float x, int threads, int use) {
+    __shared__ float s[2][4];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
+    if ((threadIdx.x & 63) == 0) s[use][threadIdx.x >> 6] = x;
+    __syncthreads();
+    for (int w = 0; w < threads >> 6; ++w) x = fmaxf(x, s[use][w]);
+    return x;
+}
+
 // One workgroup per (touched page, kv head, K or V): the block's new values are read once and stay
 // in registers between the maximum and the rounding. A thread holds CPT chunks of 16 codes: for K
 // 16 values of one token, for V four tokens of four values (np.h), so that every store is one
@@ -27,11 +37,11 @@ __device__ inline int exp_for(float a) {
 template <typename T, int CPT>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     const KvView& kv = a.kv;
-    const int b = find_item(a.b, blockIdx.x);
-    const int h = blockIdx.y, side = blockIdx.z;
+    const int item = blockIdx.x / kv.n_kv, h = blockIdx.x - item * kv.n_kv, side = blockIdx.y;
+    const int b = find_item(a.b, item);
     const int pt = 1 << kv.page_shift;
     const int before = a.b.before[b], fresh = a.b.fresh[b];
-    const int index = (before >> kv.page_shift) + ((int)blockIdx.x - a.b.item0[b]);
+    const int index = (before >> kv.page_shift) + (item - a.b.item0[b]);
     const int t0 = index << kv.page_shift;
     const int lo = max(0, before - t0), hi = min(pt, before + fresh - t0);  // new tokens of the page
     const int page = page_of(kv, a.b.seq[b], index);
@@ -72,20 +82,31 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
             }
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float m = fabsf(v[u][k]);
-            top = fmaxf(top, m < __builtin_inff() ? m : 0.0f);  // infinities and NaN do not set the scale
-        }
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]));  // ignores NaN
     }
+    top = block_max(top, nt, 0);
+    const bool infinite = top == __builtin_inff();
+    if (infinite) {  // infinities do not set the scale, and saturate
+        top = 0.0f;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    __shared__ float s_top[4];
-    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
-    __syncthreads();
-    for (int w = 0; w < nt >> 6; ++w) top = fmaxf(top, s_top[w]);
+        for (int u = 0; u < CPT; ++u)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]) < __builtin_inff() ? fabsf(v[u][k]) : 0.0f);
+        top = block_max(top, nt, 1);
+    }
     const int e = max(exp_for(top), e0);
     const bool grown = lo > 0 && e > e0;
     const float down = pow2i(max(-126, e0 - e)), unit = pow2i(-e);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[u][k] *= unit;
+    if (infinite) {
+#pragma unroll
+        for (int u = 0; u < CPT; ++u)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[u][k] = sat448(v[u][k]);
+    }
 
 #pragma unroll
     for (int u = 0; u < CPT; ++u) {
@@ -99,7 +120,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
             if (t >= lo) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = to_e4m3(v[u][4 * k] * unit, v[u][4 * k + 1] * unit, v[u][4 * k + 2] * unit, v[u][4 * k + 3] * unit);
+                    w[k] = to_e4m3(v[u][4 * k], v[u][4 * k + 1], v[u][4 * k + 2], v[u][4 * k + 3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] = rescale_e4m3(w[k], down);
@@ -117,7 +138,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
             if (fresh_m != ~0u && lo == 0) w = block[c];  // tokens past the new ones keep what they hold
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t n = to_e4m3(v[u][k] * unit, v[u][4 + k] * unit, v[u][8 + k] * unit, v[u][12 + k] * unit);
+                const uint32_t n = to_e4m3(v[u][k], v[u][4 + k], v[u][8 + k], v[u][12 + k]);
                 uint32_t r = (w[k] & ~fresh_m) | (n & fresh_m);
                 if (grown && old_m) r = (r & ~old_m) | (rescale_e4m3(w[k], down) & old_m);
                 w[k] = r;
@@ -133,7 +154,7 @@ hipError_t append_as(const AppendArgs& a, hipStream_t s) {
     const int chunks = (1 << a.kv.page_shift) * a.kv.slabs * 4;  // 64 .. 2048, a multiple of 64
     const int nt = chunks < 256 ? chunks : 256;
     const int per = (chunks + nt - 1) / nt;
-    const dim3 grid(a.b.item0[a.b.n], a.kv.n_kv, 2);
+    const dim3 grid((unsigned)a.b.item0[a.b.n] * a.kv.n_kv, 2);  // heads first: neighbours read neighbouring parts of the same rows
     if (per <= 1) k_kv_append<T, 1><<<grid, nt, 0, s>>>(a);
     else if (per <= 2) k_kv_append<T, 2><<<grid, nt, 0, s>>>(a);
     else if (per <= 4) k_kv_append<T, 4><<<grid, nt, 0, s>>>(a);

@@ -72,10 +72,10 @@ __device__ inline void load_row(float* o, const _Float16* p) {
 // every finite value) saturates, NaN stays.
 __device__ inline float sat448(float x) { return x != x ? x : fminf(fmaxf(x, -448.0f), 448.0f); }
 
-// Four fp32 to four e4m3 bytes (round to nearest even).
+// Four fp32 of at most 448 (or NaN) to four e4m3 bytes (round to nearest even).
 __device__ inline uint32_t to_e4m3(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat448(a), sat448(b), 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(sat448(c), sat448(d), w, true);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     return (uint32_t)w;
 }
 

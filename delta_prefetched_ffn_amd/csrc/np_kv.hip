@@ -405,6 +405,8 @@ np_status append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t
         return f ? kv->pages_for((int64_t)b + f) - (b >> kv->page_shift) : 0;
     });
     if (a.b.item0[a.b.n] == 0) return NP_OK;
+    if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads >= (int64_t)1 << 31)
+        return fail(NP_EINVAL, "%d pages of %d heads in one call are too many", a.b.item0[a.b.n], D.n_kv_heads);
     DeviceGuard g(D.device);
     NP_HIP(launch_kv_append(a, dtype, s));
     return NP_OK;
@@ -449,7 +451,7 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.part = kv->part;
     a.arrived = kv->arrived;
     const int group = D.n_heads / D.n_kv_heads, n = (int)kv->b_seq.size();
-    if (rows * group > 1 << 28) return fail(NP_EINVAL, "%lld query rows in one call are too many", (long long)rows * group);
+    if (rows * D.n_heads > 1 << 30) return fail(NP_EINVAL, "%lld rows of %d heads in one call are too many", (long long)rows, D.n_heads);
     DeviceGuard g(D.device);
     // Sequences of many rows (prompts) go to the matrix units in large tiles, the others below.
     const auto many = [&](int i) { return (int64_t)kv->b_fresh[i] * group >= kManyRows; };
