@@ -9,6 +9,7 @@ no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from functools import lru_cache
@@ -287,6 +288,10 @@ class KVCache:
         self.n_layers, self.n_heads, self.n_kv_heads, self.head_dim = n_layers, n_heads, n_kv_heads, head_dim
         self.page_tokens, self.n_pages, self.max_seqs, self.max_pages = page_tokens, n_pages, max_seqs, max_pages
         self._keepalive = keepalive
+        # What the page calls hand back, kept: they run between decode steps.
+        self._pages = (ctypes.c_int32 * max_pages)()
+        self._n = ctypes.c_int32(0)
+        self._n_ref, self._pages_at = ctypes.byref(self._n), ctypes.addressof(self._pages)
 
     def close(self) -> None:
         if self.h:
@@ -340,8 +345,13 @@ class KVCache:
 
     def adopt(self, seq: int, pages, n_tokens: int, stream: int = 0) -> None:
         """The empty sequence seq becomes these pages of the pool, holding n_tokens tokens (nothing is enqueued)."""
-        p = np.ascontiguousarray(pages, dtype=np.int32)
-        _check(lib().np_kv_adopt(self.h, seq, p.ctypes.data, p.size, n_tokens))
+        if isinstance(pages, list):
+            p = array.array("i", pages)
+            at, n = p.buffer_info()
+        else:
+            p = np.ascontiguousarray(pages, dtype=np.int32)
+            at, n = p.ctypes.data, p.size
+        _check(lib().np_kv_adopt(self.h, seq, at, n, n_tokens))
 
     def evict(self, seq: int, window: int, sinks: int = 0, stream: int = 0) -> int:
         """Drops the pages that no later query of this window sees; how many (nothing is enqueued)."""
@@ -356,14 +366,12 @@ class KVCache:
         return n.value
 
     def pages(self, seq: int) -> np.ndarray:
-        out = np.empty(self.max_pages, dtype=np.int32)
-        n = ctypes.c_int32(0)
-        _check(lib().np_kv_read_pages(self.h, seq, out.ctypes.data, out.size, ctypes.byref(n), None))
-        return out[: n.value].copy()
+        _check(lib().np_kv_read_pages(self.h, seq, self._pages_at, self.max_pages, self._n_ref, None))
+        return np.frombuffer(self._pages, np.int32, self._n.value).copy() if self._n.value else np.empty(0, np.int32)
 
     def tokens(self, seq: int) -> int:
-        n, t = ctypes.c_int32(0), ctypes.c_int32(0)
-        _check(lib().np_kv_read_pages(self.h, seq, None, 0, ctypes.byref(n), ctypes.byref(t)))
+        t = ctypes.c_int32(0)
+        _check(lib().np_kv_read_pages(self.h, seq, None, 0, self._n_ref, ctypes.byref(t)))
         return t.value
 
     def read_tokens(self, layer: int, seq: int, first: int = 0, n: int | None = None) -> tuple[np.ndarray, np.ndarray]:
