@@ -531,10 +531,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     }
 }
 
-// Waves of a workgroup for many rows: 8, two to a SIMD at 256 registers, where q, O and the scores fit;
-// 4 at 512 registers for fp32 (three summands of q) and the longest heads.
-template <typename T, int NS>
-constexpr int kTileWaves = NS * (sizeof(T) == 4 ? 3 : 1) <= 3 ? 8 : 4;
+// Waves of a workgroup for many rows: 8, two to a SIMD at 256 registers, where q, O and the scores fit
+// (nearly, at 192 values a head); 4 at 512 registers for longer heads.
+template <int NS>
+constexpr int kTileWaves = NS <= 3 ? 8 : 4;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
@@ -946,7 +946,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 
 template <typename T, int NS>
 hipError_t tile_as(const AttnArgs& a, hipStream_t s) {
-    constexpr int W = kTileWaves<T, NS>;
+    constexpr int W = kTileWaves<NS>;
     constexpr int kLds = 4 * 64 * NS * 64 * 2;  // two steps of K and V, 16 bits a value
     static const hipError_t ready =
         hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tile<T, NS, W>), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
@@ -968,26 +968,27 @@ hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, int NS>
+hipError_t tile_16(const AttnArgs& a, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) return tile_as<T, NS>(a, s);
+    return hipErrorInvalidValue;  // attn_tile_rows() gives fp32 no tiles here
+}
+
 template <typename T>
 hipError_t attn_as(const AttnArgs& a, hipStream_t s) {
     switch (a.kv.slabs) {
         case 1: return a.part ? rows_as<T, 1>(a, s) : tile_as<T, 1>(a, s);
-        case 2: return a.part ? rows_as<T, 2>(a, s) : tile_as<T, 2>(a, s);
-        case 3: return a.part ? rows_as<T, 3>(a, s) : tile_as<T, 3>(a, s);
-        default: return a.part ? rows_as<T, 4>(a, s) : tile_as<T, 4>(a, s);
+        case 2: return a.part ? rows_as<T, 2>(a, s) : tile_16<T, 2>(a, s);
+        case 3: return a.part ? rows_as<T, 3>(a, s) : tile_16<T, 3>(a, s);
+        default: return a.part ? rows_as<T, 4>(a, s) : tile_16<T, 4>(a, s);
     }
 }
 
 }  // namespace
 
 int attn_tile_rows(int dtype, int slabs) {
-    const bool f32 = dtype == kF32;
-    switch (slabs) {
-        case 1: return 32 * (f32 ? kTileWaves<float, 1> : kTileWaves<__bf16, 1>);
-        case 2: return 32 * (f32 ? kTileWaves<float, 2> : kTileWaves<__bf16, 2>);
-        case 3: return 32 * (f32 ? kTileWaves<float, 3> : kTileWaves<__bf16, 3>);
-        default: return 32 * (f32 ? kTileWaves<float, 4> : kTileWaves<__bf16, 4>);
-    }
+    if (dtype == kF32) return slabs == 1 ? 32 * kTileWaves<1> : 0;
+    return 32 * (slabs == 1 ? kTileWaves<1> : slabs == 2 ? kTileWaves<2> : slabs == 3 ? kTileWaves<3> : kTileWaves<4>);
 }
 
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s) {

@@ -107,7 +107,7 @@ hipError_t launch_kv_append(const AppendArgs& a, int dtype, hipStream_t s);
 hipError_t launch_kv_table(const TableArgs& a, hipStream_t s);
 hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
 // part set: few rows a sequence (items are row tiles of kRowTile rows, split); part nullptr: many
-// rows (items are attn_tile_rows() rows each).
+// rows (items are attn_tile_rows() rows each; 0: there is no such kernel).
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s);
 int attn_tile_rows(int dtype, int slabs);
 

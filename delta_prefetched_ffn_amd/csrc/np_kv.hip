@@ -27,8 +27,24 @@ namespace {
 constexpr int kCus = 256;
 constexpr int kFewPieces = 16;
 
-// Rows (query tokens x heads of a group) of a sequence from which its attention runs in large tiles.
+// Sequences of many rows (query tokens x heads of a group) may run in large tiles on the matrix units
+// (k_attn_tile) instead of 16-row tiles (k_attn_rows). The first is bound by its steps of 64 tokens
+// (the longest workgroup's, or all of them over the compute units), the second by the bytes and
+// products of its row tiles plus a start and a join of each, and it splits the key axis where there
+// are few. Microseconds, measured at 1 Ki .. 4 Ki tokens x 32 heads and at 32 .. 512 rows over 0 .. 20 Ki
+// tokens: a tile's step, 256 rows x 64 tokens in row tiles, a row tile. E.g. head_dim 128, 16 bits: 4 Ki
+// tokens x 32 heads 167 against 499 us; 512 rows x 8 heads over 20 Ki tokens 606 against 107 us. For
+// fp32 the tiles pay up to 64 values a head (4 Ki tokens x 32 heads: 234 against 344 us); beyond, q's
+// three summands leave a wave too few registers.
 constexpr int kManyRows = 128;
+struct TileCost {
+    double step, unit;
+};
+constexpr double kRowTileCost = 0.018;
+TileCost tile_cost(int dtype, int slabs) {
+    static constexpr TileCost k16[4] = {{1.9, 0.007}, {2.2, 0.020}, {4.3, 0.027}, {4.8, 0.032}};
+    return dtype != NP_F32 ? k16[slabs - 1] : TileCost{3.4, 0.0113};
+}
 
 struct Seq {
     std::vector<int32_t> pages;  // -1: dropped
@@ -453,9 +469,23 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     const int group = D.n_heads / D.n_kv_heads, n = (int)kv->b_seq.size();
     if (rows * D.n_heads > 1 << 30) return fail(NP_EINVAL, "%lld rows of %d heads in one call are too many", (long long)rows, D.n_heads);
     DeviceGuard g(D.device);
-    // Sequences of many rows (prompts) go to the matrix units in large tiles, the others below.
-    const auto many = [&](int i) { return (int64_t)kv->b_fresh[i] * group >= kManyRows; };
     const int tile_rows = attn_tile_rows(dtype, kv->slabs);
+    const auto large = [&](int i) { return tile_rows > 0 && (int64_t)kv->b_fresh[i] * group >= kManyRows; };
+    double longest = 0, steps = 0, units = 0, row_tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!large(i)) continue;
+        // Steps of the first and of the last tile; those between lie between.
+        const double f = kv->b_fresh[i], all_rows = f * group, seen = window ? (double)window + sinks + tile_rows / group : 1e18;
+        const double last = std::min(kv->b_before[i] + f, seen) / 64 + 1;
+        const double first = std::min(kv->b_before[i] + std::min(f, (double)tile_rows / group), seen) / 64 + 1;
+        longest = std::max(longest, last);
+        steps += std::ceil(all_rows / tile_rows) * D.n_kv_heads * (first + last) / 2;
+        units += all_rows / 256 * D.n_kv_heads * (first + last) / 2;
+        row_tiles += std::ceil(all_rows / kRowTile) * D.n_kv_heads;
+    }
+    const TileCost cost = tile_cost(dtype, kv->slabs);
+    const bool pays = cost.step * std::max(longest, steps / kCus) < cost.unit * units + kRowTileCost * row_tiles;
+    const auto many = [&](int i) { return pays && large(i); };
     fill_batch(kv, a.b, [&](int i) { return many(i) ? (kv->b_fresh[i] * group + tile_rows - 1) / tile_rows : 0; });
     if (a.b.item0[n] > 0) {
         a.part = nullptr;
