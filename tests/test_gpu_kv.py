@@ -448,3 +448,56 @@ def test_refusals_with_a_device():
     e.append(e.rand(3, 2, "f32"), e.rand(3, 2, "f32"), "f32")   # still usable
     e.check_tokens([0])
     e.attend("f32")
+
+
+# ------------------------------------------------------------------------------------------------- many rows, many heads
+# Enough heads and rows that prompts run in large tiles (the tests above stay below: few workgroups).
+
+TILES = [("bf16", 128), ("f16", 128), ("bf16", 64), ("f32", 64), ("f16", 80), ("bf16", 40), ("bf16", 192), ("f16", 256)]
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+@pytest.mark.parametrize("group,new,before,window,sinks", [(1, 300, 0, 0, 0), (2, 170, 77, 0, 0), (1, 290, 0, 50, 3), (1, 257, 130, 64, 70), (3, 129, 5, 1, 0)])
+def test_prompt_tiles(dtype, hd, group, new, before, window, sinks):
+    e = Env(heads=64 * group, kv=64, hd=hd, page=32, pages=40, seqs=3, seed=new)
+    if before:
+        e.step([0, 1], [before, before // 3], dtype)
+    e.step([0, 2, 1], [new, 0, 1], dtype)     # a prompt beside a single token: both kernels in one call
+    e.attend(dtype, window=window, sinks=sinks, layout="fused")
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+def test_prompt_tiles_nan_scales_and_dropped_pages(dtype, hd):
+    # Value blocks of very different size, NaN values that only some rows see, NaN codes in every unwritten byte.
+    e = Env(heads=64, kv=64, hd=hd, page=16, pages=40, seqs=2)
+    rows = 260
+    e.extend([0], [rows])
+    mags = np.repeat([1.0, 2.0 ** 6, 2.0 ** -9, 2.0 ** 8, 1e-3, 0.0, 5.0, 2.0 ** -14, 1.0, 1.0, 2.0 ** -20, 30.0, 1.0, 1.0, 1.0, 1.0, 1.0], 16)[:rows]
+    k = e.rng.standard_normal((rows, 64, hd)) * 0.3
+    k[:, :, 0] = np.where(mags > 10, -40, 3)[:, None]
+    v = e.rng.standard_normal((rows, 64, hd)) * mags[:, None, None]
+    v[40, ::7, 5], v[201, 3, hd - 1], k[100, 9, 1] = np.nan, np.nan, np.nan
+    v[150, 11, 2] = np.inf
+    kt, vt = (torch.from_numpy(x.astype(np.float32)) for x in (k, v))
+    e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    q = e.rng.standard_normal((rows, 64, hd)).astype(np.float32) * 0.3
+    q[:, :, 0] = 1.0
+    qt = torch.from_numpy(q).to(tdt(dtype))
+    e.attend(dtype, q=(qt, qt.double().numpy()), window=23, sinks=2, scale=1.0)
+    e.attend(dtype, q=(qt, qt.double().numpy()), scale=1.0)
+    # restored without its first pages
+    e.kv.free(0)
+    e.kv.adopt(0, [-1] * 5 + list(range(20)), 80, e.stream())
+    e.ref[0][0] = R.RefSeq(64, hd, 16)
+    e.ref[0][0].codes, e.ref[0][0].exps = np.full((80, 2, 64, hd), np.nan), np.zeros((5, 2, 64), dtype=np.int64)
+    e.step([0], [250], "f32")
+    e.attend(dtype, held={0: np.arange(1000) >= 80}, window=100, sinks=10)
+    e.attend(dtype, held={0: np.arange(1000) >= 80}, layout="heads")
+
+
+def test_prompt_tiles_are_the_same_from_run_to_run():
+    e = Env(heads=64, kv=64, hd=128, page=64, pages=12, seqs=1)
+    e.step([0], [300], "bf16")
+    q = e.rand(300, 64, "bf16")
+    runs = [e.attend("bf16", q=q, lse=False).clone() for _ in range(3)]
+    assert all(torch.equal(r, runs[0]) for r in runs)
