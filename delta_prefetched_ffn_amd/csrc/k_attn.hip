@@ -14,6 +14,7 @@
 // group, and the V tile's dword i of the lane's chunk holds exactly those four tokens of value
 // 4 r + i. So neither P nor V crosses lanes, and a lane's results are 16 consecutive values.
 #include <algorithm>
+#include <atomic>
 
 #include "kv_device.hpp"
 
@@ -542,13 +543,21 @@ __device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amd
 
 // Many rows: one workgroup of W waves per (32 W rows, kv head), 32 rows a wave, 64 tokens a step.
 //
-// Bound by the matrix units, with the exponentials next (per 64 tokens a wave has 32 products of
-// 32x32x16, 1024 clocks, and 32 exponentials a lane, 512). So what is not theirs is kept off the
-// waves: codes are widened to 16 bits once per workgroup, by the wave that moved them into LDS (every
-// wave reads them all, 1 KiB of consecutive operands at a time), with V's scale folded into that
-// conversion; the products are transposed as above, so P needs no trip through LDS; and the next
-// step's codes are asked for before this step's products. The workgroups of one kv head have numbers
-// that leave them on one die (its cache then holds the head's K and V), the longest rows first.
+// Per 64 tokens a wave has 32 products of 32x32x16 (33 clocks each) and 32 exponentials a lane. Codes
+// are widened to 16 bits once per workgroup, by the wave that moved them into LDS (every wave reads
+// them all, 1 KiB of consecutive operands at a time), with V's scale folded into that conversion; the
+// products are transposed as above, so P needs no trip through LDS. The two waves of a SIMD are half a
+// step apart: one's products run beside the other's softmax and moves. Neighbouring workgroups are of
+// different kv heads, so a head's row tiles run on one die (8 divides most head counts), whose cache
+// then holds its K and V; the longest rows come first.
+//
+// Measured at head_dim 128: a causal prompt of 4 Ki tokens x 32 heads 165 us, 833 TFLOP/s (a large
+// library product reaches 1,354); 8,191 tokens x 32 over 8 heads with a window of 4 Ki 464 us, 888
+// TFLOP/s. A step takes about 4,900 clocks where its products need 2,112: a wave alone reads LDS at 33
+// bytes a clock, one operand per product's time (62 clocks for both; 33 with two waves), and the vector
+// work (masks and maxima 600, exponentials 610, widening 800 for K and 1,360 for V) of two waves
+// is longer than their products. Without the half-step distance 175 us; with codes moved by all waves at
+// the end of a step 187 us.
 //
 // Operand slots: S^T lane (half, row) holds tokens 8 (i / 4) + 4 half + i % 4, i < 16, of a 32-token
 // block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
@@ -944,14 +953,17 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             !seen ? -__builtin_inff() : m == -__builtin_inff() ? __builtin_nanf("") : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
+// LDS of k_attn_rows per row of its tile (the join), and of k_attn_tile (two steps of K and V, 16 bits
+// a value).
+template <int NS>
+constexpr size_t kRowLds = (size_t)kAttnWaves * (2 + NS * 64 + 4) * sizeof(float);
+template <int NS>
+constexpr int kTileLds = 4 * 64 * NS * 64 * 2;
+
 template <typename T, int NS>
 hipError_t tile_as(const AttnArgs& a, hipStream_t s) {
     constexpr int W = kTileWaves<NS>;
-    constexpr int kLds = 4 * 64 * NS * 64 * 2;  // two steps of K and V, 16 bits a value
-    static const hipError_t ready =
-        hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tile<T, NS, W>), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (ready != hipSuccess) return ready;
-    k_attn_tile<T, NS, W><<<(unsigned)a.b.item0[a.b.n] * a.kv.n_kv, 64 * W, kLds, s>>>(a);
+    k_attn_tile<T, NS, W><<<(unsigned)a.b.item0[a.b.n] * a.kv.n_kv, 64 * W, kTileLds<NS>, s>>>(a);
     return hipGetLastError();
 }
 
@@ -959,11 +971,7 @@ template <typename T, int NS>
 hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
     constexpr int W = kAttnWaves;
     const dim3 grid(a.b.item0[a.b.n], a.kv.n_kv);
-    constexpr size_t kRowLds = (size_t)W * (2 + NS * 64 + 4) * sizeof(float);
-    const size_t lds = std::max(kRowLds * a.row_cap, sizeof(bf16x8) * 64 * 2 * NS * Kind<T>::kQ);
-    static const hipError_t ready = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_rows<T, NS, W>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kRowLds * kRows));
-    if (ready != hipSuccess) return ready;
+    const size_t lds = std::max(kRowLds<NS> * a.row_cap, sizeof(bf16x8) * 64 * 2 * NS * Kind<T>::kQ);
     k_attn_rows<T, NS, W><<<grid, 64 * W, lds, s>>>(a);
     return hipGetLastError();
 }
@@ -984,11 +992,40 @@ hipError_t attn_as(const AttnArgs& a, hipStream_t s) {
     }
 }
 
+template <typename T, int NS>
+hipError_t prepare() {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_rows<T, NS, kAttnWaves>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kRowLds<NS> * kRows));
+    if constexpr (sizeof(T) == 2 || NS == 1) {
+        if (e == hipSuccess)
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_attn_tile<T, NS, kTileWaves<NS>>),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds<NS>);
+    }
+    return e;
+}
+template <typename T>
+hipError_t prepare_all() {
+    for (hipError_t e : {prepare<T, 1>(), prepare<T, 2>(), prepare<T, 3>(), prepare<T, 4>()})
+        if (e != hipSuccess) return e;
+    return hipSuccess;
+}
+
 }  // namespace
 
 int attn_tile_rows(int dtype, int slabs) {
     if (dtype == kF32) return slabs == 1 ? 32 * kTileWaves<1> : 0;
     return 32 * (slabs == 1 ? kTileWaves<1> : slabs == 2 ? kTileWaves<2> : slabs == 3 ? kTileWaves<3> : kTileWaves<4>);
+}
+
+hipError_t attn_prepare() {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    for (hipError_t x : {prepare_all<float>(), prepare_all<__bf16>(), prepare_all<_Float16>()})
+        if (x != hipSuccess) e = x;
+    if (e == hipSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
 }
 
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s) {

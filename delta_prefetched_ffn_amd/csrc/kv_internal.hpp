@@ -110,5 +110,7 @@ hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
 // rows (items are attn_tile_rows() rows each; 0: there is no such kernel).
 hipError_t launch_attn(const AttnArgs& a, int dtype, hipStream_t s);
 int attn_tile_rows(int dtype, int slabs);
+// Lets the attention kernels of the current device use the LDS they ask for (above 64 KiB).
+hipError_t attn_prepare();
 
 }  // namespace np

@@ -327,6 +327,7 @@ np_status create(const np_kv_desc* desc, np_kv** out) {
             (void)hipGetLastError();
             return fail(NP_ENOMEM, "cannot allocate the page table (%zu bytes) and scratch (%zu bytes)", table_bytes, part_bytes);
         }
+        NP_HIP(attn_prepare());
         NP_HIP(hipMemset(kv->table, 0xff, table_bytes));
         NP_HIP(hipMemset(kv->arrived, 0, kMaxPartials * sizeof(uint32_t)));
         NP_HIP(hipDeviceSynchronize());
@@ -461,6 +462,9 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.o_row = S[2];
     a.o_head = S[3];
     a.scale2 = scale * 1.44269504088896341f;
+    // Beyond the longest sequence both mean "all"; the kernels' differences then stay within 32 bits.
+    window = std::min(window, 2 * kMaxSeqTokens);
+    sinks = std::min(sinks, 2 * kMaxSeqTokens);
     a.window = window;
     a.sinks = sinks;
     a.layer = layer;

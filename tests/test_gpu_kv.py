@@ -501,3 +501,14 @@ def test_prompt_tiles_are_the_same_from_run_to_run():
     q = e.rand(300, 64, "bf16")
     runs = [e.attend("bf16", q=q, lse=False).clone() for _ in range(3)]
     assert all(torch.equal(r, runs[0]) for r in runs)
+
+
+@pytest.mark.parametrize("kv", [2, 64])
+def test_windows_and_first_tokens_up_to_the_largest_number(kv):
+    e = Env(heads=kv, kv=kv, hd=64, page=16, pages=24, seqs=1)
+    e.step([0], [20], "bf16")
+    e.step([0], [280], "bf16")
+    q = e.rand(280, kv, "bf16")
+    full = e.attend("bf16", q=q, lse=False).clone()
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 28, 1), (7, 2 ** 31 - 1), (300, 0)):
+        assert torch.equal(e.attend("bf16", q=q, window=window, sinks=sinks, lse=False), full), (window, sinks)
