@@ -292,6 +292,8 @@ class KVCache:
         self._pages = (ctypes.c_int32 * max_pages)()
         self._n = ctypes.c_int32(0)
         self._n_ref, self._pages_at = ctypes.byref(self._n), ctypes.addressof(self._pages)
+        # The calls of every layer and token: their functions and the strides in use, looked up once.
+        self._append, self._attend, self._strides = lib().np_kv_append, lib().np_kv_attend, {None: None}
 
     def close(self) -> None:
         if self.h:
@@ -318,18 +320,24 @@ class KVCache:
 
     def append(self, layer: int, k_ptr: int, v_ptr: int, dtype: str, strides=None, stream: int = 0) -> None:
         """Stores the current tokens' k, v [rows][n_kv_heads][head_dim]; strides (elements): k row, k head, v row, v head."""
-        st = None if strides is None else (ctypes.c_int64 * 4)(*strides)
-        rc = lib().np_kv_append(self.h, layer, k_ptr, v_ptr, DTYPES[dtype], st, stream or None)
+        rc = self._append(self.h, layer, k_ptr, v_ptr, DTYPES[dtype], self._stride_array(strides), stream or None)
         if rc:
             _check(rc)
+
+    def _stride_array(self, strides):
+        try:
+            return self._strides[strides]
+        except (KeyError, TypeError):   # new ones, or a list
+            if len(self._strides) > 64:
+                self._strides = {None: None}
+            return self._strides.setdefault(tuple(strides), (ctypes.c_int64 * 4)(*strides))
 
     def attend(self, layer: int, q_ptr: int, out_ptr: int, dtype: str, strides=None, *, scale: float, window: int = 0,
                sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
         """Attention of the current tokens: q, out [rows][n_heads][head_dim]; strides (elements): q row, q head, out row,
         out head; window 0: every earlier token, else the last `window` and the first `sinks`."""
-        st = None if strides is None else (ctypes.c_int64 * 4)(*strides)
-        rc = lib().np_kv_attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], st, scale, window, sinks,
-                                stream or None)
+        rc = self._attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
+                          window, sinks, stream or None)
         if rc:
             _check(rc)
 

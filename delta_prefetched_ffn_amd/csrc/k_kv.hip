@@ -36,7 +36,7 @@ __device__ inline float block_max(float x, int threads, int use) {
 // end on a multiple of four) are merged in registers. Bound by memory: 4,097 tokens x 32 heads of bf16
 // 28.5 us (3.5 TB/s; a large copy reaches 4.85), five prompts of fp32 31.7 us (4.25 TB/s). With pages
 // first in the grid instead of heads 28.9 and 33.1 us; saturating every value 29.4 and 33.3 us. One token:
-// 8.6 us a call, of which the kernel is 5: page, row, maximum over the block, store.
+// 8.1 us a call, of which the kernel is 5: page, row, maximum over the block, store.
 template <typename T, int CPT>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     const KvView& kv = a.kv;
