@@ -713,7 +713,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                 int side, g, c;
                 tile_at(j, side, g, c);
                 if (side == 0) continue;
-                const int e = __builtin_amdgcn_readlane(my_ev, from + g), u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+                const int u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
+                // A group that is not held has page 0's codes, whose exponent the unit knows nothing of: they are taken
+                // at the unit. Its weights are 0, but codes that overflow would be infinities, and 0 times those NaN.
+                const int e = holds >> g & 1 ? __builtin_amdgcn_readlane(my_ev, from + g) : u;
                 const int quad = lane >> 4, r = lane & 15;
                 uint32_t bad = 0;
 #pragma unroll

@@ -512,3 +512,52 @@ def test_windows_and_first_tokens_up_to_the_largest_number(kv):
     full = e.attend("bf16", q=q, lse=False).clone()
     for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 28, 1), (7, 2 ** 31 - 1), (300, 0)):
         assert torch.equal(e.attend("bf16", q=q, window=window, sinks=sinks, lse=False), full), (window, sinks)
+
+
+# ---------------------------------------------------------------------------------------- pages that are not the sequence's
+# Where a sequence holds no page (dropped, or past its last token) the kernels have page 0's address at hand. Nothing of it
+# may matter: here it belongs to nobody or to another sequence, with finite codes at a scale far from the rows' own.
+
+def page_zero_of_nobody(e):
+    """Page 0 as an unwritten pool may hold it: the largest finite codes at the largest exponent, in no sequence."""
+    assert e.layers == 1
+    e.codes[:e.codes.numel() // e.kv.n_pages] = 0x7E
+    e.exps[:2 * e.nkv] = 120
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+@pytest.mark.parametrize("new", [260, 129])
+def test_prompt_tiles_end_inside_a_step(dtype, hd, new):
+    e = Env(heads=64, kv=64, hd=hd, page=16, pages=24, seqs=2, seed=new)
+    page_zero_of_nobody(e)
+    e.kv.adopt(0, list(range(1, 20)), 0, e.stream())
+    e.step([0], [new], dtype)
+    e.attend(dtype)
+    e.attend(dtype, window=100, sinks=3)
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+def test_prompt_tiles_with_values_of_zero(dtype, hd):
+    # The last page's values are zero, and one head's everywhere: the unit of the sums goes far below page 0's scale.
+    e = Env(heads=64, kv=64, hd=hd, page=16, pages=24, seqs=2)
+    e.step([1], [16], "f32")             # another sequence's ordinary tokens in page 0
+    assert e.kv.pages(1).tolist() == [0]
+    e.extend([0], [260])
+    k, v = (e.rng.standard_normal((260, 64, hd)).astype(np.float32) for _ in range(2))
+    v[256:] = 0
+    v[:, 5] = 0
+    kt, vt = torch.from_numpy(k), torch.from_numpy(v)
+    e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    e.attend(dtype)
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+def test_prompt_tiles_behind_dropped_pages(dtype, hd):
+    e = Env(heads=64, kv=64, hd=hd, page=16, pages=32, seqs=1)
+    page_zero_of_nobody(e)
+    e.kv.adopt(0, [-1] * 9 + list(range(1, 23)), 144, e.stream())
+    e.ref[0][0].codes, e.ref[0][0].exps = np.full((144, 2, 64, hd), np.nan), np.zeros((9, 2, 64), dtype=np.int64)
+    e.step([0], [330], "f32")
+    held = {0: np.arange(1000) >= 144}
+    e.attend(dtype, held=held)
+    e.attend(dtype, held=held, window=300, sinks=70)
