@@ -402,7 +402,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
             clean = !__any(bad != 0);
         }
-        if (clean && near) {
+        if (!held[0] && !held[1]) {
+            // Nothing of the piece counts, and what was read is page 0's: its exponents must not move the unit.
+        } else if (clean && near) {
             fit_unit(e0, e1);
             const float f0 = pow2i(max(-126, e0 - unit)), f1 = pow2i(max(-126, e1 - unit));
             P8 pv[Kd::kP];

@@ -561,3 +561,23 @@ def test_prompt_tiles_behind_dropped_pages(dtype, hd):
     held = {0: np.arange(1000) >= 144}
     e.attend(dtype, held=held)
     e.attend(dtype, held=held, window=300, sinks=70)
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("f16", 128), ("f32", 64), ("f32", 128), ("bf16", 192), ("f16", 256)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_tokens_behind_dropped_pages(dtype, hd, page):
+    # Whole pieces of 32 tokens are not held, and no window hides them.
+    e = Env(heads=4, kv=2, hd=hd, page=page, pages=32, seqs=1)
+    page_zero_of_nobody(e)
+    e.kv.adopt(0, [-1] * 9 + list(range(1, 20)), 9 * page, e.stream())
+    e.ref[0][0].codes, e.ref[0][0].exps = np.full((9 * page, 2, 2, hd), np.nan), np.zeros((9, 2, 2), dtype=np.int64)
+    held = {0: np.arange(2000) >= 9 * page}
+    for new in (1, 3, 40):
+        e.step([0], [new], dtype)
+        e.attend(dtype, held=held)
+        e.attend(dtype, held=held, window=8 * page, sinks=page + 3)
+    # and pages dropped behind a window that the next call does not use
+    gone = e.kv.evict(0, 16, 0, e.stream())
+    held = {0: np.arange(2000) >= (9 + gone) * page}
+    e.step([0], [1], dtype)
+    e.attend(dtype, held=held)
