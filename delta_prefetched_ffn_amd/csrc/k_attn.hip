@@ -141,7 +141,7 @@ __device__ inline void store_row(const AttnArgs& a, int row0, int group, int h, 
     __builtin_memcpy(__builtin_assume_aligned(out, 4 * sizeof(T)), y, sizeof y);
     if (a.lse && d == 0)
         a.lse[(int64_t)(row0 + t) * a.kv.n_heads + head] =
-            none ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(ll)) * 0.69314718055994531f;
+            none ? -__builtin_inff() : ll == 0.0f ? __builtin_nanf("") : (mm + __builtin_amdgcn_logf(ll)) * 0.69314718055994531f;
 }
 
 // Partial results pass between dies: stores and loads that bypass the die's own cache.
@@ -451,7 +451,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     seen = (__ballot(seen) >> col & 0x0001000100010001ull) != 0;
-    if (seen && m == -__builtin_inff()) l = __builtin_nanf("");  // every visible score is -inf: 0 / 0
+    // Every score this wave saw is -inf. Beside finite scores they weigh 0; if the whole row's are, it is 0 / 0. The
+    // lowest finite maximum joins as just that.
+    if (seen && m == -__builtin_inff()) m = -__FLT_MAX__;
     constexpr int D = NS * 64, DS = D + 4;
     __syncthreads();  // the q tile is done with
     const int cap = a.row_cap;

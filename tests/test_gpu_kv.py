@@ -581,3 +581,40 @@ def test_tokens_behind_dropped_pages(dtype, hd, page):
     held = {0: np.arange(2000) >= (9 + gone) * page}
     e.step([0], [1], dtype)
     e.attend(dtype, held=held)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,new", [(1, 1), (1, 20), (64, 400)])
+def test_scores_of_minus_infinity_beside_finite_ones(dtype, heads, new):
+    # q . k of most tokens overflows to -inf: their weight is 0, and the 32 tokens with finite scores make the row. The
+    # reference leaves the others out (in 64 bits they weigh exp(-1e40) = 0).
+    e = Env(heads=heads, kv=heads, hd=64, page=16, pages=48, seqs=1)
+    total = 500
+    k, v = (e.rng.standard_normal((total, heads, 64)).astype(np.float32) for _ in range(2))
+    finite = (np.arange(2000) >= 96) & (np.arange(2000) < 128)
+    k[:, :, 0] = np.where(finite[:total], 0.0, -224.0)[:, None]
+    for lo, hi in ((0, total - new), (total - new, total)):
+        e.extend([0], [hi - lo])
+        kt, vt = torch.from_numpy(k[lo:hi]), torch.from_numpy(v[lo:hi])
+        e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    q = e.rng.standard_normal((new, heads, 64)).astype(np.float32)
+    q[:, :, 0] = 2.0 ** 126
+    qt = torch.from_numpy(q).to(tdt(dtype))
+    e.attend(dtype, q=(qt, qt.double().numpy()), held={0: finite}, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,new", [(1, 1), (64, 300)])
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(dtype, heads, new):
+    e = Env(heads=heads, kv=heads, hd=64, page=16, pages=48, seqs=1)
+    e.extend([0], [100])
+    k = np.abs(e.rng.standard_normal((300, heads, 64))).astype(np.float32) + 1
+    kt = torch.from_numpy(k[:100])
+    e.append((kt, kt.double().numpy()), e.rand(100, heads, "f32"), "f32")
+    e.extend([0], [new])
+    kt = torch.from_numpy(k[:new])
+    e.append((kt, kt.double().numpy()), e.rand(new, heads, "f32"), "f32")
+    q, _ = e.rand(new, heads, dtype)
+    q[0, 0, 3] = -float("inf")
+    out = e.attend(dtype, q=(q, q.double().numpy()))
+    assert bool(out[0, 0].isnan().all()) and int(out.isnan().sum()) == 64
