@@ -102,6 +102,7 @@ constexpr float kLazy = 8.0f;
 // 448 * 2^7 < 65504), so widening is exact; a block further off moves the unit. It moves down by at
 // most kDrop from the largest exponent met (O would overflow fp32): blocks below that vanish.
 constexpr int kFar = 5, kNear = 7, kDrop = 40;
+constexpr int kNoUnit = -1000;  // below every exponent: no block met so far
 
 // The tokens a row tile reads, as 32-token pieces: the first tokens' pieces, then those of
 // [first, end).
@@ -235,8 +236,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         for (int i = 0; i < 4; ++i) o[c][i] = f32x4{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0.0f;  // l: this lane's tokens only, joined at the end
     bool seen = false;
-    int unit = 0, top = 0;  // o is in units of 2^unit
-    bool begun = false;
+    int unit = kNoUnit, top = kNoUnit;  // o is in units of 2^unit
 
     // K of the next piece is asked for once this one's products have read K, V once they have read V:
     // a wave always has loads in flight and holds one piece only. The last piece's "next" loads read
@@ -361,10 +361,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         // one unit (the other group's codes are then out of the product: they would overflow).
         const auto fit_unit = [&](int ea, int eb) {
             const int lo_e = min(ea, eb), hi_e = max(ea, eb);
-            if (!begun) {
-                unit = top = min(hi_e, lo_e + kFar);
-                begun = true;
-            }
             top = max(top, hi_e);
             const int to = max(min(hi_e, lo_e + kFar), top - kDrop);
             if (to != unit && (hi_e > unit + kNear || lo_e < unit - kFar)) {
@@ -376,7 +372,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                 unit = to;
             }
         };
-        const int e0 = held[0] ? ev[0] : ev[1], e1 = held[1] ? ev[1] : ev[0];
+        // Exponents of groups that are not held are page 0's: they must not move the unit.
+        const int e0 = held[0] ? ev[0] : held[1] ? ev[1] : unit, e1 = held[1] ? ev[1] : e0;
         const bool near = e0 - e1 <= kNear + kFar && e1 - e0 <= kNear + kFar;
         // NaN codes of tokens that a row does not see must not reach it: 0 * NaN is NaN. Tokens that no row
         // of the tile sees (often bytes never written) are cleared here; the path below keeps real NaN
@@ -402,9 +399,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
             }
             clean = !__any(bad != 0);
         }
-        if (!held[0] && !held[1]) {
-            // Nothing of the piece counts, and what was read is page 0's: its exponents must not move the unit.
-        } else if (clean && near) {
+        if (clean && near) {
             fit_unit(e0, e1);
             const float f0 = pow2i(max(-126, e0 - unit)), f1 = pow2i(max(-126, e1 - unit));
             P8 pv[Kd::kP];
