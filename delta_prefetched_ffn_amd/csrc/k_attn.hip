@@ -24,26 +24,30 @@ namespace {
 // What differs by the type of q and out. K codes become Op values (exact), q is held as kTerms
 // summands of that type: bf16 and fp16 as they are, fp32 as three bf16 summands (8 + 8 + 8 bits:
 // exact). P is rounded to fp16 for 16-bit outputs (2^-11 of the value, below the output's own
-// rounding for bf16 and equal to it for fp16) and to three bf16 summands (2^-24) for fp32.
+// rounding for bf16 and equal to it for fp16) and to three bf16 summands (2^-24) for fp32. In fp16 it
+// is held times 2^kLift, so that it is between 2^7 and 2^15 at the row's maximum: weights from 2^-21 of
+// that on are rounded by 2^-11 of themselves, smaller ones by at most 2^-32 of the largest (fp16's last
+// places). N tokens are then off by at most N * 2^-32 of the row's sum together, half a step of fp16 at
+// 2 Mi tokens; without the factor it was at 16 Ki.
 template <typename T>
 struct Kind;
 template <>
 struct Kind<__bf16> {
     typedef __bf16 Q;
     typedef _Float16 P;
-    static constexpr int kQ = 1, kP = 1;
+    static constexpr int kQ = 1, kP = 1, kLift = 7;
 };
 template <>
 struct Kind<_Float16> {
     typedef _Float16 Q;
     typedef _Float16 P;
-    static constexpr int kQ = 1, kP = 1;
+    static constexpr int kQ = 1, kP = 1, kLift = 7;
 };
 template <>
 struct Kind<float> {
     typedef __bf16 Q;
     typedef __bf16 P;
-    static constexpr int kQ = 3, kP = 3;
+    static constexpr int kQ = 3, kP = 3, kLift = 0;
 };
 
 template <typename E>
@@ -95,7 +99,7 @@ __device__ inline void split(typename Vec8<E>::t* o, const float* x) {
 
 constexpr int kRows = kRowTile;      // query rows of a tile
 constexpr int kPiece = kPieceTokens;  // tokens of one step
-// P's values reach 2^kLazy before the running maximum is raised, so most steps rescale nothing.
+// P's values reach 2^kLazy (times 2^kLift) before the running maximum is raised, so most steps rescale nothing.
 constexpr float kLazy = 8.0f;
 // O is kept in units of 2^unit; a block's V codes are widened times 2^(ev - unit). Within
 // [-kFar, kNear] of the unit every code is a normal fp16 number (2^-9 * 2^-5 = 2^-14 and
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[c][i] *= f;
         }
-        const float m0 = m == -__builtin_inff() ? 0.0f : m;  // a row that has seen nothing finite
+        const float m0 = (m == -__builtin_inff() ? 0.0f : m) - Kd::kLift;  // 0: a row that has seen nothing finite
         float p[8];
 #pragma unroll
         for (int k8 = 0; k8 < 8; ++k8) {
@@ -445,6 +449,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     // Join the waves: rows' maximum, sum and O in true units.
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    l *= 1.0f / (1 << Kd::kLift);
     seen = (__ballot(seen) >> col & 0x0001000100010001ull) != 0;
     // Every score this wave saw is -inf. Beside finite scores they weigh 0; if the whole row's are, it is 0 / 0. The
     // lowest finite maximum joins as just that.
@@ -456,7 +461,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     float* const s_l = s_m + W * cap;
     float* const s_o = s_l + W * cap;  // [W][cap][DS]
     const int tile_rows = min(kRows, rows - r0);
-    const float back = pow2i(max(-126, min(127, unit)));
+    const float back = __builtin_amdgcn_ldexpf(1.0f, unit - Kd::kLift);
     if (col < tile_rows) {
         float* const dst = s_o + (wave * cap + col) * DS + quad * 16;
 #pragma unroll
@@ -859,7 +864,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 #pragma unroll
             for (int i = 0; i < 2 * NS; ++i) o[i] *= f;
         }
-        const float m0 = m == -__builtin_inff() ? 0.0f : m;
+        const float m0 = (m == -__builtin_inff() ? 0.0f : m) - Kd::kLift;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             float p[8];
@@ -927,11 +932,12 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     if (kShift && !second) __syncthreads();
 
     l += __shfl_xor(l, 32);
+    l *= 1.0f / (1 << Kd::kLift);
     seen = (__ballot(seen) >> col & 0x0000000100000001ull) != 0;
     if (!real) return;
     // Every visible score -inf: 0 / 0. No visible token: 0.
     const float inv = !seen ? 0.0f : m == -__builtin_inff() ? __builtin_nanf("") : 1.0f / l;
-    const float back = pow2i(max(-126, min(127, unit)));
+    const float back = __builtin_amdgcn_ldexpf(1.0f, unit - Kd::kLift);
     T* const out = static_cast<T*>(a.out) + (int64_t)(a.b.row0[b] + tq) * a.o_row + (int64_t)head * a.o_head;
 #pragma unroll
     for (int c = 0; c < NS; ++c)

@@ -496,8 +496,9 @@ np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, i
  * overlap). lse, fp32 [rows][n_heads], receives ln sum exp(s_j) (NULL: not).
  * Sums and softmax statistics are fp32; K and V enter exactly (V scales of
  * one head that lie more than 2^40 below the largest vanish); the weights
- * exp(s_j) are rounded to fp16 for 16-bit dtypes and kept to 24 bits for
- * NP_F32. Results are the same from run to run.
+ * exp(s_j) are kept to 24 bits for NP_F32 and rounded to fp16 for 16-bit
+ * dtypes: off by 2^-11 of themselves or 2^-32 of the row's largest, whichever
+ * is more. Results are the same from run to run.
  * Errors: NP_EINVAL (scale not positive and finite, a negative window), NP_ESTATE (no
  * current tokens). */
 np_status np_kv_attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,

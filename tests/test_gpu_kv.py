@@ -618,3 +618,45 @@ def test_a_row_whose_scores_are_all_minus_infinity_is_nan(dtype, heads, new):
     q[0, 0, 3] = -float("inf")
     out = e.attend(dtype, q=(q, q.double().numpy()))
     assert bool(out[0, 0].isnan().all()) and int(out.isnan().sum()) == 64
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("prompt", [True, False])
+def test_small_weights_of_many_tokens_count(dtype, hd, prompt):
+    # One dominant first token whose value is 0; each later token weighs 2^-25.6 of it, so together they make the output.
+    # A 16-bit weight is off by 2^-11 of itself or, at the bottom of fp16's range, by 2^-32 of the running largest weight
+    # (half of 2^-24, the weights being held times 2^7 at least).
+    heads, n, seqs = (32, 4100, 1) if prompt else (64, 2000, 8)
+    e = Env(heads=heads, kv=heads, hd=hd, page=64, pages=300, seqs=seqs)
+    k, v = torch.zeros((n, heads, hd)), torch.rand((n, heads, hd), generator=torch.Generator().manual_seed(1)) + 0.5
+    k[0, :, 0], v[0] = 16.0, 0.0
+    kd, vd = k.cuda(), v.cuda()
+    for s in range(seqs):
+        e.kv.extend([s], [n], e.stream())
+        e.kv.append(0, kd.data_ptr(), vd.data_ptr(), "f32", None, e.stream())
+    new = n if prompt else seqs
+    if not prompt:      # the rows' own tokens: another one of the kind
+        e.kv.extend(list(range(seqs)), [1] * seqs, e.stream())
+        own = kd[1:2].repeat(seqs, 1, 1), vd[1:2].repeat(seqs, 1, 1)
+        e.kv.append(0, own[0].data_ptr(), own[1].data_ptr(), "f32", None, e.stream())
+    scale, w = 25.6 * math.log(2) / 16, 2.0 ** -25.6
+    q = torch.zeros((new, heads, hd))
+    q[:, :, 0] = 1.0
+    qd = q.to(tdt(dtype)).cuda()
+    out = torch.empty_like(qd)
+    e.kv.attend(0, qd.data_ptr(), out.data_ptr(), dtype, scale=scale, stream=e.stream())
+    got = out.double().cpu().numpy()
+    _, val = e.kv.read_tokens(0, 0)
+    total = np.cumsum(val.astype(np.float64), axis=0)
+    if not prompt:
+        total = np.repeat(total[-1:], seqs, axis=0)
+    count = np.arange(n)[:, None, None] if prompt else n
+    want = w * total / (1 + w * count)
+    tiny = 2.0 ** -24 if dtype == "f16" else 2.0 ** -126
+    weights = 2.0 ** -24 if dtype == "f32" else 2.0 ** -11
+    scores, sums = 16 * 26 * 2.0 ** -24, 2 * (n + 16) * 2.0 ** -24   # as in kv_reference.bound, one product a score
+    bottom = 0 if dtype == "f32" else 2.0 ** -32
+    tol = R.U[dtype] * np.abs(want) * 1.01 + 2 * (want * (weights + 2 * scores + sums) + bottom * total) + tiny
+    err = np.abs(got - want)
+    assert (err <= tol).all(), f"worst {np.max(err / tol):.2f} bounds, {np.max(err[-1] / want[-1]):.3f} of the last row"
