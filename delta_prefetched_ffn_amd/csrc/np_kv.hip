@@ -131,6 +131,14 @@ struct np_kv {
         stale.clear();
         drop_batch();
     }
+    // Room that calls need after their checks: they change nothing unless all of it is there.
+    void reserve() {
+        stale.reserve(desc.max_seqs);  // each sequence once
+        for (std::vector<int32_t>* v : {&b_seq, &b_before, &b_fresh}) v->reserve(kMaxBatch);
+    }
+    void reserve_pages(Seq& q, size_t n) const {
+        if (n > q.pages.capacity()) q.pages.reserve(std::min<size_t>(std::max(n, 2 * q.pages.capacity()), desc.max_pages));
+    }
     KvView view() const {
         KvView v;
         v.codes = static_cast<uint8_t*>(desc.codes);
@@ -310,6 +318,7 @@ np_status create(const np_kv_desc* desc, np_kv** out) {
     kv->page_bytes = page_bytes_of(D);
     kv->layer_bytes = kv->page_bytes * D.n_pages;
     kv->clear();
+    kv->reserve();
     if (D.device != NP_KV_HOST) {
         if (!D.codes || !D.exps || !aligned16(D.codes))
             return fail(NP_EINVAL, "codes and exps must be device pointers, codes 16-byte aligned");
@@ -369,9 +378,15 @@ np_status extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new
     if (need > kv->n_free) return fail(NP_ECAPACITY, "%lld pages needed, %d free", (long long)need, kv->n_free);
     if (rows > 1 << 28) return fail(NP_EINVAL, "%lld new tokens in one call exceed 2^28", (long long)rows);
 
+    std::vector<Move> moves;
+    moves.reserve(n);
+    for (int i = 0; i < n; ++i) {
+        Seq& q = kv->seqs[seqs[i]];
+        kv->reserve_pages(q, kv->pages_for((int64_t)q.tokens + n_new[i]));
+    }
+
     // From here on nothing is refused. A page given up by a copy is still held by another sequence,
     // so copies read pages that nothing writes.
-    std::vector<Move> moves;
     kv->drop_batch();
     for (int i = 0; i < n; ++i) {
         Seq& q = kv->seqs[seqs[i]];
@@ -552,10 +567,12 @@ np_status fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mo
         if (need > kv->n_free) return fail(NP_ECAPACITY, "%lld pages needed, %d free", (long long)need, kv->n_free);
     }
     Seq& q = kv->seqs[dst];
+    std::vector<Move> moves;
+    if (mode == NP_KV_COPY) moves.reserve(n);
+    kv->reserve_pages(q, n);
     q.pages.assign(from.begin(), from.begin() + n);
     q.tokens = n_tokens;
     kv->drop_batch_of(dst);
-    std::vector<Move> moves;
     for (int32_t& p : q.pages) {
         if (p < 0) continue;
         if (mode == NP_KV_COPY) {
@@ -590,6 +607,7 @@ np_status adopt(np_kv* kv, int32_t seq, const int32_t* pages, int32_t n_pages, i
         taken[p >> 6] |= bit;
     }
     Seq& q = kv->seqs[seq];
+    kv->reserve_pages(q, n_pages);
     q.pages.assign(pages, pages + n_pages);
     q.tokens = n_tokens;
     kv->drop_batch_of(seq);

@@ -1,0 +1,104 @@
+"""The host side of the 8-bit key/value cache where something fails beneath it, on the CPU: np_kv.hip compiled together with
+tests/kv_stub.cpp, which stands for the device (allocations, the current device and launches fail on demand there)."""
+import ctypes
+import importlib.util
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "delta_prefetched_ffn_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def B(tmp_path_factory):
+    """The binding over the stubbed library, with the stub's switches as B.stub."""
+    so = str(tmp_path_factory.mktemp("kv") / "libkv_stub.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    "-I" + CSRC, "-I" + os.path.join(ROOT, "include"), "-x", "c++", os.path.join(CSRC, "np_kv.hip"),
+                    os.path.join(ROOT, "tests", "kv_stub.cpp"), "-o", so], check=True, capture_output=True, text=True)
+    spec = importlib.util.spec_from_file_location("kv_stubbed_binding", os.path.join(ROOT, "delta_prefetched_ffn_amd", "binding.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    real, stub = m.lib(), ctypes.CDLL(so)
+    for name in m.EXPORTS:
+        if name.startswith("np_kv_"):
+            getattr(stub, name).argtypes = getattr(real, name).argtypes
+    stub.np_last_error.restype = ctypes.c_char_p
+    stub.stub_fail_new.argtypes = [ctypes.c_long]
+    stub.stub_launches.restype = stub.stub_wrong_device.restype = ctypes.c_long
+    stub.stub_table.restype = ctypes.POINTER(ctypes.c_int32)
+    m.lib = lambda: stub
+    m.stub = stub
+    return m
+
+
+def cache(B, **kw):
+    base = dict(n_layers=2, n_heads=8, n_kv_heads=4, head_dim=64, page_tokens=16, n_pages=40, max_seqs=6, max_pages=12, device=1,
+                codes=1 << 20, exps=1 << 20)
+    base.update(kw)
+    return B.KVCache(**base)
+
+
+def books(kv):
+    return [(kv.pages(s).tolist(), kv.tokens(s)) for s in range(kv.max_seqs)], kv.info()
+
+
+def prepared(B):
+    """Sequences with shared, dropped, half-filled and reserved pages, and holes in the pool."""
+    kv = cache(B)
+    kv.extend([0, 1], [75, 40])
+    kv.fork(0, 2, 70)
+    kv.extend([1], [20])
+    kv.evict(1, 16, 0)
+    kv.adopt(3, [30, 31, 38], 20)
+    kv.extend([0, 3], [0, 0])
+    return kv
+
+
+CALLS = {
+    "extend": lambda kv: kv.extend([0, 2, 1, 4], [60, 100, 1, 33]),
+    "extend_copies": lambda kv: kv.extend([2, 0], [1, 1]),
+    "share": lambda kv: kv.fork(0, 4, 66),
+    "copy": lambda kv: kv.fork(0, 4, 66, "copy"),
+    "adopt": lambda kv: kv.adopt(4, [20, 21, 22, 23, 24], 70),
+    "evict": lambda kv: kv.evict(0, 5, 0),
+    "compact": lambda kv: kv.compact(),
+    "trim": lambda kv: kv.trim(2, 3),
+    "reset": lambda kv: kv.reset(),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_failed_allocations_change_nothing(B, name):
+    call = CALLS[name]
+    want = prepared(B)
+    call(want)
+    for after in range(200):
+        kv = prepared(B)
+        before = books(kv)
+        B.stub.stub_fail_new(after)
+        try:
+            call(kv)
+            failed = False
+        except B.NPError as e:
+            failed = True
+            assert e.status == B.NP_ENOMEM
+        finally:
+            B.stub.stub_fail_new(-1)
+        if failed:
+            assert books(kv) == before, f"changed by a call that failed at allocation {after}"
+            call(kv)
+        assert books(kv) == books(want)
+        # and the device's page table follows
+        live = [s for s in range(kv.max_seqs) if kv.tokens(s) % 16]
+        if live:
+            kv.extend(live, [0] * len(live))
+            for s in live:
+                at = s * kv.max_pages
+                assert B.stub.stub_table()[at:at + len(kv.pages(s))] == kv.pages(s).tolist(), s
+        if not failed:
+            return
+    assert False, "never came through"
