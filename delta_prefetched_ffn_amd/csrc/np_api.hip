@@ -16,7 +16,6 @@
 #include <mutex>
 #include <condition_variable>
 #include <functional>
-#include <string>
 #include <thread>
 #include <vector>
 
@@ -61,17 +60,17 @@ void setup_scratch(int dev) {
     g_scratch[dev].ptr = static_cast<uint64_t*>(p);
 }
 
-thread_local std::string g_err;
+thread_local char g_err[512];  // no allocation: errors are also reported where one has just failed
 }  // namespace
 
 namespace np {
 np_status fail(np_status st, const char* fmt, ...) {
-    char buf[512];
+    char buf[sizeof g_err];  // an argument may be the last error's text
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_err = buf;
+    std::memcpy(g_err, buf, sizeof buf);
     return st;
 }
 
@@ -956,7 +955,7 @@ std::shared_ptr<DecodePlan> get_plan(np_layer* const* layers, int n, hipStream_t
 
 extern "C" {
 
-const char* np_last_error(void) { return g_err.c_str(); }
+const char* np_last_error(void) { return g_err; }
 
 np_status np_layer_create(const np_layer_desc* desc, np_layer** out) {
     if (!desc || !out) return fail(NP_EINVAL, "desc and out must not be NULL");
@@ -1347,7 +1346,7 @@ np_status np_decode_step(np_layer* const* layers, int32_t n_layers, const int32_
         if (de != NP_OK) return de;
         int32_t u;
         np_status st = check_cids(L, cids[2 * l], cids[2 * l + 1], &u);
-        if (st != NP_OK) return fail(st, "layer %d: %s", l, g_err.c_str());
+        if (st != NP_OK) return fail(st, "layer %d: %s", l, g_err);
         u_eff[l] = u;
         S[l].resize(L->W);
         n_act[l] = combine_host(L, cids[2 * l], u, S[l].data());

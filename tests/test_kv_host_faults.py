@@ -102,3 +102,31 @@ def test_failed_allocations_change_nothing(B, name):
         if not failed:
             return
     assert False, "never came through"
+
+
+def test_an_error_is_reported_without_memory(tmp_path):
+    # The text of an error is kept without an allocation: a throw from there would leave a C entry.
+    src = tmp_path / "new.cpp"
+    src.write_text("#include <cstdlib>\n#include <new>\nextern \"C\" { int no_memory = 0; }\n"
+                   "void* operator new(size_t n) { if (no_memory) throw std::bad_alloc(); return std::malloc(n ? n : 1); }\n"
+                   "void operator delete(void* p) noexcept { std::free(p); }\nvoid operator delete(void* p, size_t) noexcept { std::free(p); }\n")
+    so = str(tmp_path / "libnew.so")
+    subprocess.run(["g++", "-O1", "-shared", "-fPIC", str(src), "-o", so], check=True)
+    script = ("import ctypes, sys\n"
+              "L, new = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])\n"
+              "L.np_last_error.restype = ctypes.c_char_p\n"
+              "off = ctypes.c_int.in_dll(new, 'no_memory')\n"
+              "desc = (ctypes.c_int32 * 16)(1, 7, 3, 64, 16, 4, 1, 4, -1)\n"
+              "h = ctypes.c_void_p()\n"
+              "off.value = 1\n"
+              "bad = L.np_kv_create(desc, ctypes.byref(h))\n"          # n_heads no multiple of n_kv_heads
+              "desc[1] = 6\n"
+              "none = L.np_kv_create(desc, ctypes.byref(h))\n"         # in order, but there is no memory for it
+              "off.value = 0\n"
+              "print(bad, none, L.np_last_error().decode())\n")
+    env = dict(os.environ)
+    env["LD_PRELOAD"] = so + (":" + env["LD_PRELOAD"] if env.get("LD_PRELOAD") else "")
+    r = subprocess.run(["python3", "-c", script, os.path.join(ROOT, "delta_prefetched_ffn_amd", "libnp.so"), so],
+                       env=env, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.strip() == "1 3 host allocation failed"
