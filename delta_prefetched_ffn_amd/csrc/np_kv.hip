@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <optional>
 #include <unordered_map>
 #include <utility>
 #include <vector>
@@ -241,6 +242,13 @@ np_status check_kv(const np_kv* kv) {
     return NP_OK;
 }
 
+// Makes the cache's device current, if it has one: after the checks of a call, before it changes anything.
+np_status make_current(const np_kv* kv, std::optional<DeviceGuard>& g) {
+    if (kv->host_only()) return NP_OK;
+    g.emplace(kv->desc.device);
+    return g->ok ? NP_OK : fail(NP_EHIP, "hipSetDevice(%d) failed", kv->desc.device);
+}
+
 int elem_bytes(int32_t dtype) { return dtype == NP_F32 ? 4 : 2; }
 
 np_status check_layer_io(const np_kv* kv, int32_t layer, int32_t dtype) {
@@ -384,6 +392,8 @@ np_status extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new
         Seq& q = kv->seqs[seqs[i]];
         kv->reserve_pages(q, kv->pages_for((int64_t)q.tokens + n_new[i]));
     }
+    std::optional<DeviceGuard> g;
+    if ((st = make_current(kv, g)) != NP_OK) return st;
 
     // From here on nothing is refused. A page given up by a copy is still held by another sequence,
     // so copies read pages that nothing writes.
@@ -406,8 +416,6 @@ np_status extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t* n_new
         while ((int)q.pages.size() < kv->pages_for(q.tokens)) q.pages.push_back(kv->take());
         kv->touch(seqs[i], had, (int32_t)q.pages.size());
     }
-    if (kv->host_only()) return flush_table(kv, s);
-    DeviceGuard g(kv->desc.device);
     if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
     return flush_table(kv, s);
 }
@@ -439,7 +447,8 @@ np_status append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t
     if (a.b.item0[a.b.n] == 0) return NP_OK;
     if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads >= (int64_t)1 << 31)
         return fail(NP_EINVAL, "%d pages of %d heads in one call are too many", a.b.item0[a.b.n], D.n_kv_heads);
-    DeviceGuard g(D.device);
+    std::optional<DeviceGuard> g;
+    if ((st = make_current(kv, g)) != NP_OK) return st;
     NP_HIP(launch_kv_append(a, dtype, s));
     return NP_OK;
 }
@@ -487,7 +496,8 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     a.arrived = kv->arrived;
     const int group = D.n_heads / D.n_kv_heads, n = (int)kv->b_seq.size();
     if (rows * D.n_heads > 1 << 30) return fail(NP_EINVAL, "%lld rows of %d heads in one call are too many", (long long)rows, D.n_heads);
-    DeviceGuard g(D.device);
+    std::optional<DeviceGuard> g;
+    if ((st = make_current(kv, g)) != NP_OK) return st;
     const int tile_rows = attn_tile_rows(dtype, kv->slabs);
     const auto large = [&](int i) { return tile_rows > 0 && (int64_t)kv->b_fresh[i] * group >= kManyRows; };
     double longest = 0, steps = 0, units = 0, row_tiles = 0;
@@ -570,6 +580,8 @@ np_status fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mo
     std::vector<Move> moves;
     if (mode == NP_KV_COPY) moves.reserve(n);
     kv->reserve_pages(q, n);
+    std::optional<DeviceGuard> g;
+    if (mode == NP_KV_COPY && (st = make_current(kv, g)) != NP_OK) return st;
     q.pages.assign(from.begin(), from.begin() + n);
     q.tokens = n_tokens;
     kv->drop_batch_of(dst);
@@ -583,8 +595,6 @@ np_status fork(np_kv* kv, int32_t src, int32_t dst, int32_t n_tokens, int32_t mo
         }
     }
     kv->touch(dst, 0, n);
-    if (moves.empty() || kv->host_only()) return NP_OK;
-    DeviceGuard g(kv->desc.device);
     return copy_pages(kv, moves, s);
 }
 
@@ -652,6 +662,8 @@ np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
         moves.push_back({p, hole});
         to[p] = hole++;
     }
+    std::optional<DeviceGuard> g;
+    if (!moves.empty() && (st = make_current(kv, g)) != NP_OK) return st;
     if (n_moved) *n_moved = (int32_t)moves.size();
     if (moves.empty()) return NP_OK;
     for (int32_t q = 0; q < kv->desc.max_seqs; ++q) {
@@ -668,8 +680,6 @@ np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
         kv->free_w[m.second >> 6] &= ~(1ull << (m.second & 63));
         kv->free_w[m.first >> 6] |= 1ull << (m.first & 63);
     }
-    if (kv->host_only()) return NP_OK;
-    DeviceGuard g(kv->desc.device);
     if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
     return kv->b_seq.empty() ? NP_OK : flush_table(kv, s);  // the current step goes on with the new pages
 }
@@ -690,7 +700,8 @@ np_status read_tokens(const np_kv* kv, int32_t layer, int32_t seq, int32_t first
         return fail(NP_EINVAL, "tokens [%d, %lld) out of range [0, %d)", first, (long long)first + n, q.tokens);
     if (kv->host_only()) return fail(NP_ESTATE, "a bookkeeping-only cache holds no tokens");
     const np_kv_desc& D = kv->desc;
-    DeviceGuard g(D.device);
+    std::optional<DeviceGuard> g;
+    if ((st = make_current(kv, g)) != NP_OK) return st;
     NP_HIP(hipDeviceSynchronize());
     const int pt = kv->pt(), hd64 = kv->slabs * kTileDims;
     std::vector<uint8_t> codes(kv->page_bytes);

@@ -130,3 +130,51 @@ def test_an_error_is_reported_without_memory(tmp_path):
                        env=env, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.strip() == "1 3 host allocation failed"
+
+
+STREAM_CALLS = {
+    "extend": lambda kv: kv.extend([0, 2], [60, 1]),
+    "append": lambda kv: kv.append(0, 4096, 4096, "bf16"),
+    "attend": lambda kv: kv.attend(0, 4096, 4096, "bf16", scale=1.0),
+    "copy": lambda kv: kv.fork(0, 4, 66, "copy"),
+    "compact": lambda kv: kv.compact(),
+    "read_tokens": lambda kv: kv.read_tokens(0, 3, 0, 0),
+}
+
+
+@pytest.mark.parametrize("name", list(STREAM_CALLS))
+def test_a_device_that_cannot_be_made_current_is_reported(B, name):
+    # The current device is another one (0); work for the cache's would go to it.
+    kv = prepared(B)
+    kv.extend([0, 1], [3, 2])
+    before, wrong, launches = books(kv), B.stub.stub_wrong_device(), B.stub.stub_launches()
+    B.stub.stub_fail_set_device(1)
+    try:
+        with pytest.raises(B.NPError) as e:
+            STREAM_CALLS[name](kv)
+    finally:
+        B.stub.stub_fail_set_device(0)
+    assert e.value.status == B.NP_EHIP and "hipSetDevice" in str(e.value)
+    assert books(kv) == before and B.stub.stub_launches() == launches
+    STREAM_CALLS[name](kv)
+    assert B.stub.stub_wrong_device() == wrong and B.stub.stub_device() == 0
+
+
+def test_a_failed_launch_asks_for_a_reset(B):
+    for call in (lambda kv: kv.extend([0, 2], [60, 1]), lambda kv: kv.fork(0, 4, 66, "copy"), lambda kv: kv.compact()):
+        kv = prepared(B)
+        B.stub.stub_fail_launch(0)
+        try:
+            with pytest.raises(B.NPError) as e:
+                call(kv)
+        finally:
+            B.stub.stub_fail_launch(-1)
+        assert e.value.status == B.NP_EHIP
+        for again in (lambda: kv.extend([0], [1]), lambda: kv.append(0, 4096, 4096, "f32"), lambda: kv.attend(0, 4096, 4096, "f32", scale=1.0),
+                      lambda: kv.fork(0, 5, 1), lambda: kv.free(0), lambda: kv.adopt(5, [], 0), lambda: kv.compact()):
+            with pytest.raises(B.NPError) as e:
+                again()
+            assert e.value.status == B.NP_ESTATE
+        kv.reset()
+        kv.extend([0], [17])
+        assert B.stub.stub_table()[:2] == kv.pages(0).tolist() == [0, 1]
