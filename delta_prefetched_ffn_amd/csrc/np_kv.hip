@@ -38,6 +38,11 @@ constexpr int kFewPieces = 16;
 // fp32 the tiles pay up to 64 values a head (4 Ki tokens x 32 heads: 234 against 344 us); beyond, q's
 // three summands leave a wave too few registers.
 constexpr int kManyRows = 128;
+
+// A launch has at most 2^32 - 1 threads along x: workgroups of k_kv_append (256 threads) and of k_attn_rows.
+// (k_attn_tile's stay below for the 2^30 rows x heads a call may have.)
+constexpr int64_t kMaxAppendBlocks = (int64_t)1 << 24;
+constexpr int64_t kMaxRowTiles = ((int64_t)1 << 32) / (64 * kAttnWaves);
 struct TileCost {
     double step, unit;
 };
@@ -445,7 +450,7 @@ np_status append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t
         return f ? kv->pages_for((int64_t)b + f) - (b >> kv->page_shift) : 0;
     });
     if (a.b.item0[a.b.n] == 0) return NP_OK;
-    if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads >= (int64_t)1 << 31)
+    if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads >= kMaxAppendBlocks)
         return fail(NP_EINVAL, "%d pages of %d heads in one call are too many", a.b.item0[a.b.n], D.n_kv_heads);
     std::optional<DeviceGuard> g;
     if ((st = make_current(kv, g)) != NP_OK) return st;
@@ -515,12 +520,6 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
     const TileCost cost = tile_cost(dtype, kv->slabs);
     const bool pays = cost.step * std::max(longest, steps / kCus) < cost.unit * units + kRowTileCost * row_tiles;
     const auto many = [&](int i) { return pays && large(i); };
-    fill_batch(kv, a.b, [&](int i) { return many(i) ? (kv->b_fresh[i] * group + tile_rows - 1) / tile_rows : 0; });
-    if (a.b.item0[n] > 0) {
-        a.part = nullptr;
-        NP_HIP(launch_attn(a, dtype, s));
-        a.part = kv->part;
-    }
     // Pieces of a sequence's last row tile (the most of its tiles), and of all tiles together.
     const auto tiles = [&](int i) { return many(i) ? 0 : (kv->b_fresh[i] * group + kRowTile - 1) / kRowTile; };
     const auto pieces = [&](int i) {
@@ -534,7 +533,6 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
         all += pieces(i) * tiles(i) * D.n_kv_heads;
         if (tiles(i)) a.row_cap = std::max(a.row_cap, std::min(kRowTile, kv->b_fresh[i] * group));
     }
-    if (!all) return NP_OK;
     // Pieces of a workgroup: one per wave at least, else so many that the launch is not a few workgroups
     // more than its turns hold (they would be a turn of their own).
     const int64_t most = kCus * (all > (int64_t)kCus * kAttnWaves * kFewPieces ? 2 : 1);
@@ -548,14 +546,23 @@ np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse,
         }
         if (wgs <= std::max(most, least)) break;
     }
-    int64_t partials = 0;
+    int64_t partials = 0, row_wgs = 0;
     for (int i = 0; i < n; ++i) {
         int64_t sp = std::max<int64_t>(1, splits(i, per));
         if ((partials + tiles(i) * sp) * D.n_kv_heads > std::min(kMaxPartials, kMaxPartialRows / a.row_cap)) sp = 1;
         a.b.splits[i] = (int32_t)sp;
         a.b.part0[i] = (int32_t)partials;
         if (sp > 1) partials += tiles(i) * sp;
+        row_wgs += tiles(i) * sp;
     }
+    if (row_wgs >= kMaxRowTiles) return fail(NP_EINVAL, "%lld tiles of %d rows in one call are too many", (long long)row_wgs, kRowTile);
+    fill_batch(kv, a.b, [&](int i) { return many(i) ? (kv->b_fresh[i] * group + tile_rows - 1) / tile_rows : 0; });
+    if (a.b.item0[n] > 0) {
+        a.part = nullptr;
+        NP_HIP(launch_attn(a, dtype, s));
+        a.part = kv->part;
+    }
+    if (!all) return NP_OK;
     fill_batch(kv, a.b, [&](int i) { return tiles(i) * a.b.splits[i]; });
     NP_HIP(launch_attn(a, dtype, s));
     return NP_OK;

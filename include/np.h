@@ -480,7 +480,8 @@ np_status np_kv_extend(np_kv* kv, int32_t n, const int32_t* seqs, const int32_t*
  * Infinities are stored as +-448 * 2^e and NaN as NaN; neither enters e. A
  * second call for the same tokens overwrites them, but e does not go down
  * again for a page that holds earlier tokens.
- * Errors: NP_EINVAL, NP_ESTATE (no current tokens). */
+ * Errors: NP_EINVAL (also from 2^24 blocks in one call on), NP_ESTATE (no
+ * current tokens). */
 np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t dtype, const int64_t* strides,
                        void* stream);
 
@@ -499,8 +500,9 @@ np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, i
  * exp(s_j) are kept to 24 bits for NP_F32 and rounded to fp16 for 16-bit
  * dtypes: off by 2^-11 of themselves or 2^-32 of the row's largest, whichever
  * is more. Results are the same from run to run.
- * Errors: NP_EINVAL (scale not positive and finite, a negative window), NP_ESTATE (no
- * current tokens). */
+ * Errors: NP_EINVAL (scale not positive and finite, a negative window; more
+ * than 2^30 rows x heads, or 2^27 of one key/value head where they run 16 at
+ * a time), NP_ESTATE (no current tokens). */
 np_status np_kv_attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,
                        const int64_t* strides, float scale, int32_t window, int32_t sinks, void* stream);
 

@@ -178,3 +178,29 @@ def test_a_failed_launch_asks_for_a_reset(B):
         kv.reset()
         kv.extend([0], [17])
         assert B.stub.stub_table()[:2] == kv.pages(0).tolist() == [0, 1]
+
+
+def test_calls_too_large_for_a_launch_are_refused_before_anything_is_enqueued(B):
+    # 2^24 blocks of one append, 2^23 row tiles of one attend: a grid would pass 2^32 threads.
+    kv = cache(B, n_heads=1024, n_kv_heads=1024, head_dim=8, n_pages=1 << 15, max_pages=1 << 15)
+    kv.extend([0], [((1 << 14) - 1) * 16])
+    kv.append(0, 4096, 4096, "bf16")
+    kv.extend([0], [16 * ((1 << 14) - 1)])
+    kv.append(0, 4096, 4096, "bf16")
+    kv.free(0)
+    kv.extend([0], [1 << 18])
+    launches = B.stub.stub_launches()
+    with pytest.raises(B.NPError) as e:
+        kv.append(0, 4096, 4096, "bf16")
+    assert e.value.status == B.NP_EINVAL
+    kv = cache(B, n_heads=4096, n_kv_heads=1, head_dim=128, n_pages=1 << 14, max_pages=1 << 14, page_tokens=128)
+    kv.extend([0], [(1 << 15) - 16])
+    kv.attend(0, 4096, 4096, "f32", scale=1.0)
+    assert B.stub.stub_launches() == launches + 2      # a table of at most 480 entries, the attention
+    kv.extend([0], [1 << 15])
+    launches = B.stub.stub_launches()
+    with pytest.raises(B.NPError) as e:
+        kv.attend(0, 4096, 4096, "f32", scale=1.0)
+    assert e.value.status == B.NP_EINVAL
+    kv.attend(0, 4096, 4096, "bf16", scale=1.0)        # large tiles: 256 rows a workgroup
+    assert B.stub.stub_launches() == launches + 1
