@@ -333,8 +333,8 @@ np_status create(const np_kv_desc* desc, np_kv** out) {
     kv->clear();
     kv->reserve();
     if (D.device != NP_KV_HOST) {
-        if (!D.codes || !D.exps || !aligned16(D.codes))
-            return fail(NP_EINVAL, "codes and exps must be device pointers, codes 16-byte aligned");
+        if (!D.codes || !D.exps || !aligned16(D.codes) || ((uintptr_t)D.exps & 1u))
+            return fail(NP_EINVAL, "codes and exps must be device pointers, 16-byte and 2-byte aligned");
         int ndev = 0;
         NP_HIP(hipGetDeviceCount(&ndev));
         if (D.device < 0 || D.device >= ndev) return fail(NP_EINVAL, "device %d out of range [0, %d)", D.device, ndev);

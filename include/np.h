@@ -440,8 +440,8 @@ typedef struct np_kv_desc {
     int32_t max_pages;   /* pages of one sequence at most                    */
     int32_t device;      /* HIP device ordinal, or NP_KV_HOST                */
     /* The pool, BORROWED: device memory of the sizes np_kv_bytes gives, codes
-     * 16-byte aligned, alive while the cache exists. The caller may save and
-     * restore it (np_kv_adopt). Not used with NP_KV_HOST. */
+     * 16-byte and exps 2-byte aligned, alive while the cache exists. The caller
+     * may save and restore it (np_kv_adopt). Not used with NP_KV_HOST. */
     void* codes;
     int8_t* exps;
 } np_kv_desc;

@@ -204,3 +204,13 @@ def test_calls_too_large_for_a_launch_are_refused_before_anything_is_enqueued(B)
     assert e.value.status == B.NP_EINVAL
     kv.attend(0, 4096, 4096, "bf16", scale=1.0)        # large tiles: 256 rows a workgroup
     assert B.stub.stub_launches() == launches + 1
+
+
+def test_exponents_at_an_odd_address_are_refused(B):
+    # The attention reads a head's two exponents as one 16-bit number.
+    for exps in ((1 << 20) + 1, (1 << 20) + 3):
+        with pytest.raises(B.NPError) as e:
+            cache(B, exps=exps)
+        assert e.value.status == B.NP_EINVAL and "exps" in str(e.value)
+    cache(B, exps=(1 << 20) + 2)
+    cache(B, device=B.KV_HOST, codes=0, exps=0)
