@@ -328,9 +328,12 @@ class KVCache:
         try:
             return self._strides[strides]
         except (KeyError, TypeError):   # new ones, or a list
+            four = array.array("q", strides)
+            if len(four) != 4:
+                raise ValueError(f"strides: {len(four)} numbers instead of 4")
             if len(self._strides) > 64:
                 self._strides = {None: None}
-            return self._strides.setdefault(tuple(strides), (ctypes.c_int64 * 4)(*strides))
+            return self._strides.setdefault(tuple(four), (ctypes.c_int64 * 4)(*four))
 
     def attend(self, layer: int, q_ptr: int, out_ptr: int, dtype: str, strides=None, *, scale: float, window: int = 0,
                sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:

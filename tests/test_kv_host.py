@@ -269,3 +269,19 @@ def test_fork_trim_evict_refusals():
     cap = np.zeros(1, np.int32)
     n = ctypes.c_int32()
     assert B.lib().np_kv_read_pages(kv.h, 0, cap.ctypes.data, 1, ctypes.byref(n), None) == B.NP_EINVAL
+
+
+def test_strides_are_four_numbers():
+    # A short tuple was filled up with zeros: every row of v the first one.
+    kv = cache()
+    kv.extend([0], [5])
+    for bad in ((256, 64), (256, 64, 256), (), [256, 64], (256, 64, 256, 64, 1)):
+        with pytest.raises(ValueError):
+            kv.append(0, 4096, 4096, "f32", bad)
+        with pytest.raises(ValueError):
+            kv.attend(0, 4096, 4096, "f32", bad, scale=1.0)
+    with pytest.raises(OverflowError):
+        kv.append(0, 4096, 4096, "f32", (256, 64, 256, (1 << 64) + 64))
+    for good in ((256, 64, 256, 64), [256, 64, 256, 64], np.array([256, 64, 256, 64])):
+        for _ in range(2):
+            refused(B.NP_ESTATE, kv.append, 0, 4096, 4096, "f32", good)   # only the missing device is left to refuse
