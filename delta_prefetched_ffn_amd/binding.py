@@ -134,6 +134,13 @@ def _ptr(a: np.ndarray | None) -> int | None:
     return None if a is None else a.ctypes.data
 
 
+def _i32(x: int) -> int:
+    """x, if it fits the C ABI's 32 bits (ctypes would cut it)."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise OverflowError(f"{x} does not fit in 32 bits")
+    return x
+
+
 class Layer:
     """One sparse FFN layer (np_layer). row_store is a device or pinned-host pointer (int)."""
 
@@ -268,7 +275,7 @@ class Layer:
 def kv_bytes(*, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
              max_seqs: int = 1, max_pages: int = 1) -> tuple[int, int]:
     """Bytes of a cache's pool: (codes, exps)."""
-    desc = KVDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, KV_HOST, None, None)
+    desc = KVDesc(*map(_i32, (n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages)), KV_HOST, None, None)
     out = (ctypes.c_int64 * 2)()
     _check(lib().np_kv_bytes(ctypes.byref(desc), out))
     return out[0], out[1]
@@ -280,7 +287,7 @@ class KVCache:
 
     def __init__(self, *, n_layers: int, n_heads: int, n_kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
                  max_seqs: int, max_pages: int, codes: int = 0, exps: int = 0, device: int = 0, keepalive=None):
-        desc = KVDesc(n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, device,
+        desc = KVDesc(*map(_i32, (n_layers, n_heads, n_kv_heads, head_dim, page_tokens, n_pages, max_seqs, max_pages, device)),
                       codes or None, exps or None)
         h = ctypes.c_void_p()
         _check(lib().np_kv_create(ctypes.byref(desc), ctypes.byref(h)))
@@ -315,11 +322,13 @@ class KVCache:
         n = len(seqs)
         if len(n_new) != n:
             raise ValueError(f"extend: {n} sequences and {len(n_new)} counts")
-        a = ctypes.c_int32 * n
-        _check(lib().np_kv_extend(self.h, n, a(*seqs), a(*n_new), stream or None))
+        s, c = array.array("i", seqs), array.array("i", n_new)
+        _check(lib().np_kv_extend(self.h, n, s.buffer_info()[0], c.buffer_info()[0], stream or None))
 
     def append(self, layer: int, k_ptr: int, v_ptr: int, dtype: str, strides=None, stream: int = 0) -> None:
         """Stores the current tokens' k, v [rows][n_kv_heads][head_dim]; strides (elements): k row, k head, v row, v head."""
+        if layer >> 31 > 0:
+            _i32(layer)
         rc = self._append(self.h, layer, k_ptr, v_ptr, DTYPES[dtype], self._stride_array(strides), stream or None)
         if rc:
             _check(rc)
@@ -339,6 +348,9 @@ class KVCache:
                sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
         """Attention of the current tokens: q, out [rows][n_heads][head_dim]; strides (elements): q row, q head, out row,
         out head; window 0: every earlier token, else the last `window` and the first `sinks`."""
+        if (layer | window | sinks) >> 31 > 0:
+            for x in (layer, window, sinks):
+                _i32(x)
         rc = self._attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
                           window, sinks, stream or None)
         if rc:
@@ -346,13 +358,13 @@ class KVCache:
 
     def fork(self, src: int, dst: int, n_tokens: int, mode: str = "share", stream: int = 0) -> None:
         """The empty sequence dst becomes the first n_tokens of src ("share": shared pages, copied on write; "copy")."""
-        _check(lib().np_kv_fork(self.h, src, dst, n_tokens, KV_MODES[mode], stream or None))
+        _check(lib().np_kv_fork(self.h, _i32(src), _i32(dst), _i32(n_tokens), KV_MODES[mode], stream or None))
 
     def trim(self, seq: int, n_tokens: int) -> None:
-        _check(lib().np_kv_trim(self.h, seq, n_tokens))
+        _check(lib().np_kv_trim(self.h, _i32(seq), _i32(n_tokens)))
 
     def free(self, seq: int) -> None:
-        _check(lib().np_kv_free(self.h, seq))
+        _check(lib().np_kv_free(self.h, _i32(seq)))
 
     def adopt(self, seq: int, pages, n_tokens: int, stream: int = 0) -> None:
         """The empty sequence seq becomes these pages of the pool, holding n_tokens tokens (nothing is enqueued)."""
@@ -360,14 +372,20 @@ class KVCache:
             p = array.array("i", pages)
             at, n = p.buffer_info()
         else:
-            p = np.ascontiguousarray(pages, dtype=np.int32)
+            given = np.asarray(pages)
+            if given.ndim != 1 or (given.size and given.dtype.kind not in "iu"):
+                raise TypeError("pages must be a list of whole numbers")
+            if given.size:
+                _i32(int(given.min()))
+                _i32(int(given.max()))
+            p = np.ascontiguousarray(given, dtype=np.int32)
             at, n = p.ctypes.data, p.size
-        _check(lib().np_kv_adopt(self.h, seq, at, n, n_tokens))
+        _check(lib().np_kv_adopt(self.h, _i32(seq), at, n, _i32(n_tokens)))
 
     def evict(self, seq: int, window: int, sinks: int = 0, stream: int = 0) -> int:
         """Drops the pages that no later query of this window sees; how many (nothing is enqueued)."""
         n = ctypes.c_int32(0)
-        _check(lib().np_kv_evict(self.h, seq, window, sinks, ctypes.byref(n)))
+        _check(lib().np_kv_evict(self.h, _i32(seq), _i32(window), _i32(sinks), ctypes.byref(n)))
         return n.value
 
     def compact(self, stream: int = 0) -> int:
@@ -377,17 +395,19 @@ class KVCache:
         return n.value
 
     def pages(self, seq: int) -> np.ndarray:
-        _check(lib().np_kv_read_pages(self.h, seq, self._pages_at, self.max_pages, self._n_ref, None))
+        _check(lib().np_kv_read_pages(self.h, _i32(seq), self._pages_at, self.max_pages, self._n_ref, None))
         return np.frombuffer(self._pages, np.int32, self._n.value).copy() if self._n.value else np.empty(0, np.int32)
 
     def tokens(self, seq: int) -> int:
         t = ctypes.c_int32(0)
-        _check(lib().np_kv_read_pages(self.h, seq, None, 0, self._n_ref, ctypes.byref(t)))
+        _check(lib().np_kv_read_pages(self.h, _i32(seq), None, 0, self._n_ref, ctypes.byref(t)))
         return t.value
 
     def read_tokens(self, layer: int, seq: int, first: int = 0, n: int | None = None) -> tuple[np.ndarray, np.ndarray]:
         """Keys and values fp32 [n][n_kv_heads][head_dim] of tokens [first, first + n) (host)."""
         n = self.tokens(seq) - first if n is None else n
+        for x in (layer, seq, first, n):
+            _i32(x)
         k = np.empty((max(n, 0), self.n_kv_heads, self.head_dim), dtype=np.float32)
         v = np.empty_like(k)
         _check(lib().np_kv_read_tokens(self.h, layer, seq, first, n, k.ctypes.data, v.ctypes.data))

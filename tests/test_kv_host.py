@@ -285,3 +285,35 @@ def test_strides_are_four_numbers():
     for good in ((256, 64, 256, 64), [256, 64, 256, 64], np.array([256, 64, 256, 64])):
         for _ in range(2):
             refused(B.NP_ESTATE, kv.append, 0, 4096, 4096, "f32", good)   # only the missing device is left to refuse
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    # They were cut to their lower 32 bits: a window of 2^32 + 5 became one of 5, a page 2^32 + 3 page 3.
+    big = 1 << 32
+    kv = cache()
+    kv.extend([0], [40])
+    before = kv.pages(0).tolist(), kv.tokens(0), kv.info()
+    for call in (lambda: kv.extend([big + 1], [1]), lambda: kv.extend([1], [big + 1]), lambda: kv.append(big, 4096, 4096, "f32"),
+                 lambda: kv.attend(big, 4096, 4096, "f32", scale=1.0), lambda: kv.attend(0, 4096, 4096, "f32", scale=1.0, window=big + 5),
+                 lambda: kv.attend(0, 4096, 4096, "f32", scale=1.0, window=1 << 31), lambda: kv.attend(0, 4096, 4096, "f32", scale=1.0, window=7, sinks=big),
+                 lambda: kv.trim(0, big), lambda: kv.trim(big, 0), lambda: kv.free(big), lambda: kv.fork(0, 1, big + 3), lambda: kv.fork(big, 1, 3),
+                 lambda: kv.fork(0, big + 1, 3), lambda: kv.evict(0, big + 1), lambda: kv.evict(0, 1, big), lambda: kv.evict(big, 1),
+                 lambda: kv.adopt(1, [big + 5], 1), lambda: kv.adopt(1, np.array([big + 5]), 1), lambda: kv.adopt(1, (big + 5,), 1),
+                 lambda: kv.adopt(1, np.array([5, (1 << 63) + 9], np.uint64), 1), lambda: kv.adopt(1, [5], big + 1), lambda: kv.adopt(big + 1, [5], 1),
+                 lambda: kv.pages(big), lambda: kv.tokens(big), lambda: kv.read_tokens(0, 0, 0, big), lambda: kv.read_tokens(big, 0),
+                 lambda: cache(n_pages=big + 40), lambda: cache(max_seqs=(1 << 33) + 6),
+                 lambda: kv_bytes(n_layers=big + 1, n_heads=8, n_kv_heads=4, head_dim=64, page_tokens=16, n_pages=5)):
+        with pytest.raises(OverflowError):
+            call()
+    for pages in (np.array([5.0]), [5.0], np.array([[5, 6]])):
+        with pytest.raises((TypeError, ValueError)):
+            kv.adopt(1, pages, 1)
+    assert before == (kv.pages(0).tolist(), kv.tokens(0), kv.info())
+    for pages in ([20, 21], (20, 21), np.array([20, 21]), np.array([20, 21], np.uint8), np.array([20, 0, 21, 0], np.int32)[::2], np.array([20, 21], np.uint64)):
+        kv.adopt(1, pages, 30)
+        assert kv.pages(1).tolist() == [20, 21]
+        kv.free(1)
+    kv.adopt(1, [], 0)
+    kv.adopt(1, np.array([], np.int32), 0)
+    kv.extend(np.array([0, 1]), (np.int64(1), 2))
+    assert kv.tokens(1) == 2
