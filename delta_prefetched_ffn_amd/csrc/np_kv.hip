@@ -66,6 +66,7 @@ struct np_kv {
     int64_t page_bytes = 0, layer_bytes = 0;
     std::vector<int32_t> refs;      // sequences that hold each page
     std::vector<uint64_t> free_w;   // bit set: free
+    size_t first_free = 0;          // no word before it has a bit set
     int32_t n_free = 0;
     std::vector<Seq> seqs;
     std::vector<int32_t> stale;     // sequences with such entries
@@ -79,17 +80,9 @@ struct np_kv {
     int pt() const { return desc.page_tokens; }
     int pages_for(int64_t tokens) const { return (int)((tokens + pt() - 1) >> page_shift); }
 
-    int32_t lowest_free(size_t* from) const {
-        for (size_t w = *from; w < free_w.size(); ++w)
-            if (free_w[w]) {
-                *from = w;
-                return (int32_t)(w * 64 + __builtin_ctzll(free_w[w]));
-            }
-        return -1;
-    }
     int32_t take() {  // the free page with the lowest number (the caller has counted them)
-        size_t w = 0;
-        const int32_t p = lowest_free(&w);
+        while (!free_w[first_free]) ++first_free;
+        const int32_t p = (int32_t)(first_free * 64 + __builtin_ctzll(free_w[first_free]));
         take_page(p);
         return p;
     }
@@ -101,6 +94,7 @@ struct np_kv {
     void release(int32_t p) {
         if (p < 0 || --refs[p] > 0) return;
         free_w[p >> 6] |= 1ull << (p & 63);
+        first_free = std::min(first_free, (size_t)p >> 6);
         ++n_free;
     }
     // Entries [lo, hi) of a sequence have changed.
@@ -128,6 +122,7 @@ struct np_kv {
         refs.assign(desc.n_pages, 0);
         free_w.assign((desc.n_pages + 63) / 64, ~0ull);
         if (desc.n_pages & 63) free_w.back() = (1ull << (desc.n_pages & 63)) - 1;
+        first_free = 0;
         n_free = desc.n_pages;
         for (Seq& q : seqs) {
             q.pages.clear();
@@ -685,7 +680,7 @@ np_status compact(np_kv* kv, int32_t* n_moved, hipStream_t s) {
         kv->refs[m.second] = kv->refs[m.first];
         kv->refs[m.first] = 0;
         kv->free_w[m.second >> 6] &= ~(1ull << (m.second & 63));
-        kv->free_w[m.first >> 6] |= 1ull << (m.first & 63);
+        kv->free_w[m.first >> 6] |= 1ull << (m.first & 63);  // past the holes, so first_free holds
     }
     if ((st = copy_pages(kv, moves, s)) != NP_OK) return st;
     return kv->b_seq.empty() ? NP_OK : flush_table(kv, s);  // the current step goes on with the new pages

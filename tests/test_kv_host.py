@@ -2,6 +2,7 @@
 as one on a GPU, so every allocation rule and every refusal is checked here against a plain model."""
 import ctypes
 import random
+import time
 
 import numpy as np
 import pytest
@@ -317,3 +318,24 @@ def test_numbers_beyond_32_bits_are_refused():
     kv.adopt(1, np.array([], np.int32), 0)
     kv.extend(np.array([0, 1]), (np.int64(1), 2))
     assert kv.tokens(1) == 2
+
+
+def test_taking_pages_does_not_search_the_pool_again():
+    # 2^21 pages taken in one call, then the low half given back and taken again: each page's search began at page 0.
+    kv = cache(n_layers=1, n_pages=1 << 21, max_pages=1 << 21)
+    t = time.process_time()
+    kv.extend([0], [1 << 24])
+    kv.extend([1], [16 * (1 << 20)])
+    t = time.process_time() - t
+    assert kv.tokens(1) == 1 << 24
+    kv.free(0)
+    kv.extend([2], [1600])
+    assert kv.pages(2).tolist() == list(range(100))
+    kv.free(1)
+    kv.compact()
+    kv.extend([3], [16])
+    assert kv.pages(3).tolist() == [100]
+    kv.adopt(4, [101, 103], 20)
+    kv.extend([5], [40])
+    assert kv.pages(5).tolist() == [102, 104, 105]
+    assert t < 2.0, f"{t:.1f} s for 2^21 pages"
