@@ -1,5 +1,6 @@
 """The 8-bit key/value cache on the GPU against the fp64 definitions in tests/kv_reference.py: appended codes and exponents
 exactly, attention within bounds counted from its roundings."""
+import ctypes
 import math
 
 import numpy as np
@@ -660,3 +661,102 @@ def test_small_weights_of_many_tokens_count(dtype, hd, prompt):
     tol = R.U[dtype] * np.abs(want) * 1.01 + 2 * (want * (weights + 2 * scores + sums) + bottom * total) + tiny
     err = np.abs(got - want)
     assert (err <= tol).all(), f"worst {np.max(err / tol):.2f} bounds, {np.max(err[-1] / want[-1]):.3f} of the last row"
+
+
+# ------------------------------------------------------------------------------------------------ which kernels are reached
+
+class _KernelNode(ctypes.Structure):   # hipKernelNodeParams
+    _fields_ = [("block", ctypes.c_uint32 * 3), ("extra", ctypes.c_void_p), ("func", ctypes.c_void_p), ("grid", ctypes.c_uint32 * 3),
+                ("args", ctypes.c_void_p), ("lds", ctypes.c_uint32)]
+
+
+def kernels_of(call):
+    """Names of the kernels that `call` launches: from a captured graph that is never run."""
+    hip = ctypes.CDLL("libamdhip64.so.7")
+    hip.hipKernelNameRefByPtr.restype = ctypes.c_char_p
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        call(torch.cuda.current_stream().cuda_stream)
+    graph, n = ctypes.c_void_p(g.raw_cuda_graph()), ctypes.c_size_t()
+    assert hip.hipGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert hip.hipGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    names = []
+    for node in nodes:
+        p = _KernelNode()
+        assert hip.hipGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        names.append(hip.hipKernelNameRefByPtr(ctypes.c_void_p(p.func), None).decode())
+    return names
+
+
+def attention_kernels(heads, kv, hd, page, before, new, dtype, window=0, sinks=0):
+    e = Env(heads=heads, kv=kv, hd=hd, page=page, pages=sum(-(-(b + n) // page) for b, n in zip(before, new)) + 1, seqs=len(new))
+    seqs = list(range(len(new)))
+    e.kv.extend(seqs, before, e.stream())
+    e.kv.extend(seqs, new, e.stream())
+    q = torch.empty((sum(new), heads, hd), dtype=tdt(dtype), device="cuda")
+    names = kernels_of(lambda s: e.kv.attend(0, q.data_ptr(), q.data_ptr(), dtype, scale=1.0, window=window, sinks=sinks, stream=s))
+    return ["tile" if "k_attn_tile" in n else "rows" if "k_attn_rows" in n else n for n in names]
+
+
+@pytest.mark.parametrize("dtype,hd", TILES)
+def test_prompt_tests_reach_the_large_tiles(dtype, hd):
+    # The shapes of the tests above that are there for k_attn_tile, with single tokens beside a prompt in k_attn_rows.
+    for group, new, before, window, sinks in ((1, 300, 0, 0, 0), (2, 170, 77, 0, 0), (1, 290, 0, 50, 3), (1, 257, 130, 64, 70), (3, 129, 5, 1, 0)):
+        got = attention_kernels(64 * group, 64, hd, 32, [before, before // 3, 0], [new, 1, 0], dtype, window, sinks)
+        assert got == ["tile", "rows"], (group, new, before, window)
+    for before, new, window, sinks in ((0, 260, 0, 0), (0, 260, 100, 3), (0, 260, 23, 2), (144, 330, 0, 0), (144, 330, 300, 70), (100, 400, 0, 0),
+                                       (100, 300, 0, 0), (80, 250, 100, 10)):
+        assert attention_kernels(64, 64, hd, 16, [before], [new], dtype, window, sinks) == ["tile"], (before, new, window)
+
+
+def test_few_rows_reach_the_row_tiles():
+    for dtype in ("f32", "bf16", "f16"):
+        assert attention_kernels(4, 2, 64, 16, [153], [40], dtype) == ["rows"]
+        assert attention_kernels(64, 64, 128, 64, [2000] * 8, [1] * 8, dtype) == ["rows"]
+    assert attention_kernels(32, 32, 128, 64, [0], [1024], "f32") == ["rows"]   # q's three summands leave no room for tiles
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f16", 64), ("f32", 64), ("bf16", 256)])
+@pytest.mark.parametrize("heads,new,kernel", [(2, 32, "rows"), (64, 272, "tile")])
+def test_rows_that_see_nothing(dtype, hd, heads, new, kernel):
+    # A step's rows see their own tokens at least. A graph of it that is replayed after pages were dropped may have rows
+    # that see none: 0, lse -inf. Here the first page only is left, and the window hides it from all but the first rows.
+    e = Env(heads=heads, kv=heads, hd=hd, page=16, pages=24, seqs=2)
+    page_zero_of_nobody(e)
+    e.kv.adopt(0, list(range(1, 18)), 0, e.stream())
+    e.step([0], [new], dtype)
+    assert attention_kernels(heads, heads, hd, 16, [0], [new], dtype, 5) == [kernel]
+    qt, q64 = e.rand(new, heads, dtype)
+    q = qt.cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((new, heads), 7.0, device="cuda")
+
+    def attend(window, sinks):
+        e.kv.attend(0, q.data_ptr(), out.data_ptr(), dtype, scale=0.1, window=window, sinks=sinks, lse_ptr=lse.data_ptr(), stream=torch.cuda.current_stream().cuda_stream)
+
+    attend(5, 0)
+    torch.cuda.synchronize()
+    graphs = []
+    for window, sinks in ((5, 0), (0, 0), (5, 16)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            attend(window, sinks)
+    k, v = e.ref[0][0].values()
+    for sinks, held in ((16, np.arange(new) < 16), (0, np.zeros(new, bool))):
+        e.kv.evict(0, 1, sinks)
+        e.kv.extend([1], [1], e.stream())          # writes the page table
+        for g, (window, first) in zip(graphs, ((5, 0), (0, 0), (5, 16))):
+            want, wl, terms, mag = R.attention(q64, k, v, 0, 0.1, window, first, held)
+            for _ in range(2):
+                out.fill_(7.0)
+                lse.fill_(7.0)
+                g.replay()
+                torch.cuda.synchronize()
+                got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+                assert (np.abs(got - want) <= R.bound(want, terms, mag, new, hd, dtype)).all()
+                assert np.array_equal(np.isneginf(gl), np.isneginf(wl)) and not np.isnan(gl).any()
+                fin = np.isfinite(wl)
+                assert (np.abs(gl - wl)[fin] <= R.lse_bound(wl, mag, new, hd)[fin]).all()
+                assert (got[np.isneginf(wl)] == 0).all()
+    assert np.isneginf(wl).all()                   # the last round: nothing held at all
