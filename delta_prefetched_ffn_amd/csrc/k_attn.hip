@@ -165,8 +165,8 @@ __device__ inline f32x2 get2(const float* p) {
 //
 // Bound by the cache's bytes (4 * group products per byte). A wave asks for a piece's K and V (8 KiB
 // at head_dim 128) a step ahead; page numbers and exponents of its next 32 pieces are fetched by its
-// lanes in two loads, so a piece's address needs no memory round trip of its own. Measured, at 1, 4
-// and 56 pieces a wave (32 heads x 4 Ki tokens; 8 x 8 heads x 4 Ki; 24 x 8 heads x 4 .. 32 Ki): 4
+// lanes in two loads, so a piece's address needs no memory round trip of its own. Measured where 256
+// workgroups of 8 waves have 2, 4 and 63 pieces a wave (32 heads x 4 Ki tokens; 8 x 8 heads x 4 Ki; 24 x 8 heads x 4 .. 32 Ki): 4
 // waves 15.2, 18.7 and 196 us, 8 waves 13.5, 18.5 and 192 us, 16 waves 15.7, 20.3 and 210 us.
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_rows(AttnArgs a) {
@@ -536,8 +536,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     }
 }
 
-// Waves of a workgroup for many rows: 8, two to a SIMD at 256 registers, where q, O and the scores fit
-// (nearly, at 192 values a head); 4 at 512 registers for longer heads.
+// Waves of a workgroup for many rows: 8, two to a SIMD at 256 registers, where q, O and the scores fit; 4
+// at 512 registers for heads above 192 values, one to a SIMD, so without the half-step distance. At 192
+// values they do not quite fit: 38 (bf16) or 46 (fp16) registers are spilled, to 156 bytes of scratch a
+// lane. A causal prompt of 4 Ki tokens x 32 heads takes 136 us at 64 values, 306 us at 192 and 652 us at
+// 256, where the products at a large library product's rate would take 51, 152 and 203.
 template <int NS>
 constexpr int kTileWaves = NS <= 3 ? 8 : 4;
 
@@ -545,29 +548,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
 __device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 
-// Many rows: one workgroup of W waves per (32 W rows, kv head), 32 rows a wave, 64 tokens a step.
-//
-// Per 64 tokens a wave has 32 products of 32x32x16 (33 clocks each) and 32 exponentials a lane. Codes
-// are widened to 16 bits once per workgroup, by the wave that moved them into LDS (every wave reads
-// them all, 1 KiB of consecutive operands at a time), with V's scale folded into that conversion; the
-// products are transposed as above, so P needs no trip through LDS. The two waves of a SIMD are half a
-// step apart: one's products run beside the other's softmax and moves. Neighbouring workgroups are of
-// different kv heads, so a head's row tiles run on one die (8 divides most head counts), whose cache
-// then holds its K and V; the longest rows come first.
-//
-// Measured at head_dim 128: a causal prompt of 4 Ki tokens x 32 heads 165 us, 833 TFLOP/s (a large
-// library product reaches 1,354); 8,191 tokens x 32 over 8 heads with a window of 4 Ki 464 us, 888
-// TFLOP/s. A step takes about 4,900 clocks where its products need 2,112: a wave alone reads LDS at 33
-// bytes a clock, one operand per product's time (62 clocks for both; 33 with two waves), and the vector
-// work (masks and maxima 600, exponentials 610, widening 800 for K and 1,360 for V) of two waves
-// is longer than their products. Without the half-step distance 175 us; with codes moved by all waves at
-// the end of a step 187 us.
-//
-// Operand slots: S^T lane (half, row) holds tokens 8 (i / 4) + 4 half + i % 4, i < 16, of a 32-token
-// block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
-// V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho % 16) + 2 vt +
-// rho / 16: then the lanes that widen V write without bank conflicts, and a lane ends with runs of 16
-// consecutive values of its row.
 // x, but made where it stands: what rare paths compute from the lane is not kept in registers across
 // the loop for them.
 __device__ inline int here(int x) {
@@ -583,6 +563,29 @@ __device__ inline V settled(V x) {
     return __builtin_bit_cast(V, w);
 }
 
+// Many rows: one workgroup of W waves per (32 W rows, kv head), 32 rows a wave, 64 tokens a step.
+//
+// Per 64 tokens a wave has 32 products of 32x32x16 (33 clocks each) and 32 exponentials a lane. Codes
+// are widened to 16 bits once per workgroup, by the wave that moved them into LDS (every wave reads
+// them all, 1 KiB of consecutive operands at a time), with V's scale folded into that conversion; the
+// products are transposed as above, so P needs no trip through LDS. The two waves of a SIMD are half a
+// step apart: one's products run beside the other's softmax and moves. Neighbouring workgroups are of
+// different kv heads, so a head's row tiles run on one die (8 divides most head counts), whose cache
+// then holds its K and V; the longest rows come first.
+//
+// Measured at head_dim 128: a causal prompt of 4 Ki tokens x 32 heads 164 us, 838 TFLOP/s (a large
+// library product reaches 1,354); 8,191 tokens x 32 over 8 heads with a window of 4 Ki 466 us, 885
+// TFLOP/s. A step takes about 4,900 clocks where its products need 2,112: a wave alone reads LDS at 33
+// bytes a clock, one operand per product's time (62 clocks for both; 33 with two waves), and the vector
+// work (masks and maxima 600, exponentials 610, widening 800 for K and 1,360 for V) of two waves
+// is longer than their products. Without the half-step distance 175 us; with codes moved by all waves at
+// the end of a step 187 us.
+//
+// Operand slots: S^T lane (half, row) holds tokens 8 (i / 4) + 4 half + i % 4, i < 16, of a 32-token
+// block; so slot j of the second product is token 8 (j / 4) + 4 half + j % 4 of a 16-token group, i.e.
+// V quads half and 2 + half. Row rho of V^T tile (slab, vt) is value 64 slab + 4 (rho % 16) + 2 vt +
+// rho / 16: then the lanes that widen V write without bank conflicts, and a lane ends with runs of 16
+// consecutive values of its row.
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_tile(AttnArgs a) {
     typedef Kind<T> Kd;

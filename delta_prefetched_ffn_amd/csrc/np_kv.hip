@@ -22,9 +22,9 @@ namespace {
 
 // Attention over few rows splits the key axis into workgroups for every compute unit: one each while
 // a wave then has at most kFewPieces pieces (each further workgroup costs the launch a join), two
-// each beyond (one's start and join hide behind the other's stream). Measured at 1, 4 and 56 pieces a
-// wave: 256 workgroups 13.5, 18.5 and 216 us, 512 workgroups 20.7, 23.0 and 192 us, 1024 workgroups
-// 20.7, 33.3 and 193 us.
+// each beyond (one's start and join hide behind the other's stream). Measured where 256 workgroups
+// have 2, 4 and 63 pieces a wave: 256 workgroups 13.5, 18.5 and 216 us, 512 workgroups 20.7, 23.0 and
+// 192 us, 1024 workgroups 20.7, 33.3 and 193 us.
 constexpr int kCus = 256;
 constexpr int kFewPieces = 16;
 

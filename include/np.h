@@ -382,9 +382,11 @@ np_status np_layer_raise_error(np_layer* layer, int32_t bits, void* stream);
 
 /* ---- 8-bit key/value cache and the attention over it ----
  *
- * The attention of the decode steps that np_decode_step runs the FFNs of: keys
- * and values of past tokens in 8 bits, in pages that sequences share, so that
- * the cache leaves the device memory to the resident rows.
+ * The attention next to the sparse FFNs: keys and values of past tokens in 8
+ * bits, in pages that sequences share, so that the cache leaves the device
+ * memory to the resident rows. np_decode_step takes every layer's x at once;
+ * where attention runs between the FFNs, the layers are driven one by one
+ * (np_delta_assign, np_sparse_ffn_acc), without its prefetch.
  *
  * Format. A pool of n_pages pages of page_tokens tokens, the same page number
  * in every layer:
@@ -396,8 +398,9 @@ np_status np_layer_raise_error(np_layer* layer, int32_t bits, void* stream);
  * page, head, and K or V (the quantisation block). 1024 bytes hold 16 tokens x
  * 64 values: for K, byte (16 g + t) * 16 + b is token t, value 16 g + b; for
  * V, byte (16 g + r) * 16 + 4 i + t is token 4 g + t, value 4 r + i.
- * Values past head_dim are zero. Bytes of tokens that a sequence has not
- * reached are unspecified.
+ * Values past head_dim are zero, and held like the others: a head_dim of 40 or
+ * 80 takes 1.6 times its values' bytes, 96 takes 1.33 times. Bytes of tokens
+ * that a sequence has not reached are unspecified.
  *
  * A sequence is a list of pages and a length: token j lies in its page
  * j / page_tokens. The page lists live on the host (the library's, exact) and
@@ -412,7 +415,9 @@ np_status np_layer_raise_error(np_layer* layer, int32_t bits, void* stream);
  * tokens in the order of np_kv_extend: the first sequence's, then the
  * second's. Calls of one cache must be ordered (one stream, or the caller's
  * events) and are not thread-safe; different caches are independent. Calls
- * that a graph captures replay with the sequences and lengths of the capture.
+ * that a graph captures replay with the sequences and lengths of the capture;
+ * np_kv_extend, np_kv_fork and np_kv_compact stay out of graphs (a replay would
+ * write the capture's pages and page lists again).
  * After NP_EHIP from a call that changes the cache, np_kv_reset is needed
  * (NP_ESTATE until then). Limits: 1 <= n_layers <= 1024, 1 <= n_kv_heads <=
  * 1024, n_heads a multiple of it and <= 4096, head_dim a multiple of 8 in
@@ -491,11 +496,15 @@ np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, i
  *   s_j = scale * q . k_j,   out = sum exp(s_j) v_j / sum exp(s_j).
  * Token j is visible if j <= i, its page is held (np_kv_evict), and, with
  * window > 0, i - j < window or j < sinks: a sliding window with a few first
- * tokens that stay visible. A row without a visible token gives 0 (lse -inf).
+ * tokens that stay visible. A row without a visible token gives 0 (lse -inf);
+ * a step's rows see their own tokens at least, so this takes a graph that is
+ * replayed after their pages were dropped. A row whose visible scores are all
+ * -inf gives NaN.
  * q, out [rows][n_heads][head_dim] of dtype, 16-byte aligned; strides as
  * above: q's row and head stride, then out's (whose elements must not
- * overlap). lse, fp32 [rows][n_heads], receives ln sum exp(s_j) (NULL: not).
- * Sums and softmax statistics are fp32; K and V enter exactly (V scales of
+ * overlap, nor lie in q). lse, fp32 [rows][n_heads], receives ln sum exp(s_j) (NULL: not).
+ * Sums and softmax statistics are fp32 (sums of values above 2^120 / tokens may
+ * overflow); K and V enter exactly (V scales of
  * one head that lie more than 2^40 below the largest vanish); the weights
  * exp(s_j) are kept to 24 bits for NP_F32 and rounded to fp16 for 16-bit
  * dtypes: off by 2^-11 of themselves or 2^-32 of the row's largest, whichever
