@@ -633,6 +633,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
         ahead_at = reinterpret_cast<uint64_t>(codes + max(page, 0) * kv.page_bytes + (int64_t)2 * h * side_bytes +
                                               (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes));
         asm volatile("" : "+v"(ahead_exps));  // waited for here
+        // A group that is not held has page 0's codes, whose exponent the unit knows nothing of. Its weights are 0, but
+        // codes that overflow would be infinities, and 0 times those NaN: the lowest exponent keeps them small.
+        if (page < 0) ahead_exps = 0x8000;
     };
     fetch(0);
 
@@ -720,10 +723,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
                 int side, g, c;
                 tile_at(j, side, g, c);
                 if (side == 0) continue;
-                const int u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
-                // A group that is not held has page 0's codes, whose exponent the unit knows nothing of: they are taken
-                // at the unit. Its weights are 0, but codes that overflow would be infinities, and 0 times those NaN.
-                const int e = holds >> g & 1 ? __builtin_amdgcn_readlane(my_ev, from + g) : u;
+                const int e = __builtin_amdgcn_readlane(my_ev, from + g), u = g < 2 ? (g ? un[1] : un[0]) : g == 2 ? un[2] : un[3];
                 const int quad = lane >> 4, r = lane & 15;
                 uint32_t bad = 0;
 #pragma unroll
