@@ -573,8 +573,8 @@ __device__ inline V settled(V x) {
 // different kv heads, so a head's row tiles run on one die (8 divides most head counts), whose cache
 // then holds its K and V; the longest rows come first.
 //
-// Measured at head_dim 128: a causal prompt of 4 Ki tokens x 32 heads 164 us, 838 TFLOP/s (a large
-// library product reaches 1,354); 8,191 tokens x 32 over 8 heads with a window of 4 Ki 466 us, 885
+// Measured at head_dim 128: a causal prompt of 4 Ki tokens x 32 heads 165 us, 833 TFLOP/s (a large
+// library product reaches 1,354); 8,191 tokens x 32 over 8 heads with a window of 4 Ki 461 us, 895
 // TFLOP/s. A step takes about 4,900 clocks where its products need 2,112: a wave alone reads LDS at 33
 // bytes a clock, one operand per product's time (62 clocks for both; 33 with two waves), and the vector
 // work (masks and maxima 600, exponentials 610, widening 800 for K and 1,360 for V) of two waves
