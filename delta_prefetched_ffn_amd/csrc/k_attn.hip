@@ -123,6 +123,12 @@ __device__ inline Pieces pieces_of(int pos_lo, int pos_hi, int window, int sinks
     return p;
 }
 
+// Whether any row at positions pos_lo .. pos_hi sees any of the 16 tokens from t on. A group that none
+// sees is treated as one that is not held: its values' scale must not decide what the others keep.
+__device__ inline bool group_seen(const AttnArgs& a, int t, int pos_lo, int pos_hi) {
+    return t <= pos_hi && (!a.window || pos_lo - (t + 15) < a.window || t < a.sinks);
+}
+
 // Adds a part (maximum mp, sum lp, values v) to a row's join at the maximum mm >= mp. A part that
 // saw no token (mp = -inf, lp = 0) adds nothing, whatever mm is.
 __device__ inline void join(f32x4& x, float& ll, float mm, float mp, float lp, f32x4 v) {
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     int ahead_page = -1, ahead_exps = 0;
     const auto fetch_pages = [&](int n0) {
         const int n = n0 + (lane >> 1), t = n < count ? token_of(n) + 16 * (lane & 1) : pos_hi + 1;
-        ahead_page = t <= pos_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
+        ahead_page = group_seen(a, t, pos_lo, pos_hi) ? page_of(kv, seq, t >> kv.page_shift) : -1;
     };
     const auto fetch_exps = [&] {
         ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(ahead_page, 0) * kv.n_kv + h) * 2);
@@ -627,7 +633,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
     bool ahead_held = false;
     const auto fetch = [&](int n0) __attribute__((always_inline)) {
         const int own = here(lane), n = n0 + (own >> 2), t = n < steps ? token_of(n) + 16 * (own & 3) : wg_hi + 1;
-        const int page = t <= wg_hi ? page_of(kv, seq, t >> kv.page_shift) : -1;
+        const int page = group_seen(a, t, wg_lo, wg_hi) ? page_of(kv, seq, t >> kv.page_shift) : -1;
         ahead_held = page >= 0;
         ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(page, 0) * kv.n_kv + h) * 2);
         ahead_at = reinterpret_cast<uint64_t>(codes + max(page, 0) * kv.page_bytes + (int64_t)2 * h * side_bytes +

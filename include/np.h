@@ -504,11 +504,11 @@ np_status np_kv_append(np_kv* kv, int32_t layer, const void* k, const void* v, i
  * above: q's row and head stride, then out's (whose elements must not
  * overlap, nor lie in q). lse, fp32 [rows][n_heads], receives ln sum exp(s_j) (NULL: not).
  * Sums and softmax statistics are fp32 (sums of values above 2^120 / tokens may
- * overflow); K and V enter exactly (V scales of
- * one head that lie more than 2^40 below the largest vanish); the weights
- * exp(s_j) are kept to 24 bits for NP_F32 and rounded to fp16 for 16-bit
- * dtypes: off by 2^-11 of themselves or 2^-32 of the row's largest, whichever
- * is more. Results are the same from run to run.
+ * overflow); K and V enter exactly (V scales of one head that lie more than
+ * 2^40 below the largest among the tokens that up to 256 neighbouring rows see
+ * may vanish); the weights exp(s_j) are kept to 24 bits for NP_F32 and rounded
+ * to fp16 for 16-bit dtypes: off by 2^-11 of themselves or 2^-32 of the row's
+ * largest, whichever is more. Results are the same from run to run.
  * Errors: NP_EINVAL (scale not positive and finite, a negative window; more
  * than 2^30 rows x heads, or 2^27 of one key/value head where they run 16 at
  * a time), NP_ESTATE (no current tokens). */

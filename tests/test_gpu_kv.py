@@ -757,6 +757,21 @@ def test_rows_that_see_nothing(dtype, hd, heads, new, kernel):
                 assert (np.abs(got - want) <= R.bound(want, terms, mag, new, hd, dtype)).all()
                 assert np.array_equal(np.isneginf(gl), np.isneginf(wl)) and not np.isnan(gl).any()
                 fin = np.isfinite(wl)
-                assert (np.abs(gl - wl)[fin] <= R.lse_bound(wl, mag, new, hd)[fin]).all()
+                assert (np.abs(gl[fin] - wl[fin]) <= R.lse_bound(wl, mag, new, hd)[fin]).all()
                 assert (got[np.isneginf(wl)] == 0).all()
     assert np.isneginf(wl).all()                   # the last round: nothing held at all
+
+
+@pytest.mark.parametrize("dtype,hd", [("f32", 64), ("bf16", 128), ("f16", 64), ("bf16", 256), ("f16", 192)])
+@pytest.mark.parametrize("heads,new,kernel", [(2, 1, "rows"), (2, 3, "rows"), (64, 300, "tile")])
+def test_values_that_no_row_sees_do_not_set_the_scale(dtype, hd, heads, new, kernel):
+    # Behind the first tokens and before the window lie pages whose values are 2^80 larger; no row of the call sees them.
+    e = Env(heads=heads, kv=heads, hd=hd, page=16, pages=34, seqs=1)
+    assert attention_kernels(heads, heads, hd, 16, [200], [new], dtype, 89, 4) == [kernel]
+    k, v = (e.rng.standard_normal((200 + new, heads, hd)).astype(np.float32) for _ in range(2))
+    v[16:112] *= 2.0 ** 80                # row 200 sees tokens 112 on
+    for lo, hi in ((0, 200), (200, 200 + new)):
+        e.extend([0], [hi - lo])
+        kt, vt = torch.from_numpy(k[lo:hi]), torch.from_numpy(v[lo:hi])
+        e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    e.attend(dtype, window=89, sinks=4)
