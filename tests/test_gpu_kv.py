@@ -775,3 +775,25 @@ def test_values_that_no_row_sees_do_not_set_the_scale(dtype, hd, heads, new, ker
         kt, vt = torch.from_numpy(k[lo:hi]), torch.from_numpy(v[lo:hi])
         e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
     e.attend(dtype, window=89, sinks=4)
+
+
+@pytest.mark.parametrize("dtype,hd", [("f32", 64), ("bf16", 128), ("f16", 64), ("bf16", 256), ("f16", 192)])
+@pytest.mark.parametrize("heads,new,kernel", [(2, 150, "rows"), (64, 300, "tile")])
+def test_later_values_of_another_scale_leave_earlier_rows_alone(dtype, hd, heads, new, kernel):
+    # Rows 0 .. 95 share tiles with rows that see values 2^80 larger, and do not see them.
+    e = Env(heads=heads, kv=heads, hd=hd, page=16, pages=24, seqs=1)
+    assert attention_kernels(heads, heads, hd, 16, [0], [new], dtype) == [kernel]
+    e.extend([0], [new])
+    k, v = (e.rng.standard_normal((new, heads, hd)).astype(np.float32) for _ in range(2))
+    v[96:130] *= 2.0 ** 80
+    kt, vt = torch.from_numpy(k), torch.from_numpy(v)
+    e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
+    q, q64 = e.rand(new, heads, dtype)
+    out = torch.empty((new, heads, hd), dtype=tdt(dtype), device="cuda")
+    qd = q.cuda()
+    e.kv.attend(0, qd.data_ptr(), out.data_ptr(), dtype, scale=1 / math.sqrt(hd), stream=e.stream())
+    rk, rv = e.ref[0][0].values()
+    want, _, terms, mag = R.attention(q64[:96], rk[:96], rv[:96], 0, 1 / math.sqrt(hd))
+    err = np.abs(out.double().cpu().numpy()[:96] - want)
+    tol = R.bound(want, terms, mag, 96, hd, dtype)
+    assert (err <= tol).all(), f"worst {np.max(err / tol):.2f} bounds"
