@@ -30,6 +30,8 @@ ACTS = {"relu": ACT_RELU, "silu": ACT_SILU}
 DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
 KV_HOST = -1
 KV_MODES = {"share": 0, "copy": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "blend": 3}
 _NAMES = {0: "NP_OK", 1: "NP_EINVAL", 2: "NP_ECAPACITY", 3: "NP_ENOMEM", 4: "NP_EHIP",
           5: "NP_ESTATE", 6: "NP_EDEVICE"}
 
@@ -43,7 +45,8 @@ EXPORTS = ["np_layer_create", "np_layer_destroy", "np_layer_reset", "np_delta_as
            "np_layer_set_planar", "np_sparse_ffn_noalloc",
            "np_kv_bytes", "np_kv_create", "np_kv_destroy", "np_kv_reset", "np_kv_extend", "np_kv_append",
            "np_kv_attend", "np_kv_fork", "np_kv_trim", "np_kv_free", "np_kv_adopt", "np_kv_evict",
-           "np_kv_compact", "np_kv_read_pages", "np_kv_read_tokens", "np_kv_info"]
+           "np_kv_compact", "np_kv_read_pages", "np_kv_read_tokens", "np_kv_info",
+           "np_rope_freqs", "np_rope_create", "np_rope_destroy", "np_rope_apply", "np_rope_append"]
 
 
 class NPError(RuntimeError):
@@ -63,6 +66,12 @@ class KVDesc(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int32) for k in ("n_layers", "n_heads", "n_kv_heads", "head_dim", "page_tokens", "n_pages",
                                               "max_seqs", "max_pages", "device")] + \
                [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("head_dim", "rot_dim", "layout", "scaling")] + \
+               [("base", ctypes.c_double), ("factor", ctypes.c_double), ("context", ctypes.c_int64), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("freqs", ctypes.c_void_p), ("amplitude", ctypes.c_float), ("device", ctypes.c_int32)]
 
 
 @lru_cache(maxsize=1)
@@ -115,6 +124,11 @@ def lib() -> ctypes.CDLL:
         "np_kv_read_pages": [vp, i32, vp, i32, vp, vp],
         "np_kv_read_tokens": [vp, i32, i32, i32, i32, vp, vp],
         "np_kv_info": [vp, vp],
+        "np_rope_freqs": [ctypes.POINTER(RopeDesc), vp],
+        "np_rope_create": [ctypes.POINTER(RopeDesc), ctypes.POINTER(vp)],
+        "np_rope_destroy": [vp],
+        "np_rope_apply": [vp, i64, vp, i32, vp, vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, i32, vp, vp],
+        "np_rope_append": [vp, vp, i32, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -417,6 +431,98 @@ class KVCache:
         out = (ctypes.c_int32 * 4)()
         _check(lib().np_kv_info(self.h, out))
         return dict(zip(["n_pages", "free", "shared", "current"], list(out)))
+
+
+def _rope_desc(head_dim, rot_dim, layout, base, scaling, factor, context, low, high, freqs, amplitude, device):
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    if freqs is not None:
+        freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+        if freqs.shape != (rot_dim // 2,):
+            raise ValueError(f"freqs: {freqs.shape} numbers instead of {rot_dim // 2}")
+    if not -(1 << 63) <= context < 1 << 63:
+        raise OverflowError(f"{context} does not fit in 64 bits")
+    return RopeDesc(_i32(head_dim), _i32(rot_dim), ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], base, factor, context, low, high,
+                    _ptr(freqs), amplitude, _i32(device)), freqs
+
+
+def rope_freqs(*, head_dim: int, rot_dim: int | None = None, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               context: int = 0, low: float = 0.0, high: float = 0.0) -> np.ndarray:
+    """What each pair of a Rope turns by per position, in radians (fp64 [rot_dim / 2])."""
+    desc, _ = _rope_desc(head_dim, rot_dim, "half", base, scaling, factor, context, low, high, None, 1.0, 0)
+    out = np.empty(max(0, desc.rot_dim) // 2, dtype=np.float64)
+    _check(lib().np_rope_freqs(ctypes.byref(desc), out.ctypes.data))
+    return out
+
+
+class _Strides:
+    """Stride tuples in use as C arrays, looked up once: the calls that take them run for every layer and token."""
+
+    def __init__(self, n: int):
+        self.n, self.made = n, {None: None}
+
+    def __call__(self, strides):
+        try:
+            return self.made[strides]
+        except (KeyError, TypeError):   # new ones, or a list
+            given = array.array("q", strides)
+            if len(given) != self.n:
+                raise ValueError(f"strides: {len(given)} numbers instead of {self.n}")
+            if len(self.made) > 64:
+                self.made = {None: None}
+            return self.made.setdefault(tuple(given), (ctypes.c_int64 * self.n)(*given))
+
+
+class Rope:
+    """Rotary positions (np_rope). rot_dim None: the whole head; freqs: the pairs' radians per position instead of base and
+    scaling."""
+
+    def __init__(self, *, head_dim: int, rot_dim: int | None = None, layout: str = "half", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, context: int = 0, low: float = 0.0, high: float = 0.0,
+                 freqs=None, amplitude: float = 1.0, device: int = 0):
+        desc, keep = _rope_desc(head_dim, rot_dim, layout, base, scaling, factor, context, low, high, freqs, amplitude, device)
+        h = ctypes.c_void_p()
+        _check(lib().np_rope_create(ctypes.byref(desc), ctypes.byref(h)))
+        del keep   # read by the call
+        self.h = h
+        self.head_dim, self.rot_dim = desc.head_dim, desc.rot_dim
+        self._apply, self._append, self._strides = lib().np_rope_apply, lib().np_rope_append, _Strides(8)
+
+    def close(self) -> None:
+        if self.h:
+            _check(lib().np_rope_destroy(self.h))
+            self.h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            if getattr(self, "h", None):
+                lib().np_rope_destroy(self.h)
+        except Exception:
+            pass
+
+    def apply(self, rows: int, q_ptr: int, q_out_ptr: int, n_heads: int, dtype: str, strides=None, *, k_ptr: int = 0,
+              k_out_ptr: int = 0, n_kv_heads: int = 0, positions_ptr: int = 0, first: int = 0, q_weight_ptr: int = 0,
+              k_weight_ptr: int = 0, eps: float = 1e-6, stream: int = 0) -> None:
+        """q [rows][n_heads][head_dim] (and k) normalised where weights are given, and turned by their rows' positions (device
+        int32 [rows], or first, first + 1, ...); strides (elements): row and head of q, q_out, k, k_out."""
+        if not -(1 << 63) <= rows < 1 << 63:
+            raise OverflowError(f"{rows} does not fit in 64 bits")
+        for x in (first, n_heads, n_kv_heads):
+            _i32(x)
+        rc = self._apply(self.h, rows, positions_ptr or None, first, q_ptr, q_out_ptr, n_heads, q_weight_ptr or None, k_ptr or None,
+                         k_out_ptr or None, n_kv_heads, k_weight_ptr or None, eps, DTYPES[dtype], self._strides(strides), stream or None)
+        if rc:
+            _check(rc)
+
+    def append(self, kv: KVCache, layer: int, q_ptr: int, q_out_ptr: int, k_ptr: int, v_ptr: int, dtype: str, strides=None, *,
+               q_weight_ptr: int = 0, k_weight_ptr: int = 0, eps: float = 1e-6, stream: int = 0) -> None:
+        """The cache's current tokens: q normalised and turned into q_out; k, normalised and turned, and v stored in the cache;
+        strides (elements): row and head of q, q_out, k, v."""
+        if layer >> 31 > 0:
+            _i32(layer)
+        rc = self._append(self.h, kv.h, layer, q_ptr, q_out_ptr, k_ptr, v_ptr, q_weight_ptr or None, k_weight_ptr or None, eps,
+                          DTYPES[dtype], self._strides(strides), stream or None)
+        if rc:
+            _check(rc)
 
 
 def decode_step(layers, cids: np.ndarray, x_ptr: int, y_ptr: int, compute_stream: int = 0,

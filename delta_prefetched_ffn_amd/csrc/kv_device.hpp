@@ -21,7 +21,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 __device__ inline float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // The sequence of a work item: the number of sequences that end at or before it.
-__device__ inline int find_item(const KvBatch& b, int item) {
+template <typename Batch>
+__device__ inline int find_item(const Batch& b, int item) {
     if (b.n == 1) return 0;
     int c = 0;
     const int lane = threadIdx.x & 63;

@@ -557,6 +557,80 @@ np_status np_kv_read_tokens(const np_kv* kv, int32_t layer, int32_t seq, int32_t
  * the current step}. */
 np_status np_kv_info(const np_kv* kv, int32_t* out4);
 
+/* ---- rotary positions, with the norms of queries and keys ----
+ *
+ * For a head x of head_dim values at position p: first, where weights are
+ * given, x * weight / sqrt(mean(x^2) + eps) over the whole head; then, of its
+ * first rot_dim values, pair i turns by p * f_i radians,
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos);
+ * values from rot_dim on stay as they are. Computed in fp32 and rounded once;
+ * the angle is exact to 2^-34 turns at any 32-bit position (f_i is held as a
+ * 64-bit fraction of a turn). Squares are summed in fp32: a norm of values
+ * above 2^59 overflows. Not-a-number and infinite values spread as in the
+ * formulas (within their head). */
+typedef struct np_rope np_rope; /* opaque: one rotation, read-only after create */
+
+/* Pair i: values i and i + rot_dim / 2, or values 2 i and 2 i + 1. */
+typedef enum { NP_ROPE_HALF = 0, NP_ROPE_INTERLEAVED = 1 } np_rope_layout;
+
+/* f_i = base^(-2 i / rot_dim); LINEAR: f_i / factor (positions squeezed); NTK:
+ * of the base base * factor^(rot_dim / (rot_dim - 2)), which divides the
+ * slowest pair's by factor and keeps the fastest's; BLEND: with n_i = context * f_i
+ * / (2 pi) turns of the pair over the trained context, f_i / factor where
+ * n_i <= low, f_i where n_i >= high, and g f_i + (1 - g) f_i / factor with
+ * g = (n_i - low) / (high - low) between. */
+typedef enum { NP_ROPE_PLAIN = 0, NP_ROPE_LINEAR = 1, NP_ROPE_NTK = 2, NP_ROPE_BLEND = 3 } np_rope_scaling;
+
+typedef struct np_rope_desc {
+    int32_t head_dim;    /* a multiple of 8 in [8, 256]                      */
+    int32_t rot_dim;     /* even, 0 (norms only) .. head_dim                 */
+    int32_t layout;      /* np_rope_layout                                   */
+    int32_t scaling;     /* np_rope_scaling                                  */
+    double base;         /* positive, e.g. 10000                             */
+    double factor;       /* positive; not used by PLAIN                      */
+    int64_t context;     /* BLEND: positions of the trained context          */
+    double low, high;    /* BLEND, low < high                                */
+    const double* freqs; /* host [rot_dim / 2]: f_i themselves, any finite
+                            numbers (the fields above are then not used); or
+                            NULL. Read, not kept.                            */
+    float amplitude;     /* positive; 1 unless the scaling asks for another  */
+    int32_t device;      /* HIP device ordinal                               */
+} np_rope_desc;
+
+/* f_i of a descriptor (host [rot_dim / 2]). NP_EINVAL as np_rope_create; the
+ * device is not looked at. */
+np_status np_rope_freqs(const np_rope_desc* desc, double* freqs);
+
+/* Errors: NP_EINVAL, NP_ENOMEM, NP_EHIP; *out is NULL on any error. destroy
+ * synchronizes the device. A rope may be used from several threads and streams
+ * at once. */
+np_status np_rope_create(const np_rope_desc* desc, np_rope** out);
+np_status np_rope_destroy(np_rope* rope);
+
+/* Normalises and turns q [rows][n_heads][head_dim] into q_out and, with
+ * n_kv_heads > 0, k [rows][n_kv_heads][head_dim] into k_out, all of dtype,
+ * 16-byte aligned. positions: device int32 [rows], any values; NULL: row r is at
+ * first + r. q_weight, k_weight: device fp32 [head_dim], 16-byte aligned; NULL: no
+ * norm. strides (host, in elements, multiples of 16 bytes; NULL: contiguous): row
+ * and head stride of q, q_out, k, k_out. A result may be its input itself (same
+ * address and strides), and must not overlap any input in another way, nor
+ * itself or the other result. rows 0 enqueues nothing.
+ * Errors: NP_EINVAL (also rows above 2^28, or more waves than a launch holds: 2^26). */
+np_status np_rope_apply(const np_rope* rope, int64_t rows, const int32_t* positions, int32_t first, const void* q, void* q_out,
+                        int32_t n_heads, const float* q_weight, const void* k, void* k_out, int32_t n_kv_heads,
+                        const float* k_weight, float eps, int32_t dtype, const int64_t* strides, void* stream);
+
+/* np_rope_apply and np_kv_append in one launch, for the cache's current tokens
+ * (np_kv_extend): q [rows][n_heads][head_dim] is normalised and turned into q_out, k
+ * normalised, turned and, as v, stored in the cache as np_kv_append stores it (from
+ * the fp32 results, without a rounding to dtype in between). A row's position is its
+ * token's index in its sequence. strides: row and head stride of q, q_out, k, v (NULL:
+ * contiguous). The rope's and the cache's device and head_dim must be the same.
+ * Errors: as np_kv_append and np_rope_apply. */
+np_status np_rope_append(const np_rope* rope, np_kv* kv, int32_t layer, const void* q, void* q_out, const void* k,
+                         const void* v, const float* q_weight, const float* k_weight, float eps, int32_t dtype,
+                         const int64_t* strides, void* stream);
+
 /* ---- measurement probes (roofline denominators and counter scaling) ---- */
 
 /* Streaming read of `bytes` (multiple of 16) at src (device or pinned host);
