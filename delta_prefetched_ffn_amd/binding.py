@@ -46,7 +46,8 @@ EXPORTS = ["np_layer_create", "np_layer_destroy", "np_layer_reset", "np_delta_as
            "np_kv_bytes", "np_kv_create", "np_kv_destroy", "np_kv_reset", "np_kv_extend", "np_kv_append",
            "np_kv_attend", "np_kv_fork", "np_kv_trim", "np_kv_free", "np_kv_adopt", "np_kv_evict",
            "np_kv_compact", "np_kv_read_pages", "np_kv_read_tokens", "np_kv_info",
-           "np_rope_freqs", "np_rope_create", "np_rope_destroy", "np_rope_apply", "np_rope_append"]
+           "np_rope_freqs", "np_rope_create", "np_rope_destroy", "np_rope_apply", "np_rope_append",
+           "np_w4_create", "np_w4_destroy", "np_w4_matvec"]
 
 
 class NPError(RuntimeError):
@@ -72,6 +73,11 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int32) for k in ("head_dim", "rot_dim", "layout", "scaling")] + \
                [("base", ctypes.c_double), ("factor", ctypes.c_double), ("context", ctypes.c_int64), ("low", ctypes.c_double),
                 ("high", ctypes.c_double), ("freqs", ctypes.c_void_p), ("amplitude", ctypes.c_float), ("device", ctypes.c_int32)]
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("n_out", "n_in", "group", "scale_dtype", "device")] + \
+               [(k, ctypes.c_void_p) for k in ("codes", "scales", "zeros")]
 
 
 @lru_cache(maxsize=1)
@@ -129,6 +135,9 @@ def lib() -> ctypes.CDLL:
         "np_rope_destroy": [vp],
         "np_rope_apply": [vp, i64, vp, i32, vp, vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, i32, vp, vp],
         "np_rope_append": [vp, vp, i32, vp, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp],
+        "np_w4_create": [ctypes.POINTER(W4Desc), ctypes.POINTER(vp)],
+        "np_w4_destroy": [vp],
+        "np_w4_matvec": [vp, i64, vp, i32, i64, vp, i32, i64, i32, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -521,6 +530,44 @@ class Rope:
             _i32(layer)
         rc = self._append(self.h, kv.h, layer, q_ptr, q_out_ptr, k_ptr, v_ptr, q_weight_ptr or None, k_weight_ptr or None, eps,
                           DTYPES[dtype], self._strides(strides), stream or None)
+        if rc:
+            _check(rc)
+
+
+class W4:
+    """A matrix of 4-bit weights (np_w4). codes uint8 [n_out][n_in / 2], scales [n_out][ceil(n_in / group)] of scale_dtype and
+    zeros uint8 of the same shape (0: 8 everywhere) are device pointers (ints) that are read here and not kept."""
+
+    def __init__(self, *, n_out: int, n_in: int, group: int, codes_ptr: int, scales_ptr: int, scale_dtype: str, zeros_ptr: int = 0,
+                 device: int = 0):
+        desc = W4Desc(_i32(n_out), _i32(n_in), _i32(group), DTYPES[scale_dtype], _i32(device), codes_ptr or None, scales_ptr or None,
+                      zeros_ptr or None)
+        h = ctypes.c_void_p()
+        _check(lib().np_w4_create(ctypes.byref(desc), ctypes.byref(h)))
+        self.h = h
+        self.n_out, self.n_in = n_out, n_in
+        self._matvec = lib().np_w4_matvec
+
+    def close(self) -> None:
+        if self.h:
+            _check(lib().np_w4_destroy(self.h))
+            self.h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            if getattr(self, "h", None):
+                lib().np_w4_destroy(self.h)
+        except Exception:
+            pass
+
+    def matvec(self, rows: int, x_ptr: int, x_dtype: str, y_ptr: int, y_dtype: str, *, x_stride: int = 0, y_stride: int = 0,
+               accumulate: bool = False, stream: int = 0) -> None:
+        """y [rows][n_out] = x [rows][n_in] times the weights (accumulate: added to y); strides in elements, 0: contiguous."""
+        for n in (rows, x_stride, y_stride):
+            if not -(1 << 63) <= n < 1 << 63:
+                raise OverflowError(f"{n} does not fit in 64 bits")
+        rc = self._matvec(self.h, rows, x_ptr, DTYPES[x_dtype], x_stride, y_ptr, DTYPES[y_dtype], y_stride, 1 if accumulate else 0,
+                          stream or None)
         if rc:
             _check(rc)
 

@@ -16,7 +16,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "kv_device.hpp"
+#include "mfma_device.hpp"
 
 namespace np {
 namespace {
@@ -49,53 +49,6 @@ struct Kind<float> {
     typedef __bf16 P;
     static constexpr int kQ = 3, kP = 3, kLift = 0;
 };
-
-template <typename E>
-struct Vec8;
-template <>
-struct Vec8<__bf16> {
-    typedef bf16x8 t;
-};
-template <>
-struct Vec8<_Float16> {
-    typedef f16x8 t;
-};
-
-__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-__device__ inline f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-
-// Eight e4m3 codes (two dwords), each dword times its scale 2^k, to eight 16-bit floats: exact in
-// bf16, exact in fp16 while the product stays within its normal range.
-template <typename E>
-__device__ inline typename Vec8<E>::t widen(uint32_t a, uint32_t b, float sa, float sb);
-template <>
-__device__ inline bf16x8 widen<__bf16>(uint32_t a, uint32_t b, float sa, float sb) {
-    const bf16x2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sa, false), y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sa, true);
-    const bf16x2 z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sb, false), w = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sb, true);
-    return bf16x8{x[0], x[1], y[0], y[1], z[0], z[1], w[0], w[1]};
-}
-template <>
-__device__ inline f16x8 widen<_Float16>(uint32_t a, uint32_t b, float sa, float sb) {
-    const f16x2 x = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, sa, false), y = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, sa, true);
-    const f16x2 z = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, sb, false), w = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, sb, true);
-    return f16x8{x[0], x[1], y[0], y[1], z[0], z[1], w[0], w[1]};
-}
-
-// x[8] as `N` summands of type E, each the rounding of what the ones before left.
-template <typename E, int N>
-__device__ inline void split(typename Vec8<E>::t* o, const float* x) {
-    float r[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = x[k];
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const E e = (E)r[k];
-            o[n][k] = e;
-            if (n + 1 < N) r[k] = r[k] - (float)e;
-        }
-}
 
 constexpr int kRows = kRowTile;      // query rows of a tile
 constexpr int kPiece = kPieceTokens;  // tokens of one step
@@ -549,10 +502,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 // 256, where the products at a large library product's rate would take 51, 152 and 203.
 template <int NS>
 constexpr int kTileWaves = NS <= 3 ? 8 : 4;
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-__device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
-__device__ inline f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 
 // x, but made where it stands: what rare paths compute from the lane is not kept in registers across
 // the loop for them.

@@ -631,6 +631,53 @@ np_status np_rope_append(const np_rope* rope, np_kv* kv, int32_t layer, const vo
                          const void* v, const float* q_weight, const float* k_weight, float eps, int32_t dtype,
                          const int64_t* strides, void* stream);
 
+/* ---- products with 4-bit weights ----
+ *
+ * The dense projections next to the sparse FFNs, at a quarter of their bf16
+ * bytes. A weight is a code c in 0 .. 15 with its group's scale and zero point,
+ *   w[o][i] = scale[o][i / group] * (c[o][i] - zero[o][i / group]),
+ * and y[r][o] = sum_i w[o][i] x[r][i]. Codes, zero points and x enter exactly;
+ * per group, the fp32 sums of c x and of x are joined to sum (c - zero) x and times
+ * the scale in fp32, groups are summed in fp32, and y is rounded once. Sums of
+ * c x above fp32's range overflow even where the scale would bring them back. Results are
+ * the same from run to run; a row's bits may differ between calls with other
+ * numbers of rows. */
+typedef struct np_w4 np_w4; /* opaque: one weight matrix, read-only after create */
+
+typedef struct np_w4_desc {
+    int32_t n_out;        /* 1 .. 2^20                                        */
+    int32_t n_in;         /* a multiple of 8 in [8, 2^17]                     */
+    int32_t group;        /* inputs of a group: 32, 64, or a multiple of 128 up
+                             to 2^17 (n_in and above: one group). The last one of
+                             a row may be shorter.                            */
+    int32_t scale_dtype;  /* np_dtype of the scales                           */
+    int32_t device;       /* HIP device ordinal                               */
+    /* Memory the device can reach, read by np_w4_create and not kept. */
+    const void* codes;    /* uint8 [n_out][n_in / 2], 4-byte aligned: input 2 i in
+                             the low 4 bits of byte i, input 2 i + 1 in the high */
+    const void* scales;   /* [n_out][ceil(n_in / group)]                      */
+    const uint8_t* zeros; /* the same shape, 0 .. 15 (higher bits are ignored);
+                             NULL: 8 everywhere                               */
+} np_w4_desc;
+
+/* Lays the weights out in device memory of the library's own: n_out * n_in / 2
+ * bytes and the scales and zero points, n_out rounded up to 16 and n_in to 128.
+ * Synchronizes the device (before, so that the sources may come from any stream, and after).
+ * Errors: NP_EINVAL, NP_ENOMEM, NP_EHIP; *out is NULL on any error. destroy
+ * synchronizes the device. A matrix may be used from several threads and streams
+ * at once. */
+np_status np_w4_create(const np_w4_desc* desc, np_w4** out);
+np_status np_w4_destroy(np_w4* w);
+
+/* y[r][o] (accumulate 1: y[r][o] +=) sum_i w[o][i] x[r][i], r < rows: x [rows][n_in]
+ * of x_dtype, 16-byte aligned, its row stride (elements; 0: n_in) a multiple of 16
+ * bytes; y [rows][n_out] of y_dtype, its row stride 0 (n_out) or at least n_out. x
+ * and y must not overlap (columns of the same rows may be either's). rows 0 enqueues
+ * nothing. Allocates nothing.
+ * Errors: NP_EINVAL (also rows above 2^20, or workgroups beyond a launch). */
+np_status np_w4_matvec(const np_w4* w, int64_t rows, const void* x, int32_t x_dtype, int64_t x_row, void* y, int32_t y_dtype,
+                       int64_t y_row, int32_t accumulate, void* stream);
+
 /* ---- measurement probes (roofline denominators and counter scaling) ---- */
 
 /* Streaming read of `bytes` (multiple of 16) at src (device or pinned host);
