@@ -46,7 +46,7 @@ EXPORTS = ["np_layer_create", "np_layer_destroy", "np_layer_reset", "np_delta_as
            "np_kv_bytes", "np_kv_create", "np_kv_destroy", "np_kv_reset", "np_kv_extend", "np_kv_append",
            "np_kv_attend", "np_kv_fork", "np_kv_trim", "np_kv_free", "np_kv_adopt", "np_kv_evict",
            "np_kv_compact", "np_kv_read_pages", "np_kv_read_tokens", "np_kv_info",
-           "np_rope_freqs", "np_rope_create", "np_rope_destroy", "np_rope_apply", "np_rope_append",
+           "np_attend_shared", "np_rope_freqs", "np_rope_create", "np_rope_destroy", "np_rope_apply", "np_rope_append",
            "np_w4_create", "np_w4_destroy", "np_w4_matvec"]
 
 
@@ -130,6 +130,7 @@ def lib() -> ctypes.CDLL:
         "np_kv_read_pages": [vp, i32, vp, i32, vp, vp],
         "np_kv_read_tokens": [vp, i32, i32, i32, i32, vp, vp],
         "np_kv_info": [vp, vp],
+        "np_attend_shared": [vp, i32, vp, vp, vp, i32, vp, ctypes.c_float, i32, i32, vp],
         "np_rope_freqs": [ctypes.POINTER(RopeDesc), vp],
         "np_rope_create": [ctypes.POINTER(RopeDesc), ctypes.POINTER(vp)],
         "np_rope_destroy": [vp],
@@ -376,6 +377,17 @@ class KVCache:
                 _i32(x)
         rc = self._attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
                           window, sinks, stream or None)
+        if rc:
+            _check(rc)
+
+    def attend_shared(self, layer: int, q_ptr: int, out_ptr: int, dtype: str, strides=None, *, scale: float, window: int = 0,
+                      sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
+        """attend(), with first pages that several sequences of the step share (fork) read once for all of them."""
+        if (layer | window | sinks) >> 31 > 0:
+            for x in (layer, window, sinks):
+                _i32(x)
+        rc = lib().np_attend_shared(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
+                                    window, sinks, stream or None)
         if rc:
             _check(rc)
 

@@ -16,9 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnp.so")
 SOURCES = ["np_api.hip", "np_kv.hip", "k_delta.hip", "k_scatter.hip", "k_ffn.hip", "k_kv.hip", "k_attn.hip", "np_rope.hip", "k_rope.hip", "np_w4.hip",
-           "k_w4.hip"]
+           "k_w4.hip", "np_prefix.hip", "k_prefix.hip"]
 HEADERS = ["np_internal.hpp", "np_host.hpp", "kv_internal.hpp", "kv_device.hpp", "kv_host.hpp", "kv_quant.hpp", "rope_internal.hpp", "mfma_device.hpp",
-           "w4_internal.hpp"]
+           "w4_internal.hpp", "attn_device.hpp", "prefix_internal.hpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

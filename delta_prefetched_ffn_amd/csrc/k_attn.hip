@@ -16,51 +16,14 @@
 #include <algorithm>
 #include <atomic>
 
-#include "mfma_device.hpp"
+#include "attn_device.hpp"
+#include "prefix_internal.hpp"
 
 namespace np {
 namespace {
 
-// What differs by the type of q and out. K codes become Op values (exact), q is held as kTerms
-// summands of that type: bf16 and fp16 as they are, fp32 as three bf16 summands (8 + 8 + 8 bits:
-// exact). P is rounded to fp16 for 16-bit outputs (2^-11 of the value, below the output's own
-// rounding for bf16 and equal to it for fp16) and to three bf16 summands (2^-24) for fp32. In fp16 it
-// is held times 2^kLift, so that it is between 2^7 and 2^15 at the row's maximum: weights from 2^-21 of
-// that on are rounded by 2^-11 of themselves, smaller ones by at most 2^-32 of the largest (fp16's last
-// places). N tokens are then off by at most N * 2^-32 of the row's sum together, half a step of fp16 at
-// 2 Mi tokens; without the factor it was at 16 Ki.
-template <typename T>
-struct Kind;
-template <>
-struct Kind<__bf16> {
-    typedef __bf16 Q;
-    typedef _Float16 P;
-    static constexpr int kQ = 1, kP = 1, kLift = 7;
-};
-template <>
-struct Kind<_Float16> {
-    typedef _Float16 Q;
-    typedef _Float16 P;
-    static constexpr int kQ = 1, kP = 1, kLift = 7;
-};
-template <>
-struct Kind<float> {
-    typedef __bf16 Q;
-    typedef __bf16 P;
-    static constexpr int kQ = 3, kP = 3, kLift = 0;
-};
-
 constexpr int kRows = kRowTile;      // query rows of a tile
 constexpr int kPiece = kPieceTokens;  // tokens of one step
-// P's values reach 2^kLazy (times 2^kLift) before the running maximum is raised, so most steps rescale nothing.
-constexpr float kLazy = 8.0f;
-// O is kept in units of 2^unit; a block's V codes are widened times 2^(ev - unit). Within
-// [-kFar, kNear] of the unit every code is a normal fp16 number (2^-9 * 2^-5 = 2^-14 and
-// 448 * 2^7 < 65504), so widening is exact; a block further off moves the unit. It moves down by at
-// most kDrop from the largest exponent met (O would overflow fp32): blocks below that vanish.
-constexpr int kFar = 5, kNear = 7, kDrop = 40;
-constexpr int kNoUnit = -1000;  // below every exponent: no block met so far
-
 // The tokens a row tile reads, as 32-token pieces: the first tokens' pieces, then those of
 // [first, end).
 struct Pieces {
@@ -80,16 +43,6 @@ __device__ inline Pieces pieces_of(int pos_lo, int pos_hi, int window, int sinks
 // sees is treated as one that is not held: its values' scale must not decide what the others keep.
 __device__ inline bool group_seen(const AttnArgs& a, int t, int pos_lo, int pos_hi) {
     return t <= pos_hi && (!a.window || pos_lo - (t + 15) < a.window || t < a.sinks);
-}
-
-// Adds a part (maximum mp, sum lp, values v) to a row's join at the maximum mm >= mp. A part that
-// saw no token (mp = -inf, lp = 0) adds nothing, whatever mm is.
-__device__ inline void join(f32x4& x, float& ll, float mm, float mp, float lp, f32x4 v) {
-    if (mp == -__builtin_inff() && lp == 0.0f) return;
-    const float f = mp == mm ? 1.0f : __builtin_amdgcn_exp2f(mp - mm);
-    ll += f * lp;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] += f * v[j];
 }
 
 // Four values of a finished row (query token and head of the group: r), and its lse.
@@ -129,7 +82,7 @@ __device__ inline f32x2 get2(const float* p) {
 // waves 15.2, 18.7 and 196 us, 8 waves 13.5, 18.5 and 192 us, 16 waves 15.7, 20.3 and 210 us.
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_rows(AttnArgs a) {
-    typedef Kind<T> Kd;
+    typedef AttnKind<T> Kd;
     typedef typename Kd::Q Q;
     typedef typename Kd::P P;
     typedef typename Vec8<Q>::t Q8;
@@ -543,7 +496,7 @@ __device__ inline V settled(V x) {
 // consecutive values of its row.
 template <typename T, int NS, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4))) void k_attn_tile(AttnArgs a) {
-    typedef Kind<T> Kd;
+    typedef AttnKind<T> Kd;
     typedef typename Kd::Q Q;
     typedef typename Kd::P P;
     typedef typename Vec8<Q>::t Q8;
@@ -937,7 +890,7 @@ template <typename T, int NS>
 hipError_t rows_as(const AttnArgs& a, hipStream_t s) {
     constexpr int W = kAttnWaves;
     const dim3 grid(a.b.item0[a.b.n], a.kv.n_kv);
-    const size_t lds = std::max(kRowLds<NS> * a.row_cap, sizeof(bf16x8) * 64 * 2 * NS * Kind<T>::kQ);
+    const size_t lds = std::max(kRowLds<NS> * a.row_cap, sizeof(bf16x8) * 64 * 2 * NS * AttnKind<T>::kQ);
     k_attn_rows<T, NS, W><<<grid, 64 * W, lds, s>>>(a);
     return hipGetLastError();
 }
@@ -988,7 +941,7 @@ hipError_t attn_prepare() {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
-    for (hipError_t x : {prepare_all<float>(), prepare_all<__bf16>(), prepare_all<_Float16>()})
+    for (hipError_t x : {prepare_all<float>(), prepare_all<__bf16>(), prepare_all<_Float16>(), prefix_prepare()})
         if (x != hipSuccess) e = x;
     if (e == hipSuccess && dev < 64) done.fetch_or(1ull << dev);
     return e;

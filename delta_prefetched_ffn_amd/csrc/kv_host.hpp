@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 #include <optional>
 #include <vector>
@@ -21,6 +22,11 @@ struct Seq {
     int32_t stale_lo = 0, stale_hi = 0;  // entries that the device's page table does not have yet
 };
 
+// Tokens [t0, t1) (whole pages, all earlier than the new ones) that the sequences order[lo .. hi) of the batch share.
+struct SharedRun {
+    int32_t lo, hi, t0, t1;
+};
+
 }  // namespace np
 
 struct np_kv {
@@ -34,6 +40,10 @@ struct np_kv {
     std::vector<np::Seq> seqs;
     std::vector<int32_t> stale;     // sequences with such entries
     std::vector<int32_t> b_seq, b_before, b_fresh;  // the current batch (np_kv_extend); empty: none
+    // What the batch's sequences share, worked out by the first call that asks (np_prefix.hip).
+    bool runs_known = false;
+    std::vector<int32_t> order;     // positions in the batch
+    std::vector<np::SharedRun> runs;
     bool broken = false;            // a launch failed in the middle of a call
     int32_t* table = nullptr;
     float* part = nullptr;
@@ -77,6 +87,7 @@ struct np_kv {
         if (std::find(b_seq.begin(), b_seq.end(), seq) != b_seq.end()) drop_batch();
     }
     void drop_batch() {
+        runs_known = false;
         b_seq.clear();
         b_before.clear();
         b_fresh.clear();
@@ -160,6 +171,32 @@ inline np_status check_rows(const np_kv* kv, const void* p, int64_t row, int64_t
     if (row < 0 || head < 0 || row % unit || head % unit || row > (int64_t)1 << 40 || head > (int64_t)1 << 40)
         return fail(NP_EINVAL, "%s: strides (%lld, %lld) must be multiples of 16 bytes, not negative", what,
                     (long long)row, (long long)head);
+    return NP_OK;
+}
+
+// The checks of an attention call. S: the strides, given or contiguous; *rows: the current tokens.
+inline np_status check_attend(const np_kv* kv, int32_t layer, const void* q, const void* out, const float* lse, int32_t dtype, const int64_t* strides,
+                              float scale, int32_t window, int32_t sinks, int64_t* S, int64_t* n_rows) {
+    np_status st = check_layer_io(kv, layer, dtype);
+    if (st != NP_OK) return st;
+    const np_kv_desc& D = kv->desc;
+    if (!(std::isfinite(scale) && scale > 0.0f)) return fail(NP_EINVAL, "scale=%g must be positive and finite", scale);
+    if (window < 0 || sinks < 0) return fail(NP_EINVAL, "window=%d and sinks=%d must not be negative", window, sinks);
+    int64_t rows = 0;
+    for (int32_t f : kv->b_fresh) rows += f;
+    *n_rows = rows;
+    const int64_t plain[4] = {(int64_t)D.n_heads * D.head_dim, D.head_dim, (int64_t)D.n_heads * D.head_dim, D.head_dim};
+    for (int i = 0; i < 4; ++i) S[i] = strides ? strides[i] : plain[i];
+    if ((st = check_rows(kv, q, S[0], S[1], dtype, "q")) != NP_OK) return st;
+    if ((st = check_rows(kv, out, S[2], S[3], dtype, "out")) != NP_OK) return st;
+    if (!((S[3] >= D.head_dim || D.n_heads == 1) && (S[2] >= (D.n_heads - 1) * S[3] + D.head_dim || rows <= 1)) &&
+        !((S[2] >= D.head_dim || rows <= 1) && (S[3] >= (rows - 1) * S[2] + D.head_dim || D.n_heads == 1)))
+        return fail(NP_EINVAL, "out: strides (%lld, %lld) make rows or heads overlap", (long long)S[2], (long long)S[3]);
+    if (lse && ((uintptr_t)lse & 3u)) return fail(NP_EINVAL, "lse must be 4-byte aligned");
+    if (kv->host_only()) return fail(NP_ESTATE, "a bookkeeping-only cache holds no tokens");
+    if ((st = check_io_ptr(q, D.device, "q", "cache")) != NP_OK) return st;
+    if ((st = check_io_ptr(out, D.device, "out", "cache")) != NP_OK) return st;
+    if (lse && (st = check_io_ptr(lse, D.device, "lse", "cache")) != NP_OK) return st;
     return NP_OK;
 }
 

@@ -81,6 +81,8 @@ constexpr int kRowTile = 16;
 constexpr int kPieceTokens = 32;
 constexpr int kMaxPartials = 8192;
 constexpr int kMaxPartialRows = 32768;
+// Rows of partial results that a cache has room for: the attention over shared pages uses them all.
+constexpr int kMaxSharedRows = 65536;
 
 // Page table entries to write: table[at[k]] = page[k], k < n.
 constexpr int kTableEntries = 480;

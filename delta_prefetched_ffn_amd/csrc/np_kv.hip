@@ -169,7 +169,7 @@ np_status create(const np_kv_desc* desc, np_kv** out) {
         if ((st = check_io_ptr(D.codes, D.device, "codes", "cache")) != NP_OK) return st;
         if ((st = check_io_ptr(D.exps, D.device, "exps", "cache")) != NP_OK) return st;
         const size_t table_bytes = (size_t)D.max_seqs * D.max_pages * sizeof(int32_t);
-        const size_t part_bytes = (size_t)kMaxPartialRows * (kv->slabs * kTileDims + 2) * sizeof(float);
+        const size_t part_bytes = (size_t)kMaxSharedRows * (kv->slabs * kTileDims + 2) * sizeof(float);
         if (hipMalloc((void**)&kv->table, table_bytes) != hipSuccess || hipMalloc((void**)&kv->part, part_bytes) != hipSuccess ||
             hipMalloc((void**)&kv->arrived, kMaxPartials * sizeof(uint32_t)) != hipSuccess) {
             (void)hipGetLastError();
@@ -286,25 +286,10 @@ np_status append(np_kv* kv, int32_t layer, const void* k, const void* v, int32_t
 
 np_status attend(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype, const int64_t* strides,
                  float scale, int32_t window, int32_t sinks, hipStream_t s) {
-    np_status st = check_layer_io(kv, layer, dtype);
+    int64_t S[4], rows = 0;
+    np_status st = check_attend(kv, layer, q, out, lse, dtype, strides, scale, window, sinks, S, &rows);
     if (st != NP_OK) return st;
     const np_kv_desc& D = kv->desc;
-    if (!(std::isfinite(scale) && scale > 0.0f)) return fail(NP_EINVAL, "scale=%g must be positive and finite", scale);
-    if (window < 0 || sinks < 0) return fail(NP_EINVAL, "window=%d and sinks=%d must not be negative", window, sinks);
-    int64_t rows = 0;
-    for (int32_t f : kv->b_fresh) rows += f;
-    const int64_t plain[4] = {(int64_t)D.n_heads * D.head_dim, D.head_dim, (int64_t)D.n_heads * D.head_dim, D.head_dim};
-    const int64_t* const S = strides ? strides : plain;
-    if ((st = check_rows(kv, q, S[0], S[1], dtype, "q")) != NP_OK) return st;
-    if ((st = check_rows(kv, out, S[2], S[3], dtype, "out")) != NP_OK) return st;
-    if (!((S[3] >= D.head_dim || D.n_heads == 1) && (S[2] >= (D.n_heads - 1) * S[3] + D.head_dim || rows <= 1)) &&
-        !((S[2] >= D.head_dim || rows <= 1) && (S[3] >= (rows - 1) * S[2] + D.head_dim || D.n_heads == 1)))
-        return fail(NP_EINVAL, "out: strides (%lld, %lld) make rows or heads overlap", (long long)S[2], (long long)S[3]);
-    if (lse && ((uintptr_t)lse & 3u)) return fail(NP_EINVAL, "lse must be 4-byte aligned");
-    if (kv->host_only()) return fail(NP_ESTATE, "a bookkeeping-only cache holds no tokens");
-    if ((st = check_io_ptr(q, D.device, "q", "cache")) != NP_OK) return st;
-    if ((st = check_io_ptr(out, D.device, "out", "cache")) != NP_OK) return st;
-    if (lse && (st = check_io_ptr(lse, D.device, "lse", "cache")) != NP_OK) return st;
     if (rows == 0) return NP_OK;
 
     AttnArgs a;

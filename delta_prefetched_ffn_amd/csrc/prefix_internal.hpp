@@ -1,0 +1,55 @@
+// Internal declarations of the attention over shared first pages: what the host side (np_prefix.hip) passes to the gfx950
+// kernels of k_prefix.hip.
+#pragma once
+
+#include "kv_internal.hpp"
+
+namespace np {
+
+// Shared runs of pages that one call works out once each, at most; further ones are read by each sequence.
+constexpr int kMaxRuns = 32;
+constexpr int kRunWaves = 4;       // waves of a workgroup
+constexpr int kRunSlots = 512;     // such workgroups that the device holds at a time: two a compute unit
+constexpr uint8_t kNoRun = 255;
+
+// A run of tokens [t0, t1) (whole pages) that the sequences [s0, s1) of the batch share.
+struct PrefixRun {
+    int32_t t0, t1;
+    int32_t item0;      // its first work item: (row tile, split)
+    int32_t part0;      // its first partial row (of one kv head)
+    uint16_t splits;
+    uint8_t s0, s1;
+};
+
+struct PrefixArgs {
+    KvView kv;
+    const void* q;
+    void* out;
+    float* lse;                            // [rows][heads] or nullptr
+    int64_t q_row, q_head, o_row, o_head;  // strides in elements
+    float* part;                           // partial rows: [row][64 slabs + 2]
+    float scale2;                          // softmax scale * log2(e)
+    int32_t window, sinks, layer;
+    int32_t n, n_runs;
+    int32_t leaf_item, leaf_part;          // the sequences' own items and partial rows start here
+    int32_t leaf_cap;                      // rows of their largest tile
+    int32_t even;                          // the new tokens of every sequence, or 0: they differ
+    int32_t rows;
+    PrefixRun run[kMaxRuns];
+    // The batch, in an order in which sequences that share a run are neighbours.
+    int32_t before[kMaxBatch];             // tokens before the new ones
+    int32_t cum[kMaxBatch + 1];            // new tokens of the sequences in front
+    int32_t row0[kMaxBatch];               // first row in the caller's tensors
+    int32_t item0[kMaxBatch + 1];          // first work item of its own tokens, from leaf_item
+    uint16_t seq[kMaxBatch], splits[kMaxBatch];
+    uint8_t deepest[kMaxBatch];            // the last run that it is part of (its own tokens start behind), or kNoRun
+};
+static_assert(sizeof(PrefixArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+// Rows of a run's tile; a sequence's own rows take tiles of 16 up to 16, else of these.
+constexpr int run_tiles(int dtype, int slabs) { return slabs == 1 || (slabs == 2 && dtype != kF32) ? 4 : 2; }
+
+hipError_t launch_prefix(const PrefixArgs& a, int dtype, hipStream_t s);
+hipError_t prefix_prepare();  // lets the current device's kernels use the LDS they ask for
+
+}  // namespace np

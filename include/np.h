@@ -557,6 +557,19 @@ np_status np_kv_read_tokens(const np_kv* kv, int32_t layer, int32_t seq, int32_t
  * the current step}. */
 np_status np_kv_info(const np_kv* kv, int32_t* out4);
 
+/* np_kv_attend (same arguments, checks, visibility and errors), for sequences that
+ * share pages: np_kv_fork makes them, e.g. continuations of one prompt. A run of
+ * whole pages of earlier tokens that several sequences of the step have in common, from their
+ * first page on, is read once for the rows of all of them instead of once for each;
+ * runs may branch (a conversation forked from a conversation). What is shared is
+ * seen from the page lists; the caller says nothing. Where too little is shared
+ * for that to pay, or a sequence has many new tokens, it is np_kv_attend itself.
+ * Results are those of np_kv_attend up to the order of the fp32 sums, and the
+ * same from run to run. Two launches; a captured call replays with the runs of the
+ * capture (as np_kv_attend with its sequences and lengths). */
+np_status np_attend_shared(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,
+                           const int64_t* strides, float scale, int32_t window, int32_t sinks, void* stream);
+
 /* ---- rotary positions, with the norms of queries and keys ----
  *
  * For a head x of head_dim values at position p: first, where weights are
