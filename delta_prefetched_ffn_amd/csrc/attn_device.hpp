@@ -43,6 +43,13 @@ constexpr float kLazy = 8.0f;
 constexpr int kFar = 5, kNear = 7, kDrop = 40;
 constexpr int kNoUnit = -1000;  // below every exponent: no block met so far
 
+// x, but made where it stands: what rare paths compute from the lane is not kept in registers across
+// the loop for them.
+__device__ inline int here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Adds a part (maximum mp, sum lp, values v) to a row's join at the maximum mm >= mp. A part that
 // saw no token (mp = -inf, lp = 0) adds nothing, whatever mm is.
 __device__ inline void join(f32x4& x, float& ll, float mm, float mp, float lp, f32x4 v) {

@@ -456,13 +456,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(W / 4)))
 template <int NS>
 constexpr int kTileWaves = NS <= 3 ? 8 : 4;
 
-// x, but made where it stands: what rare paths compute from the lane is not kept in registers across
-// the loop for them.
-__device__ inline int here(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 // x, computed before what follows in the program: the compiler moves arithmetic across barriers.
 template <typename V>
 __device__ inline V settled(V x) {

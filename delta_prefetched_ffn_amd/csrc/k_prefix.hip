@@ -18,7 +18,7 @@ namespace {
 constexpr int kRows = kRowTile;
 constexpr int kPiece = kPieceTokens;
 constexpr int W = kRunWaves;
-constexpr int kMaxTileRows = 4 * kRows;
+constexpr int kMaxTileRows = 4 * kRows;  // as many as a wave has lanes
 
 // The pieces of 32 tokens of [t0, t1) that rows at positions pos_lo and up see: the first tokens', then the window's.
 struct Pieces {
@@ -51,11 +51,32 @@ __device__ inline bool group_seen(const PrefixArgs& a, const Work& w, int t) {
     return t < w.t1 && t <= w.pos_hi && (!a.window || w.pos_lo - (t + 15) < a.window || t < a.sinks);
 }
 
-// R row tiles of 16 over the range, by the workgroup's waves: each takes every W-th piece of the split, with K and V asked
-// for a piece ahead and widened once for all R. s_pos, s_q: the rows' positions and their q as operands. Ends with the
-// rows' partial results in memory.
+// What a wave takes of it: every W-th piece of the split.
+struct Share {
+    Pieces pc;
+    int first, count;
+    __device__ int operator[](int n) const { return pc[first + n * W]; }
+};
+__device__ inline Share share_of(const PrefixArgs& a, const Work& w, int wave) {
+    Share s;
+    s.pc = pieces_of(w.t0, w.t1, w.pos_lo, a.window, a.sinks);
+    const int each = s.pc.total / w.splits, more = s.pc.total - each * w.splits;
+    const int u0 = w.split * each + min(w.split, more), u1 = u0 + each + (w.split < more ? 1 : 0);
+    s.first = u0 + wave;
+    s.count = u1 > s.first ? (u1 - s.first + W - 1) / W : 0;
+    return s;
+}
+// Page of group i % 2 of piece n0 + i / 2, i the lane; -1 where it is not held or nobody sees it.
+__device__ inline int page_ahead(const PrefixArgs& a, const Work& w, const Share& s, int n0, int lane) {
+    const int n = n0 + (lane >> 1), t = n < s.count ? s[n] + 16 * (lane & 1) : w.t1;
+    return group_seen(a, w, t) ? page_of(a.kv, w.seq, t >> a.kv.page_shift) : -1;
+}
+
+// R row tiles of 16 over the range, by the workgroup's waves: each takes every W-th piece of the split, with K asked for a
+// piece ahead and V behind the scores' products, and widened once for all R. s_pos: the rows' positions; s_mem: their q as operands; s_bad: per row, a bit
+// per value that meets a NaN (0 before). Ends with the rows' partial results in memory.
 template <typename T, int NS, int R>
-__device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int* s_pos, float* s_mem) {
+__device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const Share& share, int ahead_page, const int* s_pos, uint32_t* s_bad, float* s_mem) {
     typedef AttnKind<T> Kd;
     typedef typename Kd::Q Q;
     typedef typename Kd::P P;
@@ -64,24 +85,24 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
     const KvView& kv = a.kv;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const Q8* const s_q = reinterpret_cast<const Q8*>(s_mem);  // [R][NS][2][kQ][64 lanes]
-    int pos[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) pos[r] = s_pos[r * kRows + col];
-    const Pieces pc = pieces_of(w.t0, w.t1, w.pos_lo, a.window, a.sinks);
-    const int share = pc.total / w.splits, more = pc.total - share * w.splits;
-    const int u0 = w.split * share + min(w.split, more), u1 = u0 + share + (w.split < more ? 1 : 0);
     const uint8_t* const codes = kv.codes + a.layer * kv.layer_bytes;
     const int8_t* const exps = kv.exps + (int64_t)a.layer * kv.n_pages * kv.n_kv * 2;
     const int side_bytes = (1 << kv.page_shift) * kv.slabs * kTileDims;
 
-    // As in k_attn_rows: pieces u0 + wave + n * W; lane i has page and exponents of group i % 2 of piece (n & ~31) + i / 2.
-    const int count = u1 - u0 > wave ? (u1 - u0 - wave + W - 1) / W : 0;
-    const auto token_of = [&](int n) { return pc[u0 + wave + n * W]; };
-    int ahead_page = -1, ahead_exps = 0;
-    const auto fetch = [&](int n0) {
-        const int n = n0 + (lane >> 1), t = n < count ? token_of(n) + 16 * (lane & 1) : w.t1;
-        ahead_page = group_seen(a, w, t) ? page_of(kv, w.seq, t >> kv.page_shift) : -1;
-        ahead_exps = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)max(ahead_page, 0) * kv.n_kv + w.h) * 2);
+    // Lane i, of group i % 2 of piece (n & ~31) + i / 2: its K codes' address (page 0 where it is not held or nobody sees it: its
+    // tokens are hidden below), its K factor and V exponent; a bit per group of whether it is held.
+    const int count = share.count;
+    uint64_t ahead_at = 0, ahead_held = 0;
+    float ahead_kf = 0.0f;
+    int ahead_ev = 0;
+    const auto fetch = [&](int n0) __attribute__((always_inline)) {
+        const int n = n0 + (lane >> 1), t = n < count ? share[n] + 16 * (lane & 1) : 0, page = max(ahead_page, 0);
+        const int e = *reinterpret_cast<const uint16_t*>(exps + ((int64_t)page * kv.n_kv + w.h) * 2);
+        ahead_at = reinterpret_cast<uint64_t>(codes + page * kv.page_bytes + (int64_t)2 * w.h * side_bytes +
+                                              (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes));
+        ahead_held = __ballot(ahead_page >= 0);
+        ahead_kf = fmaxf(a.scale2 * pow2i(max(-126, (int)(int8_t)e)), 1.2e-38f);  // never 0: a hidden score is -inf, and stays it times this
+        ahead_ev = max(-126, (int)(int8_t)(e >> 8));
     };
     fetch(0);
 
@@ -100,45 +121,44 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
     int unit = kNoUnit, top = kNoUnit;  // o is in units of 2^unit
 
     u32x4 k[2][NS], v[2][NS];
-    const uint8_t* at[2];
+    uint64_t at[2];
     int lane16 = lane * 16;
     const auto locate = [&](int n) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            // A group that is not held (or lies past the range) reads page 0; its tokens are hidden below.
-            const int page = max(0, __builtin_amdgcn_readlane(ahead_page, (n & 31) * 2 + g)), t = token_of(n) + 16 * g;
-            at[g] = codes + page * kv.page_bytes + (int64_t)w.h * 2 * side_bytes +
-                    (int64_t)((t & ((1 << kv.page_shift) - 1)) >> 4) * (kv.slabs * kTileBytes);
+            const int from = (n & 31) * 2 + g;
+            at[g] = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(ahead_at >> 32), from) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)ahead_at, from);
         }
     };
+    typedef const __attribute__((address_space(1))) uint8_t code;
+    typedef const __attribute__((address_space(1))) u32x4 chunk;
     const auto load_k = [&] {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-            for (int c = 0; c < NS; ++c) k[g][c] = *reinterpret_cast<const u32x4*>(at[g] + c * kTileBytes + lane16);
+            for (int c = 0; c < NS; ++c) k[g][c] = *reinterpret_cast<chunk*>(reinterpret_cast<code*>(at[g]) + c * kTileBytes + lane16);
     };
     const auto load_v = [&] {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-            for (int c = 0; c < NS; ++c) v[g][c] = *reinterpret_cast<const u32x4*>(at[g] + side_bytes + c * kTileBytes + lane16);
+            for (int c = 0; c < NS; ++c) v[g][c] = *reinterpret_cast<chunk*>(reinterpret_cast<code*>(at[g] + side_bytes) + c * kTileBytes + lane16);
     };
     if (count) {
         locate(0);
         load_k();
-        load_v();
     }
     for (int n = 0; n < count; ++n) {
-        const int tok = token_of(n);
+        const int tok = share[n];
         bool held[2];
         float kf[2];
         int ev[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            held[g] = __builtin_amdgcn_readlane(ahead_page, (n & 31) * 2 + g) >= 0;
-            const int e = __builtin_amdgcn_readlane(ahead_exps, (n & 31) * 2 + g);
-            kf[g] = a.scale2 * pow2i(max(-126, (int)(int8_t)e));
-            ev[g] = max(-126, (int)(int8_t)(e >> 8));
+            const int from = (n & 31) * 2 + g;
+            held[g] = (ahead_held >> from & 1) != 0;
+            kf[g] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ahead_kf), from));
+            ev[g] = __builtin_amdgcn_readlane(ahead_ev, from);
         }
         f32x4 acc[R][2];  // raw scores of tokens tok + 16 g + 4 quad + j
 #pragma unroll
@@ -157,17 +177,28 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
                         acc[r][1] = mfma(k1, q, acc[r][1]);
                     }
             }
+        // Operands come from LDS a few products ahead.
+        constexpr int kMfma = 0x8, kDsRead = 0x100, kReads = NS * 2 * R * Kd::kQ, kAhead = kReads < 4 ? kReads : 4;
+        __builtin_amdgcn_sched_group_barrier(kDsRead, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < kReads - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kMfma, 2 * kAhead, 0);
         __builtin_amdgcn_sched_barrier(0);
+        load_v();
         const bool last = n + 1 >= count;
         if (!last) {
             if ((n & 31) == 31) {
+                ahead_page = page_ahead(a, w, share, n + 1, lane);
                 fetch(n + 1);
-                asm volatile("" : "+v"(ahead_exps));  // waited for here, in this branch
+                asm volatile("" : "+v"(ahead_kf), "+v"(ahead_ev));  // waited for here, in this branch
             }
             locate(n + 1);
         } else {
             // The same number of loads in every turn; these read one line of the pool's start.
-            at[0] = at[1] = codes;
+            at[0] = at[1] = reinterpret_cast<uint64_t>(codes);
             lane16 = 0;
         }
         load_k();
@@ -179,23 +210,21 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
         uint32_t vis = ~0u;  // 8 bits a row tile
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float s[8];
-#pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) s[k8] = acc[r][k8 >> 2][k8 & 3] * kf[k8 >> 2];
             if (!whole) {
+                const int mine = here(lane), pos = s_pos[r * kRows + (mine & 15)], t0 = tok + 4 * (mine >> 4);
                 uint32_t see = 0;
 #pragma unroll
                 for (int k8 = 0; k8 < 8; ++k8) {
-                    const int t = tok + 16 * (k8 >> 2) + 4 * quad + (k8 & 3);
-                    const bool ok = t <= pos[r] && t < w.t1 && held[k8 >> 2] && (!a.window || pos[r] - t < a.window || t < a.sinks);
+                    const int t = t0 + 16 * (k8 >> 2) + (k8 & 3);
+                    const bool ok = t <= pos && t < w.t1 && held[k8 >> 2] && (!a.window || pos - t < a.window || t < a.sinks);
                     see |= ok ? 1u << k8 : 0u;
-                    if (!ok) s[k8] = -__builtin_inff();
+                    if (!ok) acc[r][k8 >> 2][k8 & 3] = -__builtin_inff();
                 }
                 vis = (vis & ~(0xffu << (8 * r))) | see << (8 * r);
             }
-            float mx = s[0];
+            float mx = -__builtin_inff();
 #pragma unroll
-            for (int k8 = 1; k8 < 8; ++k8) mx = fmaxf(mx, s[k8]);
+            for (int g = 0; g < 2; ++g) mx = fmaxf(mx, fmaxf(fmaxf(acc[r][g][0], acc[r][g][1]), fmaxf(acc[r][g][2], acc[r][g][3])) * kf[g]);
             if (__any(mx > m[r] + kLazy)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16));
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -209,49 +238,29 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
                     for (int i = 0; i < 4; ++i) o[r][c][i] *= f;
             }
             const float m0 = (m[r] == -__builtin_inff() ? 0.0f : m[r]) - Kd::kLift;  // 0: a row that has seen nothing finite
-            float p[8];
+            float p[8];  // 0 for hidden tokens
 #pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) p[k8] = __builtin_amdgcn_exp2f(s[k8] - m0);
-            if (!whole) {
-#pragma unroll
-                for (int k8 = 0; k8 < 8; ++k8)
-                    if (!(vis >> (8 * r + k8) & 1)) p[k8] = 0.0f;
+            for (int k8 = 0; k8 < 8; ++k8) {
+                p[k8] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[r][k8 >> 2][k8 & 3], kf[k8 >> 2], -m0));
+                l[r] += p[k8];
             }
-#pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8) l[r] += p[k8];
             split<P, Kd::kP>(pv[r], p);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) seen |= vis >> (8 * r) & 0xff ? 1u << r : 0u;
 
-        // O += V^T P^T, as in k_attn_rows: both groups at once, or one at a time where their scales lie too far apart; NaN codes of
-        // tokens that a row does not see are kept from it.
-        const auto fit_unit = [&](int ea, int eb) {
-            const int lo_e = min(ea, eb), hi_e = max(ea, eb);
-            top = max(top, hi_e);
-            const int to = max(min(hi_e, lo_e + kFar), top - kDrop);
-            if (to != unit && (hi_e > unit + kNear || lo_e < unit - kFar)) {
-                const float f = pow2i(max(-126, unit - to));
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int c = 0; c < NS; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[r][c][i] *= f;
-                unit = to;
-            }
-        };
-        const int e0 = held[0] ? ev[0] : held[1] ? ev[1] : unit, e1 = held[1] ? ev[1] : e0;
-        const bool near = e0 - e1 <= kNear + kFar && e1 - e0 <= kNear + kFar;
-        bool clean = true;
+        // Tokens that no row of the tile sees (often bytes never written) are cleared. What is NaN besides leaves the product, where 0
+        // times it would be NaN for rows that do not see it, and goes to those that do: a second product says whether a row
+        // sees a token whose value is NaN.
         if (!whole) {
             uint32_t bad = 0;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 uint32_t some = 0;
+                const int t0 = tok + 16 * g + 4 * (here(lane) >> 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int t = tok + 16 * g + 4 * quad + j;
+                    const int t = t0 + j;
                     if (held[g] && t < w.t1 && t <= w.pos_hi && (!a.window || w.pos_lo - t < a.window || t < a.sinks)) some |= 0xffu << (8 * j);
                 }
 #pragma unroll
@@ -262,11 +271,57 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
                         bad |= nan_bytes(v[g][c][i]);
                     }
             }
-            clean = !__any(bad != 0);
+            if (__any(bad != 0)) {
+#pragma unroll
+                for (int c = 0; c < NS; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t n0 = nan_bytes(v[0][c][i]) >> 7, n1 = nan_bytes(v[1][c][i]) >> 7;
+                        if (!__any((n0 | n1) != 0)) continue;
+                        const P8 odd = widen<P>(n0 * 0x38u, n1 * 0x38u, 1.0f, 1.0f);  // 0x38: 1
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            P8 sees;
+#pragma unroll
+                            for (int k8 = 0; k8 < 8; ++k8) sees[k8] = (P)(vis >> (8 * r + k8) & 1 ? 1.0f : 0.0f);
+                            const f32x4 x = mfma(odd, sees, f32x4{0, 0, 0, 0});
+                            const int mine = here(lane);
+                            uint32_t note = 0;  // value 64 c + 16 quad + 4 j + i
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) note |= x[j] > 0.0f ? 1u << (4 * j + i) : 0u;
+                            if (note) atomicOr(&s_bad[(r * kRows + (mine & 15)) * (2 * NS) + 2 * c + (mine >> 5)], note << (mine & 16));
+                            __builtin_amdgcn_sched_barrier(0);  // this path must not cost registers
+                        }
+                        v[0][c][i] &= ~(n0 * 255u);
+                        v[1][c][i] &= ~(n1 * 255u);
+                    }
+            }
         }
-        if (clean && near) {
-            fit_unit(e0, e1);
-            const float f0 = pow2i(max(-126, e0 - unit)), f1 = pow2i(max(-126, e1 - unit));
+        // O += V^T P^T. Both groups at once, or one at a time where their V scales lie too far apart for one unit.
+        const auto fit_unit = [&](int ea, int eb) {
+            const int lo_e = min(ea, eb), hi_e = max(ea, eb);
+            top = max(top, hi_e);
+            const int to = max(min(hi_e, lo_e + kFar), top - kDrop);
+            if (to != unit && (hi_e > unit + kNear || lo_e < unit - kFar)) {
+                float f = pow2i(max(-126, unit - to));
+                asm volatile("" : "+v"(f));  // a branch, not a product with 1 in every turn
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int c = 0; c < NS; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[r][c][i] *= f;
+                unit = to;
+            }
+        };
+        // Exponents of groups that are not held are page 0's: they must not move the unit.
+        const int e0 = held[0] ? ev[0] : held[1] ? ev[1] : unit, e1 = held[1] ? ev[1] : e0;
+        const bool near = e0 - e1 <= kNear + kFar && e1 - e0 <= kNear + kFar;
+        for (int pass = 0; pass < (near ? 1 : 2); ++pass) {
+            // One group at a time: the other one's codes, times 2^-126, are nothing beside the sums.
+            const int ea = near || pass == 0 ? e0 : e1, eb = near || pass == 1 ? e1 : e0;
+            fit_unit(ea, eb);
+            const float f0 = pow2i(near || pass == 0 ? max(-126, e0 - unit) : -126), f1 = pow2i(near || pass == 1 ? max(-126, e1 - unit) : -126);
 #pragma unroll
             for (int c = 0; c < NS; ++c)
 #pragma unroll
@@ -277,35 +332,7 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
 #pragma unroll
                         for (int t = 0; t < Kd::kP; ++t) o[r][c][i] = mfma(vv, pv[r][t], o[r][c][i]);
                 }
-        } else {
-            // Row by row, each with the codes of the tokens it sees and, of two far scales, one at a time.
-            for (int turn = 0; turn < (near ? kRows : 2 * kRows); ++turn) {
-                const int row = turn & (kRows - 1), pass = turn / kRows;
-                const int ea = near ? e0 : pass ? e1 : e0, eb = near ? e1 : ea;
-                fit_unit(ea, eb);
-                const float f0 = pow2i(max(-126, ea - unit)), f1 = pow2i(max(-126, eb - unit));
-                const uint32_t vr = __shfl(vis, quad * 16 + row);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    uint32_t in[2] = {0, 0};
-#pragma unroll
-                    for (int k8 = 0; k8 < 8; ++k8)
-                        if ((vr >> (8 * r + k8) & 1) && (near || (k8 >> 2) == pass)) in[k8 >> 2] |= 0xffu << (8 * (k8 & 3));
-#pragma unroll
-                    for (int c = 0; c < NS; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const P8 vv = widen<P>(v[0][c][i] & in[0], v[1][c][i] & in[1], f0, f1);
-                            f32x4 x = o[r][c][i];
-#pragma unroll
-                            for (int t = 0; t < Kd::kP; ++t) x = mfma(vv, pv[r][t], x);
-                            if (col == row) o[r][c][i] = x;
-                            __builtin_amdgcn_sched_barrier(0);  // this path must not cost registers
-                        }
-                }
-            }
         }
-        load_v();
     }
 
     // Join the waves, 16 rows at a time: rows' maximum, sum and O in true units.
@@ -345,6 +372,10 @@ __device__ inline void attend_rows(const PrefixArgs& a, const Work& w, const int
             f32x4 y = {0, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < W; ++x) join(y, sum, top_m, s_m[x * kRows + row], s_l[x * kRows + row], *reinterpret_cast<const f32x4*>(s_o + (x * kRows + row) * DS + d));
+            const uint32_t odd = s_bad[(r * kRows + row) * (2 * NS) + (d >> 5)] >> (d & 31);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (odd >> j & 1) y[j] = __builtin_nanf("");
             float* const p = w.part + (int64_t)(r * kRows + row) * PS;
             *reinterpret_cast<f32x2*>(p + 2 + d) = f32x2{y[0], y[1]};
             *reinterpret_cast<f32x2*>(p + 4 + d) = f32x2{y[2], y[3]};
@@ -369,7 +400,7 @@ constexpr int kTiles = run_tiles(sizeof(T) == 4 ? kF32 : kBF16, NS);
 
 // Workgroups of a kv head's items are 8 apart where 8 divides the heads, so a head's tiles over one run share a die's cache.
 template <typename T, int NS>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) void k_prefix(PrefixArgs a) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(run_eu(sizeof(T) == 4 ? kF32 : kBF16, NS)))) void k_prefix(PrefixArgs a) {
     typedef AttnKind<T> Kd;
     typedef typename Kd::Q Q;
     typedef typename Vec8<Q>::t Q8;
@@ -381,6 +412,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
     __shared__ int s_cum[kMaxBatch + 1];
     __shared__ int s_pos[kMaxTileRows];
     __shared__ int64_t s_row[kMaxTileRows];  // where the row's q begins
+    __shared__ uint32_t s_bad[R * kRows * 2 * NS];
     extern __shared__ __attribute__((aligned(128))) float s_mem[];
 
     Work w;
@@ -427,6 +459,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
         for (int i = threadIdx.x; i <= a.n; i += 64 * W) s_cum[i] = a.cum[i];
         __syncthreads();
     }
+    for (int i = threadIdx.x; i < R * kRows * 2 * NS; i += 64 * W) s_bad[i] = 0;
     if ((int)threadIdx.x < kMaxTileRows) {
         const int row = r0 + min((int)threadIdx.x, w.rows - 1), t = first + row / group, g = row - row / group * group;
         const int s = s1 - s0 == 1 ? s0 : sequence_of(a, s_cum, t, s0, s1);
@@ -446,6 +479,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
         w.pos_hi = __builtin_amdgcn_readfirstlane(hi);
     }
     w.t1 = min(w.t1, w.pos_hi + 1);
+    const Share share = share_of(a, w, wave);
+    const int pages = page_ahead(a, w, share, 0, lane);  // on its way beside q
     Q8* const s_q = reinterpret_cast<Q8*>(s_mem);
     for (int cf = wave; cf < 2 * NS * wide; cf += W) {
         const int r = cf / (2 * NS), d = (cf >> 1) % NS * 64 + quad * 16 + (cf & 1) * 8, row = r * kRows + col;
@@ -468,8 +503,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2))) voi
         }
     }
     __syncthreads();
-    if (wide == 1) attend_rows<T, NS, 1>(a, w, s_pos, s_mem);
-    else attend_rows<T, NS, R>(a, w, s_pos, s_mem);
+    if (R == 1 || wide == 1) attend_rows<T, NS, 1>(a, w, share, pages, s_pos, s_bad, s_mem);
+    else attend_rows<T, NS, R>(a, w, share, pages, s_pos, s_bad, s_mem);
 }
 
 // Joins a row's partial results: a thread per four values of a (new token, head).
@@ -493,7 +528,7 @@ __global__ __launch_bounds__(256) void k_prefix_join(PrefixArgs a) {
     // `splits` partial rows, `step` rows apart.
     const auto take = [&](int64_t row, int64_t step, int splits) {
         const float* const p = a.part + row * PS;
-        constexpr int U = 4;  // in flight
+        constexpr int U = 8;  // in flight
         for (int s0 = 0; s0 < splits; s0 += U) {
             f32x2 ml[U], xa[U], xb[U];
 #pragma unroll

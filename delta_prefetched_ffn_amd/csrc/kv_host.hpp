@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
 #include <new>
 #include <optional>
 #include <vector>
@@ -44,6 +45,7 @@ struct np_kv {
     bool runs_known = false;
     std::vector<int32_t> order;     // positions in the batch
     std::vector<np::SharedRun> runs;
+    std::shared_ptr<void> plans;    // and how its calls are divided
     bool broken = false;            // a launch failed in the middle of a call
     int32_t* table = nullptr;
     float* part = nullptr;

@@ -26,6 +26,18 @@ constexpr int64_t kFullWaves = 256 * 16;
 // A launch has at most 2^32 - 1 threads along x, in workgroups of 256.
 constexpr int64_t kMaxGroups = (int64_t)1 << 24;
 
+// What pair i turns by per position, in radians.
+double freq_of(const np_rope_desc& D, int i) {
+    if (D.freqs) return D.freqs[i];
+    const double rot = D.rot_dim;
+    const double base = D.scaling == NP_ROPE_NTK ? D.base * std::pow(D.factor, rot / (rot - 2)) : D.base;
+    const double f = std::pow(base, -2.0 * i / rot);
+    if (D.scaling == NP_ROPE_LINEAR) return f / D.factor;
+    if (D.scaling != NP_ROPE_BLEND) return f;
+    const double keep = std::fmin(1.0, std::fmax(0.0, (D.context * f / kTwoPi - D.low) / (D.high - D.low)));
+    return f * keep + f / D.factor * (1.0 - keep);
+}
+
 np_status check_desc(const np_rope_desc& D) {
     if (D.head_dim < 8 || D.head_dim > kMaxHeadDim || D.head_dim % 8)
         return fail(NP_EINVAL, "head_dim=%d must be a multiple of 8 in [8, %d]", D.head_dim, kMaxHeadDim);
@@ -45,19 +57,9 @@ np_status check_desc(const np_rope_desc& D) {
     if (D.scaling == NP_ROPE_NTK && D.rot_dim == 2) return fail(NP_EINVAL, "a larger base does not change the only pair of rot_dim=2");
     if (D.scaling == NP_ROPE_BLEND && !(D.context > 0 && std::isfinite(D.low) && std::isfinite(D.high) && D.low < D.high))
         return fail(NP_EINVAL, "context=%lld must be positive and low=%g below high=%g", (long long)D.context, D.low, D.high);
+    for (int i = 0; i < D.rot_dim / 2; ++i)
+        if (!std::isfinite(freq_of(D, i))) return fail(NP_EINVAL, "pair %d turns by %g a position: not finite", i, freq_of(D, i));
     return NP_OK;
-}
-
-// What pair i turns by per position, in radians.
-double freq_of(const np_rope_desc& D, int i) {
-    if (D.freqs) return D.freqs[i];
-    const double rot = D.rot_dim;
-    const double base = D.scaling == NP_ROPE_NTK ? D.base * std::pow(D.factor, rot / (rot - 2)) : D.base;
-    const double f = std::pow(base, -2.0 * i / rot);
-    if (D.scaling == NP_ROPE_LINEAR) return f / D.factor;
-    if (D.scaling != NP_ROPE_BLEND) return f;
-    const double keep = std::fmin(1.0, std::fmax(0.0, (D.context * f / kTwoPi - D.low) / (D.high - D.low)));
-    return f * keep + f / D.factor * (1.0 - keep);
 }
 
 // f radians as a fraction of a turn, in 2^-64 (whole turns do not count).
@@ -78,11 +80,7 @@ np_status create(const np_rope_desc* desc, np_rope** out) {
         ~Holder() { delete r; }
     } hold;
     std::vector<uint64_t> bits(std::max(1, D.rot_dim / 2), 0);
-    for (int i = 0; i < D.rot_dim / 2; ++i) {
-        const double f = freq_of(D, i);
-        if (!std::isfinite(f)) return fail(NP_EINVAL, "pair %d turns by %g a position: not finite", i, f);
-        bits[i] = turn_bits(f);
-    }
+    for (int i = 0; i < D.rot_dim / 2; ++i) bits[i] = turn_bits(freq_of(D, i));
     int ndev = 0;
     NP_HIP(hipGetDeviceCount(&ndev));
     if (D.device < 0 || D.device >= ndev) return fail(NP_EINVAL, "device %d out of range [0, %d)", D.device, ndev);

@@ -9,7 +9,6 @@ namespace np {
 // Shared runs of pages that one call works out once each, at most; further ones are read by each sequence.
 constexpr int kMaxRuns = 32;
 constexpr int kRunWaves = 4;       // waves of a workgroup
-constexpr int kRunSlots = 512;     // such workgroups that the device holds at a time: two a compute unit
 constexpr uint8_t kNoRun = 255;
 
 // A run of tokens [t0, t1) (whole pages) that the sequences [s0, s1) of the batch share.
@@ -46,8 +45,12 @@ struct PrefixArgs {
 };
 static_assert(sizeof(PrefixArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
-// Rows of a run's tile; a sequence's own rows take tiles of 16 up to 16, else of these.
-constexpr int run_tiles(int dtype, int slabs) { return slabs == 1 || (slabs == 2 && dtype != kF32) ? 4 : 2; }
+// Row tiles of 16 that a workgroup takes over a run (or over a sequence's own tokens, where it has more than 16 rows), and the
+// waves that a SIMD then holds. A wave issues an instruction about every 8 clocks, a SIMD takes one every 2: more waves of
+// fewer rows are ahead of few of many as long as nothing is spilled. Measured at head_dim 128, bf16, two runs of 30 Ki
+// tokens for 1,080 rows each and 8 kv heads: see k_prefix.
+constexpr int run_tiles(int dtype, int slabs) { return slabs <= 2 ? 2 : 1; }
+constexpr int run_eu(int dtype, int slabs) { return slabs == 1 ? 4 : slabs == 4 ? 2 : 3; }
 
 hipError_t launch_prefix(const PrefixArgs& a, int dtype, hipStream_t s);
 hipError_t prefix_prepare();  // lets the current device's kernels use the LDS they ask for

@@ -19,12 +19,48 @@ def _torch():
     assert torch.cuda.is_available()
 
 
+def attention(q, k, v, before, scale, window=0, sinks=0, held=None):
+    """kv_reference.attention, a kv head's rows at a time (the same numbers, long sequences in less time)."""
+    n, H, hd = q.shape
+    Hk = k.shape[1]
+    G = H // Hk
+    out, terms, lse, mag = np.zeros((n, H, hd)), np.zeros((n, H, hd)), np.full((n, H), -np.inf), np.zeros((n, H))
+    for i in range(n):
+        pos = before + i
+        j = np.arange(pos + 1)
+        ok = np.ones(pos + 1, bool) if held is None else held[:pos + 1].copy()
+        if window:
+            ok &= (pos - j < window) | (j < sinks)
+        j = j[ok]
+        if not j.size:
+            continue
+        j = slice(None, pos + 1) if j.size == pos + 1 else j
+        for h in range(Hk):
+            kk, vv, g = k[j, h], v[j, h], slice(h * G, (h + 1) * G)
+            with np.errstate(all="ignore"):
+                s = q[i, g] @ kk.T * scale
+                top = s.max(-1, keepdims=True)
+                p = np.exp(s - top)
+                l = p.sum(-1, keepdims=True)
+                out[i, g], terms[i, g] = p @ vv / l, p @ np.abs(vv) / l
+                lse[i, g] = np.log(l[:, 0]) + top[:, 0]
+                mag[i, g] = (np.abs(q[i, g]) @ np.abs(kk).T).max(-1) * scale
+    return out, lse, terms, mag
+
+
 class Env(K.Env):
     """test_gpu_kv's, with attend() as attend_shared and forks that the reference follows."""
 
     def __init__(self, **kw):
         super().__init__(**kw)
         self.plain, self.kv.attend = self.kv.attend, self.kv.attend_shared
+
+    def attend(self, *a, **kw):
+        whole, R.attention = R.attention, attention
+        try:
+            return super().attend(*a, **kw)
+        finally:
+            R.attention = whole
 
     def fork(self, src, dst, n, mode="share"):
         self.kv.fork(src, dst, n, mode, self.stream())
@@ -57,37 +93,52 @@ def batch(heads, kv, hd, page, prefix, tails, dtype="bf16", seed=0, new=None, pa
     return e
 
 
+# Sharing takes calls of some 200 MB of keys and values in all (it pays from there on): 24 or 40 sequences, prompts of that length.
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("heads,kv,hd,page", [(8, 8, 64, 16), (32, 8, 128, 64), (28, 4, 80, 32), (6, 6, 40, 128), (8, 8, 256, 16), (12, 6, 192, 64), (64, 2, 128, 32), (4, 4, 128, 16)])
-def test_continuations_of_a_prompt(dtype, heads, kv, hd, page):
+@pytest.mark.parametrize("heads,kv,hd,page,prompt,n", [
+    (16, 16, 64, 16, 4003, 24), (32, 8, 128, 64, 4003, 24), (28, 4, 80, 32, 5003, 40), (12, 12, 40, 128, 5401, 24), (16, 16, 256, 16, 1003, 24), (24, 12, 192, 64, 1903, 24), (40, 4, 128, 32, 4003, 40)])
+def test_continuations_of_a_prompt(dtype, heads, kv, hd, page, prompt, n):
     rng = np.random.default_rng(heads + hd)
-    tails = [0, 1, page, 2 * page - 1] + [int(x) for x in rng.integers(0, 150, 20)]
-    e = batch(heads, kv, hd, page, 1003, tails, dtype)
+    tails = [0, 1, page, 2 * page - 1] + [int(x) for x in rng.integers(0, 150, n - 4)]
+    e = batch(heads, kv, hd, page, prompt, tails, dtype)
     assert e.shared(dtype)
     e.attend(dtype)
     e.attend(dtype, layout="fused", q_scale=4.0)
     e.attend(dtype, layout="heads", lse=False)
 
 
+def test_the_reference_of_long_sequences_is_the_reference():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.standard_normal((3, 6, 8)), rng.standard_normal((40, 3, 8)), rng.standard_normal((40, 3, 8))
+    v[5, 1, 2] = np.nan
+    held = np.arange(40) != 7
+    for kw in (dict(), dict(window=9, sinks=2), dict(held=held)):
+        for a, b in zip(attention(q, k, v, 37, 0.3, **kw), R.attention(q, k, v, 37, 0.3, **kw)):
+            np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-14)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("heads,kv,hd", [(8, 8, 64), (32, 4, 128), (12, 4, 256)])
-def test_drafts_of_different_lengths(dtype, heads, kv, hd):
-    new = [1, 5, 9, 2, 0, 3, 7, 1, 1, 12, 4, 6, 0, 2, 8, 3]
-    e = batch(heads, kv, hd, 16, 1100, [0, 40, 3, 70, 20, 16, 1, 0, 33, 90, 5, 64, 2, 8, 31, 17], dtype, new=new)
+@pytest.mark.parametrize("heads,kv,hd,prompt", [(24, 24, 64, 2500), (32, 4, 128, 4000), (24, 8, 256, 2500)])
+def test_drafts_of_different_lengths(dtype, heads, kv, hd, prompt):
+    new = [1, 5, 9, 2, 0, 3, 7, 1, 1, 12, 4, 6, 0, 2, 8, 3, 11, 10, 1, 1, 1, 14, 13, 2]
+    tails = [0, 40, 3, 70, 20, 16, 1, 0, 33, 90, 5, 64, 2, 8, 31, 17, 11, 12, 13, 14, 15, 16, 17, 18]
+    e = batch(heads, kv, hd, 16, prompt, tails, dtype, new=new, pages=-(-prompt // 16) + 24 * 10)
     assert e.shared(dtype)
     e.attend(dtype)
     # the same number for all
-    e.step([3, 1, 2, 9, 14, 6, 7, 8, 4, 5, 10, 11], [4] * 12, dtype)
+    e.step([3, 1, 2, 9, 14, 6, 7, 8, 4, 5, 10, 11, 20, 21, 22, 23, 24, 12], [4] * 18, dtype)
+    assert e.shared(dtype)
     e.attend(dtype, q_scale=3.0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_branches_families_and_strangers(dtype):
     # Two prompts; conversations forked from conversations; sequences of their own in between; all in mixed order.
-    e = Env(heads=8, kv=4, hd=64, page=32, pages=400, seqs=60)
-    e.step([0, 1, 2], [900, 700, 333], dtype)
+    e = Env(heads=16, kv=16, hd=64, page=32, pages=600, seqs=60)
+    e.step([0, 1, 2], [2900, 1700, 333], dtype)
     leaves, at = [2], 3
-    for root, n in ((0, 900), (1, 700)):
+    for root, n in ((0, 2900), (1, 1700)):
         for b in range(4):
             e.fork(root, at, n - 37 * b)
             branch = at
@@ -114,17 +165,18 @@ def test_branches_families_and_strangers(dtype):
 
 
 def test_more_runs_than_a_call_takes():
-    # 45 pairs that share 300 to 700 tokens each: the longest runs are shared, the others read by each.
-    e = Env(heads=4, kv=4, hd=64, page=16, pages=3200, seqs=91, seed=5)
-    e.step(list(range(45)), [300 + 9 * i for i in range(45)], "bf16")
-    for i in range(45):
-        e.fork(i, 45 + i, 300 + 9 * i - i % 5)
-    e.step(list(range(90)), [1] * 90, "bf16")
+    # 40 families of three that share some 3,000 tokens each: the longest runs are shared, the others read by each.
+    e = Env(heads=4, kv=4, hd=64, page=64, pages=2400, seqs=121, seed=5)
+    e.step(list(range(40)), [3000 + 19 * i for i in range(40)], "bf16")
+    for i in range(40):
+        e.fork(i, 40 + i, 3000 + 19 * i - i % 5)
+        e.fork(i, 80 + i, 3000 + 19 * i - i % 7)
+    e.step(list(range(120)), [1] * 120, "bf16")
     assert e.shared("bf16")
     e.attend("bf16")
     # one chain: each continues the one before
-    e = Env(heads=8, kv=8, hd=64, page=16, pages=900, seqs=41, seed=6)
-    e.step([0], [200], "bf16")
+    e = Env(heads=16, kv=16, hd=64, page=16, pages=900, seqs=41, seed=6)
+    e.step([0], [2000], "bf16")
     for i in range(40):
         e.fork(i, i + 1, e.kv.tokens(i) // 16 * 16)
         e.step([i + 1], [80], "bf16")
@@ -134,37 +186,37 @@ def test_more_runs_than_a_call_takes():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 3), (200, 0), (200, 70), (900, 4), (1100, 40), (5000, 0), (300, 2000)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 3), (200, 0), (200, 70), (1700, 4), (2050, 40), (5000, 0), (300, 2000), (1600, 45)])
 def test_windows_and_first_tokens(dtype, window, sinks):
-    e = batch(16, 8, 64, 32, 1000, [0, 60, 3, 90, 20, 16, 1, 0, 33, 190, 5, 64, 2, 8, 31, 17, 40, 41, 42, 43], dtype, seed=window)
+    e = batch(32, 32, 64, 32, 2000, [0, 60, 3, 90, 20, 16, 1, 0, 33, 190, 5, 64, 2, 8, 31, 17, 40, 41, 42, 43, 1, 2, 3, 4], dtype, seed=window)
     e.attend(dtype, window=window, sinks=sinks)
-    if window >= 900:
+    if window >= 1600 or sinks > 1600:
         assert e.shared(dtype, window=window, sinks=sinks)
 
 
 def test_dropped_pages():
     # A window moved on: the shared first pages are gone but for the first tokens', those behind are still shared.
-    e = batch(16, 8, 64, 16, 1200, [20 + 3 * i for i in range(20)], "bf16", seed=3)
+    e = batch(32, 32, 64, 16, 2600, [20 + 3 * i for i in range(24)], "bf16", seed=3)
     held = {}
-    for s in range(1, 21):
+    for s in range(1, 25):
         n = e.kv.tokens(s)
-        gone = e.kv.evict(s, 1000, 5)
+        gone = e.kv.evict(s, 2000, 5)
         assert gone > 0
         held[s] = np.ones(n + 10, bool)
         held[s][16:16 + 16 * gone] = False
-    e.step(list(range(1, 21)), [1] * 20, "bf16")
-    assert e.shared("bf16", window=1000, sinks=5) and e.shared("bf16")
-    e.attend("bf16", window=1000, sinks=5, held=held)
+    e.step(list(range(1, 25)), [1] * 24, "bf16")
+    assert e.shared("bf16", window=2000, sinks=5) and e.shared("bf16")
+    e.attend("bf16", window=2000, sinks=5, held=held)
     e.attend("bf16", held=held)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_nan_infinity_and_far_scales_in_the_shared_pages(dtype):
-    e = Env(heads=8, kv=8, hd=64, page=16, pages=400, seqs=25, seed=11)
-    rows = 1000
+    e = Env(heads=32, kv=32, hd=64, page=16, pages=600, seqs=25, seed=11)
+    rows = 2000
     e.extend([0], [rows])
-    k, v = (e.rng.standard_normal((rows, 8, 64)).astype(np.float32) for _ in range(2))
-    v *= np.repeat(2.0 ** e.rng.integers(-30, 8, (-(-rows // 16), 8)), 16, 0)[:rows, :, None].astype(np.float32)   # blocks of different magnitude
+    k, v = (e.rng.standard_normal((rows, 32, 64)).astype(np.float32) for _ in range(2))
+    v *= np.repeat(2.0 ** e.rng.integers(-30, 8, (-(-rows // 16), 32)), 16, 0)[:rows, :, None].astype(np.float32)   # blocks of different magnitude
     v[20, 0, 5], v[300, 1, 7], v[640, 2, 0], k[400, 3, 3], k[401, 4, 4] = np.nan, np.inf, -np.inf, np.nan, np.inf
     kt, vt = torch.from_numpy(k), torch.from_numpy(v)
     e.append((kt, kt.double().numpy()), (vt, vt.double().numpy()), "f32")
@@ -174,14 +226,16 @@ def test_nan_infinity_and_far_scales_in_the_shared_pages(dtype):
     e.step(list(range(1, 25)), [1] * 24, "f32")
     assert e.shared(dtype)
     e.attend(dtype)
-    e.attend(dtype, window=650, sinks=30)
-    q = e.rand(24, 8, dtype)
+    assert e.shared(dtype, window=1700, sinks=30)
+    e.attend(dtype, window=1700, sinks=30)
+    q = e.rand(24, 32, dtype)
     q[0][3, 1, 0], q[0][9, 5, 3] = float("nan"), float("nan")   # rows of their own, the others untouched
     e.attend(dtype, q=(q[0], q[0].double().numpy()))
 
 
 def test_the_same_from_run_to_run_on_streams_and_in_graphs():
-    e = batch(32, 8, 128, 32, 2000, [50 + 7 * i for i in range(20)], "bf16", seed=2)
+    e = batch(32, 8, 128, 32, 6000, [50 + 7 * i for i in range(20)], "bf16", seed=2)
+    assert e.shared("bf16") and e.shared("bf16", window=5500)
     q = e.rand(20, 32, "bf16")
     runs = [e.attend("bf16", q=q).clone() for _ in range(4)]
     assert all(torch.equal(r, runs[0]) for r in runs)
@@ -193,14 +247,14 @@ def test_the_same_from_run_to_run_on_streams_and_in_graphs():
     side.synchronize()
     assert torch.equal(out, runs[0])
     graphs = []
-    for window in (0, 1500):   # two graphs that share the cache's workspace
+    for window in (0, 5500):   # two graphs that share the cache's workspace
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             e.kv.attend_shared(0, qd.data_ptr(), out.data_ptr(), "bf16", scale=0.1, window=window, stream=torch.cuda.current_stream().cuda_stream)
         graphs.append(g)
     for turn in range(3):
         qd.copy_(e.rand(20, 32, "bf16")[0])
-        for g, window in zip(graphs, (0, 1500)):
+        for g, window in zip(graphs, (0, 5500)):
             out.zero_()
             g.replay()
             got = out.clone()
@@ -239,12 +293,12 @@ def test_what_does_not_share_or_pay_is_attend():
 
 def test_offsets_past_4_gib():
     # The prompt's pages lie past 4 GiB of the pool.
-    e = Env(heads=32, kv=32, hd=128, page=128, pages=4400, seqs=22, max_pages=4300, seed=4)
-    e.kv.extend([21], [4200 * 128], e.stream())
+    e = Env(heads=32, kv=32, hd=128, page=128, pages=4400, seqs=26, max_pages=4300, seed=4)
+    e.kv.extend([25], [4200 * 128], e.stream())
     e.step([0], [1000], "bf16")
     assert int(min(e.kv.pages(0))) * 32 * 2 * 128 * 128 > 1 << 32
-    for i in range(1, 21):
+    for i in range(1, 25):
         e.fork(0, i, 1000)
-    e.step(list(range(1, 21)), [1] * 20, "bf16")
+    e.step(list(range(1, 25)), [1] * 24, "bf16")
     assert e.shared("bf16")
     e.attend("bf16")
