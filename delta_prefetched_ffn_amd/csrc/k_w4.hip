@@ -136,7 +136,7 @@ constexpr int kPartStride = kW4Outs + 1;
 // Few rows: one workgroup per 16 outputs and 16 R rows; its waves take every kWaves-th chunk of 128 inputs and are joined
 // in LDS, in their order. A lane's 16 bytes of a tile are its operands of four products, x the other one: D row = row of x,
 // D column = output. x comes from the caches (kStaged: fp32, split once per workgroup into LDS).
-template <typename T, int R, int U, bool kStaged>
+template <typename T, int R, int U, bool kStaged, int G>
 __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
     typedef Kind<T> Kd;
     typedef typename Kd::E E;
@@ -147,8 +147,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
     const int64_t r0 = (int64_t)blockIdx.y * 16 * R;
     const int rows = (int)min((int64_t)16 * R, a.rows - r0);
     const uint8_t* const tiles = w.tiles + (int64_t)tile * w.chunks * kW4TileBytes + lane * 16;
-    const int64_t first_group = (int64_t)tile * w.chunks * w.per_chunk;
-    const int fold = w.per_chunk == 1 ? 8 : w.per_chunk == 2 ? 10 : 15;  // products after which a group ends
+    const int64_t first_group = (int64_t)tile * w.chunks * G;
     __shared__ float s_part[kWaves * 16 * R * kPartStride];
     extern __shared__ __attribute__((aligned(128))) uint8_t s_dyn[];
     E* const s_x = reinterpret_cast<E*>(s_dyn);  // [N][rows][x_len]
@@ -162,7 +161,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
     struct Part {
         u32x4 code;
         XRaw<T> x[kStaged ? 1 : R][4];
-        uint32_t scale[4], zero[4];
+        uint32_t scale[G], zero[G];
     };
     const auto ask = [&](Part& p, int c) __attribute__((always_inline)) {
         p.code = *reinterpret_cast<const u32x4*>(tiles + (int64_t)c * kW4TileBytes);
@@ -173,9 +172,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
                 for (int s = 0; s < 4; ++s) p.x[r][s] = load_x<T>(xr[r] + c * kW4Ins + s * 32, c * kW4Ins + s * 32 + quad * 8 < w.n_in);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (g >= w.per_chunk) continue;
-            const int64_t at = (first_group + c * w.per_chunk + g) * kW4Outs + col;
+        for (int g = 0; g < G; ++g) {
+            const int64_t at = (first_group + c * G + g) * kW4Outs + col;
             p.scale[g] = load_scale(w, at);
             p.zero[g] = w.zeros ? w.zeros[at] : 8;
         }
@@ -209,16 +207,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
                     sum[r] = mfma(x[n], ones<E>(), sum[r]);
                 }
             }
-            if (fold >> s & 1) {
-                const int g = w.per_chunk == 1 ? 0 : w.per_chunk == 2 ? s >> 1 : s;
-                const float sc = scale_value(g == 0 ? p.scale[0] : g == 1 ? p.scale[1] : g == 2 ? p.scale[2] : p.scale[3], w.scale_dtype);
-                const float z = (float)(g == 0 ? p.zero[0] : g == 1 ? p.zero[1] : g == 2 ? p.zero[2] : p.zero[3]);
+            if ((s + 1) * G % 4 == 0) {  // a group ends
+                const int g = s * G / 4;
+                const float sc = scale_value(p.scale[g], w.scale_dtype);
+                const float z = (float)p.zero[g];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) tot[r][j] = __builtin_fmaf(sc, __builtin_fmaf(-z, sum[r][j], part[r][j]), tot[r][j]);
                     part[r] = sum[r] = f32x4{0, 0, 0, 0};
                 }
+                if (R > 1) __builtin_amdgcn_sched_barrier(0);  // as few registers as there are
             }
         }
     };
@@ -263,9 +262,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
             ask(p, c);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int g = w.per_chunk == 1 ? 0 : w.per_chunk == 2 ? s >> 1 : s;
-                const float sc = scale_value(g == 0 ? p.scale[0] : g == 1 ? p.scale[1] : g == 2 ? p.scale[2] : p.scale[3], w.scale_dtype);
-                const E8 cw = weights_of<E>(p.code[s], (int)(g == 0 ? p.zero[0] : g == 1 ? p.zero[1] : g == 2 ? p.zero[2] : p.zero[3]));
+                const int g = s * G / 4;
+                const float sc = scale_value(p.scale[g], w.scale_dtype);
+                const E8 cw = weights_of<E>(p.code[s], (int)p.zero[g]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     E8 x[N];
@@ -298,160 +297,254 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
     }
 }
 
-// Many rows: one workgroup of four waves per (16 RT rows, 128 outputs), two by two; a wave has 8 RT rows x 64 outputs. The
-// workgroup's x of a chunk of 128 inputs is in LDS as operands (two chunks: one is read while the next one's loads are
-// on their way), each wave widens the codes of its outputs itself.
-template <typename T, int RT>
+// Many rows: one workgroup of four waves per (64 H rows, 128 outputs), two by two; a wave has 32 H rows x 64 outputs, in products
+// of 32x32x16. The workgroup's x of a chunk of 128 inputs is in LDS as operands (two chunks: one is read while the next one's
+// loads are on their way), with the sums of each row and group, three bf16 terms of them, that take the zero points out: one
+// more product per group, with -z as the other operand. Each wave widens the codes of its outputs itself.
+//
+// Operand slots: step (s, e) of a chunk, lane half h: inputs 32 s + 8 (h + 2 e) + j, so that a lane's 16 bytes of quad h + 2 e of a
+// tile are its operands of four steps.
+constexpr int kTileOuts = 128;
+
+template <typename T>
+__device__ inline float sum8(const XRaw<T>& r) {
+    float v = 0.0f;
+    if constexpr (sizeof(T) == 4) {
+        float x[8];
+        __builtin_memcpy(x, r.v, sizeof x);
+        v = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t u = r.v[0][k];  // a bit cast of the vector's element itself would take the first one
+            if constexpr (__is_same(T, __bf16)) v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, v, false);
+            else v = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, u), f16x2{(_Float16)1.0f, (_Float16)1.0f}, v, false);
+        }
+    }
+    return v;
+}
+// x summed over the lanes of its four neighbours.
+__device__ inline float quad_sum(float x) {
+    x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0xb1, 0xf, 0xf, true));  // 1 0 3 2
+    x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x4e, 0xf, 0xf, true));  // 2 3 0 1
+    return x;
+}
+
+template <typename T, int H, int G>
 __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, int out_blocks) {
     typedef Kind<T> Kd;
     typedef typename Kd::E E;
     typedef typename Vec8<E>::t E8;
-    constexpr int N = Kd::kTerms, H = RT / 2;
+    constexpr int N = Kd::kTerms, kRows = 64 * H;
     const W4View& w = a.w;
     // Workgroups go to the 8 dies in turn: a die takes its own outputs, with all rows one after the other.
     const int die = blockIdx.x & 7, nth = blockIdx.x >> 3;
     const int ob = die + 8 * (nth / row_blocks), rb = nth % row_blocks;
     if (ob >= out_blocks) return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-    const int64_t r0 = (int64_t)rb * 16 * RT;
-    const int rows = (int)min((int64_t)16 * RT, a.rows - r0);
-    const int half = wave & 1, tile0 = ob * 8 + (wave >> 1) * 4;
-    const int fold = w.per_chunk == 1 ? 8 : w.per_chunk == 2 ? 10 : 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    const int64_t r0 = (int64_t)rb * kRows;
+    const int rows = (int)min((int64_t)kRows, a.rows - r0);
+    const int row0 = (wave & 1) * 32 * H, tile0 = ob * 8 + (wave >> 1) * 4;
     extern __shared__ __attribute__((aligned(128))) uint8_t s_dyn[];
-    E8* const s_x = reinterpret_cast<E8*>(s_dyn);  // [2][RT][4][N][64 lanes]
+    E8* const s_x = reinterpret_cast<E8*>(s_dyn);  // [2][2 H row tiles][8 steps][N][2 halves][32 rows, changed places]
+    constexpr int kBuf = 2 * H * 8 * N * 64;
+    bf16x8* const s_sum = reinterpret_cast<bf16x8*>(s_dyn + 2 * kBuf * 16);  // [2][G][rows]
 
-    // The wave stages RT of the 4 RT (row tile, product) operands.
-    XRaw<T> stage[RT];
+    // Staging: a wave brings 16 H rows in units of 16 rows x 32 inputs: lane 4 r + q has quad q of row r. Places in LDS: row r of (step,
+    // half) at r ^ 4 q, so that a unit's 64 stores meet no bank twice.
+    XRaw<T> stage[H][4];
+    const int sr = lane >> 2, sq = lane & 3;
+    const T* xs[H];
+#pragma unroll
+    for (int u = 0; u < H; ++u) xs[u] = static_cast<const T*>(a.x) + (r0 + min(wave * 16 * H + u * 16 + sr, rows - 1)) * a.x_row + sq * 8;
     const auto ask_x = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int f = wave * RT + i, rt = f >> 2, s = f & 3;
-            const int k = c * kW4Ins + s * 32 + quad * 8;
-            stage[i] = load_x<T>(static_cast<const T*>(a.x) + (r0 + min(16 * rt + col, rows - 1)) * a.x_row + k, k < w.n_in);
-        }
+        for (int u = 0; u < H; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) stage[u][s] = load_x<T>(xs[u] + c * kW4Ins + s * 32, c * kW4Ins + s * 32 + sq * 8 < w.n_in);
     };
     const auto put_x = [&](int c) __attribute__((always_inline)) {
+        E8* const to = s_x + (c & 1) * kBuf;
+        bf16x8* const sums = s_sum + (c & 1) * G * kRows;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            E8 o[N];
-            operands<T>(o, stage[i]);
+        for (int u = 0; u < H; ++u) {
+            const int row = wave * 16 * H + u * 16 + sr;
+            float part[4];
 #pragma unroll
-            for (int n = 0; n < N; ++n) s_x[(((c & 1) * RT * 4 + wave * RT + i) * N + n) * 64 + lane] = o[n];
+            for (int s = 0; s < 4; ++s) {
+                E8 o[N];
+                operands<T>(o, stage[u][s]);
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    to[((((row >> 5) * 8 + 2 * s + (sq >> 1)) * N + n) * 2 + (sq & 1)) * 32 + ((row & 31) ^ (4 * sq))] = o[n];
+                part[s] = quad_sum(sum8<T>(stage[u][s]));
+            }
+            // Lane q writes group q's sum.
+            float v = G == 4 ? (sq == 0 ? part[0] : sq == 1 ? part[1] : sq == 2 ? part[2] : part[3])
+                             : G == 2 ? (sq ? part[2] + part[3] : part[0] + part[1]) : (part[0] + part[1]) + (part[2] + part[3]);
+            u32x4 t = {0, 0, 0, 0};
+            const uint32_t t0 = __float_as_uint(v) & 0xffff0000u;
+            v -= __uint_as_float(t0);
+            const uint32_t t1 = __float_as_uint(v) & 0xffff0000u;
+            v -= __uint_as_float(t1);
+            t[0] = t0 >> 16 | t1;
+            t[1] = __float_as_uint(v) >> 16;
+            if (sq < G) sums[sq * kRows + row] = __builtin_bit_cast(bf16x8, t);
         }
     };
-    const uint8_t* tiles[4];
-    int64_t groups[4];
+    // Codes of outputs 32 t + col: quads h and h + 2 of the tile.
+    const uint8_t* tiles[2];
+    int64_t groups[2];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int64_t tile = min(tile0 + t, w.out_tiles - 1);  // past the last: not stored
-        tiles[t] = w.tiles + tile * w.chunks * kW4TileBytes + lane * 16;
-        groups[t] = tile * w.chunks * w.per_chunk;
+    for (int t = 0; t < 2; ++t) {
+        const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);  // past the last: not stored
+        tiles[t] = w.tiles + tile * w.chunks * kW4TileBytes + (h * 16 + (col & 15)) * 16;
+        groups[t] = tile * w.chunks * G * kW4Outs + (col & 15);
     }
-    u32x4 code[4], next[4];
-    const auto ask_codes = [&](u32x4* o, int c) __attribute__((always_inline)) {
+    u32x4 code[2][2], next[2][2];
+    uint32_t scale[2][G], zero[2][G], next_scale[2][G], next_zero[2][G];
+    const auto ask_codes = [&](u32x4 (&o)[2][2], uint32_t (&sc)[2][G], uint32_t (&z)[2][G], int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] = *reinterpret_cast<const u32x4*>(tiles[t] + (int64_t)c * kW4TileBytes);
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) o[t][e] = *reinterpret_cast<const u32x4*>(tiles[t] + (int64_t)c * kW4TileBytes + e * 512);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int64_t at = groups[t] + (c * G + g) * kW4Outs;
+                sc[t][g] = load_scale(w, at);
+                z[t][g] = w.zeros ? w.zeros[at] : 8;
+            }
+        }
     };
-    f32x4 tot[H][4];
+    f32x16 tot[H][2];
 #pragma unroll
     for (int r = 0; r < H; ++r)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) tot[r][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) tot[r][t][j] = 0.0f;
 
     ask_x(0);
-    ask_codes(code, 0);
+    ask_codes(code, scale, zero, 0);
     put_x(0);
     for (int c = 0; c < w.chunks; ++c) {
         __syncthreads();
         if (c + 1 < w.chunks) {
             ask_x(c + 1);
-            ask_codes(next, c + 1);
+            ask_codes(next, next_scale, next_zero, c + 1);
         }
-        f32x4 part[H][4], sum[H];
+        const E8* const from = s_x + (c & 1) * kBuf + (row0 >> 5) * 8 * N * 64 + h * 32;
+        const bf16x8* const sums = s_sum + (c & 1) * G * kRows + row0 + col;
+        f32x16 part[H][2];
 #pragma unroll
-        for (int r = 0; r < H; ++r) {
-            sum[r] = f32x4{0, 0, 0, 0};
+        for (int r = 0; r < H; ++r)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) part[r][t] = f32x4{0, 0, 0, 0};
-        }
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[r][t][j] = 0.0f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            E8 cw[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) cw[t] = codes_of<E>(code[t][s]);
+            for (int e = 0; e < 2; ++e) {
+                E8 cw[2];
 #pragma unroll
-            for (int r = 0; r < H; ++r)
+                for (int t = 0; t < 2; ++t) cw[t] = codes_of<E>(code[t][e][s]);
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const E8 x = s_x[(((c & 1) * RT * 4 + (half * H + r) * 4 + s) * N + n) * 64 + lane];
-                    sum[r] = mfma(x, ones<E>(), sum[r]);
+                for (int r = 0; r < H; ++r)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) part[r][t] = mfma(x, cw[t], part[r][t]);
-                }
-            if (fold >> s & 1) {
-                const int g = w.per_chunk == 1 ? 0 : w.per_chunk == 2 ? s >> 1 : s;
+                    for (int n = 0; n < N; ++n) {
+                        const E8 x = from[((r * 8 + 2 * s + e) * N + n) * 64 + (col ^ (4 * (h + 2 * e)))];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int64_t at = (groups[t] + c * w.per_chunk + g) * kW4Outs + col;
-                    const float sc = scale_value(load_scale(w, at), w.scale_dtype), z = w.zeros ? (float)w.zeros[at] : 8.0f;
+                        for (int t = 0; t < 2; ++t) part[r][t] = mfma(x, cw[t], part[r][t]);
+                    }
+            }
+            if ((s + 1) * G % 4 == 0) {  // a group ends
+                const int g = s * G / 4;
+                bf16x8 xs8[H];
+#pragma unroll
+                for (int r = 0; r < H; ++r) xs8[r] = sums[g * kRows + 32 * r];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float sc = scale_value(scale[t][g], w.scale_dtype);
+                    const float z = (float)zero[t][g];
+                    const uint32_t zb = h ? 0u : __float_as_uint(-z);  // whole numbers up to 15: the upper half is bf16
+                    const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{zb >> 16 | zb, zb >> 16, 0, 0});
 #pragma unroll
                     for (int r = 0; r < H; ++r) {
+                        part[r][t] = mfma(xs8[r], minus, part[r][t]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) tot[r][t][j] = __builtin_fmaf(sc, __builtin_fmaf(-z, sum[r][j], part[r][t][j]), tot[r][t][j]);
-                        part[r][t] = f32x4{0, 0, 0, 0};
+                        for (int j = 0; j < 16; ++j) {
+                            tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
+                            part[r][t][j] = 0.0f;
+                        }
                     }
                 }
-#pragma unroll
-                for (int r = 0; r < H; ++r) sum[r] = f32x4{0, 0, 0, 0};
+                if (G > 1) __builtin_amdgcn_sched_barrier(0);  // two groups' sums at a time would not fit
             }
         }
         if (c + 1 < w.chunks) {
             put_x(c + 1);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) code[t] = next[t];
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) code[t][e] = next[t][e];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    scale[t][g] = next_scale[t][g];
+                    zero[t][g] = next_zero[t][g];
+                }
+            }
         }
     }
     bool odd = false;
 #pragma unroll
     for (int r = 0; r < H; ++r)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) odd |= not_finite(tot[r][t][j]);
+            for (int j = 0; j < 16; ++j) odd |= not_finite(tot[r][t][j]);
     if (__any(odd)) {
-        // Every output tile of the wave again, one row tile at a time, x from memory.
+        // The wave's products again, one at a time, x from memory.
 #pragma unroll 1
         for (int r = 0; r < H; ++r) {
 #pragma unroll 1
-            for (int t = 0; t < 4; ++t) {
-                const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(16 * (half * H + r) + col, rows - 1)) * a.x_row + quad * 8;
-                const int64_t tile = min(tile0 + t, w.out_tiles - 1);
-                f32x4 again = {0, 0, 0, 0};
+            for (int t = 0; t < 2; ++t) {
+                const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(row0 + 32 * r + col, rows - 1)) * a.x_row;
+                const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);
+                f32x16 again;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) again[j] = 0.0f;
 #pragma unroll 1
                 for (int c = 0; c < w.chunks; ++c) {
-                    const u32x4 cd = *reinterpret_cast<const u32x4*>(w.tiles + (tile * w.chunks + c) * kW4TileBytes + lane * 16);
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        const int q = h + 2 * e;
+                        const u32x4 cd = *reinterpret_cast<const u32x4*>(w.tiles + (tile * w.chunks + c) * kW4TileBytes + (q * 16 + (col & 15)) * 16);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int g = w.per_chunk == 1 ? 0 : w.per_chunk == 2 ? s >> 1 : s, k = c * kW4Ins + s * 32;
-                        const int64_t at = ((tile * w.chunks + c) * w.per_chunk + g) * kW4Outs + col;
-                        const float sc = scale_value(load_scale(w, at), w.scale_dtype);
-                        const E8 cw = weights_of<E>(cd[s], w.zeros ? w.zeros[at] : 8);
-                        E8 x[N];
-                        operands_of_any<T>(x, load_x<T>(x0 + k, k + quad * 8 < w.n_in));
-                        f32x4 part = {0, 0, 0, 0};
+                        for (int s = 0; s < 4; ++s) {
+                            const int g = s * G / 4, k = c * kW4Ins + s * 32 + q * 8;
+                            const int64_t at = ((tile * w.chunks + c) * G + g) * kW4Outs + (col & 15);
+                            const float sc = scale_value(load_scale(w, at), w.scale_dtype);
+                            const E8 cw = weights_of<E>(cd[s], w.zeros ? w.zeros[at] : 8);
+                            E8 x[N];
+                            operands_of_any<T>(x, load_x<T>(x0 + k, k < w.n_in));
+                            f32x16 part;
 #pragma unroll
-                        for (int n = 0; n < N; ++n) part = mfma(x[n], cw, part);
+                            for (int j = 0; j < 16; ++j) part[j] = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) again[j] = __builtin_fmaf(sc, part[j], again[j]);
+                            for (int n = 0; n < N; ++n) part = mfma(x[n], cw, part);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) again[j] = __builtin_fmaf(sc, part[j], again[j]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int rr = 0; rr < H; ++rr)
 #pragma unroll
-                    for (int tt = 0; tt < 4; ++tt)
+                    for (int tt = 0; tt < 2; ++tt)
                         if (rr == r && tt == t)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                            for (int j = 0; j < 16; ++j)
                                 if (not_finite(tot[rr][tt][j])) tot[rr][tt][j] = again[j];
             }
         }
@@ -459,11 +552,11 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
 #pragma unroll
     for (int r = 0; r < H; ++r)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 16 * (half * H + r) + 4 * quad + j, out = (tile0 + t) * kW4Outs + col;
-                if (row < rows && tile0 + t < w.out_tiles && out < w.n_out) put(a, r0 + row, out, tot[r][t][j]);
+            for (int j = 0; j < 16; ++j) {
+                const int row = row0 + 32 * r + 8 * (j >> 2) + 4 * h + (j & 3), tile = tile0 + 2 * t + (col >> 4), out = tile * kW4Outs + (col & 15);
+                if (row < rows && out < w.n_out) put(a, r0 + row, out, tot[r][t][j]);
             }
 }
 
@@ -498,34 +591,54 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4PackArgs a) {
 constexpr int kStageBytes = 96 * 1024;
 int stage_bytes(const W4Args& a) { return (int)std::min<int64_t>(1 << 30, a.rows * (a.w.chunks * kW4Ins + 8) * 3 * 2); }
 
-template <typename T, int R, int U>
+template <typename T, int R, int U, int G>
 hipError_t rows_as(const W4Args& a, hipStream_t s) {
     const dim3 grid(a.w.out_tiles, (unsigned)((a.rows + 16 * R - 1) / (16 * R)));
-    k_w4_rows<T, R, U, false><<<grid, 64 * kWaves, 0, s>>>(a);
+    k_w4_rows<T, R, U, false, G><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T>
-constexpr int kTileRows = sizeof(T) == 2 ? 8 : 4;  // row tiles of a workgroup: what two chunks of LDS hold
-template <typename T>
-constexpr int kTileLds = 2 * kTileRows<T> * 4 * Kind<T>::kTerms * 1024;
+constexpr int kTileH = sizeof(T) == 2 ? 2 : 1;  // what two chunks of LDS hold
+template <typename T, int G>
+constexpr int kTileLds = 2 * (2 * kTileH<T> * 8 * Kind<T>::kTerms * 1024 + G * 64 * kTileH<T> * 16);
 
-template <typename T>
+template <typename T, int G>
 hipError_t w4_as(const W4Args& a, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
         if (a.rows <= 16 && stage_bytes(a) <= kStageBytes) {
-            k_w4_rows<T, 1, 4, true><<<dim3(a.w.out_tiles, 1), 64 * kWaves, stage_bytes(a), s>>>(a);
+            k_w4_rows<T, 1, 4, true, G><<<dim3(a.w.out_tiles, 1), 64 * kWaves, stage_bytes(a), s>>>(a);
             return hipGetLastError();
         }
     }
-    if (a.rows <= 16) return rows_as<T, 1, sizeof(T) == 2 ? 4 : 2>(a, s);
-    if (a.rows <= 32) return rows_as<T, 2, sizeof(T) == 2 ? 2 : 1>(a, s);
-    if (a.rows <= 64) return rows_as<T, 4, sizeof(T) == 2 ? 2 : 1>(a, s);
-    constexpr int RT = kTileRows<T>;
-    const int row_blocks = (int)((a.rows + 16 * RT - 1) / (16 * RT)), out_blocks = (a.w.out_tiles + 7) / 8;
+    if (a.rows <= 16) return rows_as<T, 1, sizeof(T) == 2 ? 4 : 2, G>(a, s);
+    if (a.rows <= 32) return rows_as<T, 2, sizeof(T) == 2 ? 2 : 1, G>(a, s);
+    if (a.rows <= 64) return rows_as<T, 4, sizeof(T) == 2 ? 2 : 1, G>(a, s);
+    constexpr int H = kTileH<T>;
+    const int row_blocks = (int)((a.rows + 64 * H - 1) / (64 * H)), out_blocks = (a.w.n_out + kTileOuts - 1) / kTileOuts;
     const unsigned grid = (unsigned)((out_blocks + 7) / 8 * 8) * row_blocks;
-    k_w4_tile<T, RT><<<grid, 256, kTileLds<T>, s>>>(a, row_blocks, out_blocks);
+    k_w4_tile<T, H, G><<<grid, 256, kTileLds<T, G>, s>>>(a, row_blocks, out_blocks);
     return hipGetLastError();
+}
+template <typename T>
+hipError_t w4_any(const W4Args& a, hipStream_t s) {
+    return a.w.per_chunk == 1 ? w4_as<T, 1>(a, s) : a.w.per_chunk == 2 ? w4_as<T, 2>(a, s) : w4_as<T, 4>(a, s);
+}
+
+template <typename T, int G>
+hipError_t prepare() {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_w4_tile<T, kTileH<T>, G>), hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds<T, G>);
+    if constexpr (sizeof(T) == 4) {
+        if (e == hipSuccess)
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_w4_rows<T, 1, 4, true, G>), hipFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
+    }
+    return e;
+}
+template <typename T>
+hipError_t prepare_all() {
+    for (hipError_t e : {prepare<T, 1>(), prepare<T, 2>(), prepare<T, 4>()})
+        if (e != hipSuccess) return e;
+    return hipSuccess;
 }
 
 }  // namespace
@@ -537,9 +650,9 @@ hipError_t launch_w4_pack(const W4PackArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_w4(const W4Args& a, int x_dtype, hipStream_t s) {
-    if (x_dtype == 0) return w4_as<float>(a, s);
-    if (x_dtype == 1) return w4_as<__bf16>(a, s);
-    return w4_as<_Float16>(a, s);
+    if (x_dtype == 0) return w4_any<float>(a, s);
+    if (x_dtype == 1) return w4_any<__bf16>(a, s);
+    return w4_any<_Float16>(a, s);
 }
 
 hipError_t w4_prepare() {
@@ -547,14 +660,8 @@ hipError_t w4_prepare() {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
-    const auto allow = [&](const void* f, int bytes) {
-        const hipError_t x = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    for (hipError_t x : {prepare_all<float>(), prepare_all<__bf16>(), prepare_all<_Float16>()})
         if (x != hipSuccess) e = x;
-    };
-    allow(reinterpret_cast<const void*>(k_w4_rows<float, 1, 4, true>), kStageBytes);
-    allow(reinterpret_cast<const void*>(k_w4_tile<float, kTileRows<float>>), kTileLds<float>);
-    allow(reinterpret_cast<const void*>(k_w4_tile<__bf16, kTileRows<__bf16>>), kTileLds<__bf16>);
-    allow(reinterpret_cast<const void*>(k_w4_tile<_Float16, kTileRows<_Float16>>), kTileLds<_Float16>);
     if (e == hipSuccess && dev < 64) done.fetch_or(1ull << dev);
     return e;
 }
