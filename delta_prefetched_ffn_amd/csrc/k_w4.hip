@@ -57,14 +57,16 @@ __device__ inline typename Vec8<E>::t ones() {
     return o;
 }
 
-__device__ inline float scale_value(uint32_t raw, int dtype) {
-    if (dtype == 0) return __uint_as_float(raw);
-    if (dtype == 1) return __uint_as_float(raw << 16);
-    return (float)__builtin_bit_cast(_Float16, (uint16_t)raw);
+// A group's scale and zero point, as they are loaded, and their values.
+struct __attribute__((packed, aligned(4))) ScaleWords {
+    uint32_t w[2];
+};
+__device__ inline u32x2 load_scale(const W4View& w, int64_t at) {
+    const ScaleWords s = *reinterpret_cast<const ScaleWords*>(w.scales + at * w.scale_words);
+    return u32x2{s.w[0], s.w[1]};
 }
-__device__ inline uint32_t load_scale(const W4View& w, int64_t at) {
-    return w.scale_dtype == 0 ? static_cast<const uint32_t*>(w.scales)[at] : static_cast<const uint16_t*>(w.scales)[at];
-}
+__device__ inline float scale_value(u32x2 s, int words) { return __uint_as_float(s[0] & (words == 1 ? ~15u : ~0u)); }
+__device__ inline int zero_value(u32x2 s, int words) { return (int)((words == 1 ? s[0] : s[1]) & 15); }
 
 // y = v, or y + v, rounded once.
 __device__ inline void put(const W4Args& a, int64_t row, int out, float v) {
@@ -131,40 +133,46 @@ __device__ inline void operands_of_any(typename Vec8<typename Kind<T>::E>::t* o,
 }
 
 constexpr int kWaves = 8;
-constexpr int kPartStride = kW4Outs + 1;
 
-// Few rows: one workgroup per 16 outputs and 16 R rows; its waves take every kWaves-th chunk of 128 inputs and are joined
+// Few rows: one workgroup per 16 O outputs and 16 R rows; its waves take every kWaves-th chunk of 128 inputs and are joined
 // in LDS, in their order. A lane's 16 bytes of a tile are its operands of four products, x the other one: D row = row of x,
-// D column = output. x comes from the caches (kStaged: fp32, split once per workgroup into LDS).
-template <typename T, int R, int U, bool kStaged, int G>
-__global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
+// D column = output. x comes from the caches, once for O tiles (kStaged: fp32, split once per workgroup into LDS). U chunks are on
+// their way at a time.
+//
+// Bound by the weights' way from memory at first: one row of 4096 x 11008 takes 7.6 us (3.1 TB/s), of 32,000 x 4096 13.3 us (5.1 TB/s;
+// 25 us before O went up to 4, since every workgroup reads all of x), with the empty launch's 3.5. From 16 rows on the widening and
+// the folds of the groups' sums bound it, with 4096 outputs' 256 workgroups one wave or two a SIMD: 64 rows of 4096 x 4096 18 us.
+template <typename T, int R, int O, int U, bool kStaged, int G>
+__global__ __launch_bounds__(64 * kWaves, R == 1 ? 4 : 2) void k_w4_rows(W4Args a) {
     typedef Kind<T> Kd;
     typedef typename Kd::E E;
     typedef typename Vec8<E>::t E8;
-    constexpr int N = Kd::kTerms;
+    constexpr int N = Kd::kTerms, kStride = kW4Outs * O + 1;
     const W4View& w = a.w;
-    const int tile = blockIdx.x, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const int tile0 = blockIdx.x * O, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int64_t r0 = (int64_t)blockIdx.y * 16 * R;
     const int rows = (int)min((int64_t)16 * R, a.rows - r0);
-    const uint8_t* const tiles = w.tiles + (int64_t)tile * w.chunks * kW4TileBytes + lane * 16;
-    const int64_t first_group = (int64_t)tile * w.chunks * G;
-    __shared__ float s_part[kWaves * 16 * R * kPartStride];
     extern __shared__ __attribute__((aligned(128))) uint8_t s_dyn[];
-    E* const s_x = reinterpret_cast<E*>(s_dyn);  // [N][rows][x_len]
+    E* const s_x = reinterpret_cast<E*>(s_dyn);              // [N][rows][x_len]
+    float* const s_part = reinterpret_cast<float*>(s_dyn);   // [waves][16 R][kStride], behind the products
     const int x_len = w.chunks * kW4Ins + 8;
 
-    // Rows past the last read the last one: what they give is not stored.
+    // Rows past the last read the last one, tiles past the last the last one: what they give is not stored.
     const T* xr[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) xr[r] = static_cast<const T*>(a.x) + (r0 + min(16 * r + col, rows - 1)) * a.x_row + quad * 8;
+    int tile[O];
+#pragma unroll
+    for (int o = 0; o < O; ++o) tile[o] = min(tile0 + o, w.out_tiles - 1);
 
     struct Part {
-        u32x4 code;
+        u32x4 code[O];
         XRaw<T> x[kStaged ? 1 : R][4];
-        uint32_t scale[G], zero[G];
+        u32x2 scale[O][G];
     };
     const auto ask = [&](Part& p, int c) __attribute__((always_inline)) {
-        p.code = *reinterpret_cast<const u32x4*>(tiles + (int64_t)c * kW4TileBytes);
+#pragma unroll
+        for (int o = 0; o < O; ++o) p.code[o] = *reinterpret_cast<const u32x4*>(w.tiles + ((int64_t)tile[o] * w.chunks + c) * kW4TileBytes + lane * 16);
         if constexpr (!kStaged) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -172,11 +180,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
                 for (int s = 0; s < 4; ++s) p.x[r][s] = load_x<T>(xr[r] + c * kW4Ins + s * 32, c * kW4Ins + s * 32 + quad * 8 < w.n_in);
         }
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int64_t at = (first_group + c * G + g) * kW4Outs + col;
-            p.scale[g] = load_scale(w, at);
-            p.zero[g] = w.zeros ? w.zeros[at] : 8;
-        }
+        for (int o = 0; o < O; ++o)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int64_t at = (((int64_t)tile[o] * w.chunks + c) * G + g) * kW4Outs + col;
+                p.scale[o][g] = load_scale(w, at);
+            }
     };
     const auto x_of = [&](E8* o, const Part& p, int c, int r, int s) __attribute__((always_inline)) {
         if constexpr (kStaged) {
@@ -187,37 +196,47 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
             operands<T>(o, p.x[r][s]);
         }
     };
-    f32x4 tot[R];
+    f32x4 tot[R][O];
 #pragma unroll
-    for (int r = 0; r < R; ++r) tot[r] = f32x4{0, 0, 0, 0};
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int o = 0; o < O; ++o) tot[r][o] = f32x4{0, 0, 0, 0};
     const auto products = [&](const Part& p, int c) __attribute__((always_inline)) {
-        f32x4 part[R], sum[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) part[r] = sum[r] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const E8 cw = codes_of<E>(p.code[s]);
+        for (int g = 0; g < G; ++g) {
+            f32x4 part[R][O], sum[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                E8 x[N];
-                x_of(x, p, c, r, s);
+                sum[r] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    part[r] = mfma(x[n], cw, part[r]);
-                    sum[r] = mfma(x[n], ones<E>(), sum[r]);
-                }
+                for (int o = 0; o < O; ++o) part[r][o] = f32x4{0, 0, 0, 0};
             }
-            if ((s + 1) * G % 4 == 0) {  // a group ends
-                const int g = s * G / 4;
-                const float sc = scale_value(p.scale[g], w.scale_dtype);
-                const float z = (float)p.zero[g];
+#pragma unroll
+            for (int s = g * 4 / G; s < (g + 1) * 4 / G; ++s) {
+                E8 cw[O];
+#pragma unroll
+                for (int o = 0; o < O; ++o) cw[o] = codes_of<E>(p.code[o][s]);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    E8 x[N];
+                    x_of(x, p, c, r, s);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tot[r][j] = __builtin_fmaf(sc, __builtin_fmaf(-z, sum[r][j], part[r][j]), tot[r][j]);
-                    part[r] = sum[r] = f32x4{0, 0, 0, 0};
+                    for (int n = 0; n < N; ++n) {
+                        sum[r] = mfma(x[n], ones<E>(), sum[r]);
+#pragma unroll
+                        for (int o = 0; o < O; ++o) part[r][o] = mfma(x[n], cw[o], part[r][o]);
+                    }
                 }
-                if (R > 1) __builtin_amdgcn_sched_barrier(0);  // as few registers as there are
+            }
+#pragma unroll
+            for (int o = 0; o < O; ++o) {
+                const float sc = scale_value(p.scale[o][g], w.scale_words), z = (float)zero_value(p.scale[o][g], w.scale_words);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tot[r][o][j] = __builtin_fmaf(sc, __builtin_fmaf(-z, sum[r][j], part[r][o][j]), tot[r][o][j]);
+#pragma unroll
+                for (int r = 0; r < R; ++r) asm volatile("" : "+v"(tot[r][o]));  // here, not behind the loads to come
             }
         }
     };
@@ -251,49 +270,57 @@ __global__ __launch_bounds__(64 * kWaves) void k_w4_rows(W4Args a) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) odd |= not_finite(tot[r][j]);
+        for (int o = 0; o < O; ++o)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) odd |= not_finite(tot[r][o][j]);
     if (__any(odd)) {
-        f32x4 again[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) again[r] = f32x4{0, 0, 0, 0};
+        // The wave's products again, one at a time.
 #pragma unroll 1
-        for (int c = wave; c < w.chunks; c += kWaves) {
-            Part p;
-            ask(p, c);
+        for (int ro = 0; ro < R * O; ++ro) {
+            const int r = ro / O, t = min(tile0 + ro - r * O, w.out_tiles - 1);
+            const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(16 * r + col, rows - 1)) * a.x_row;
+            f32x4 again = {0, 0, 0, 0};
+#pragma unroll 1
+            for (int c = wave; c < w.chunks; c += kWaves) {
+                const u32x4 code = *reinterpret_cast<const u32x4*>(w.tiles + ((int64_t)t * w.chunks + c) * kW4TileBytes + lane * 16);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int g = s * G / 4;
-                const float sc = scale_value(p.scale[g], w.scale_dtype);
-                const E8 cw = weights_of<E>(p.code[s], (int)p.zero[g]);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int s = 0; s < 4; ++s) {
+                    const int64_t at = (((int64_t)t * w.chunks + c) * G + s * G / 4) * kW4Outs + col;
+                    const u32x2 words = load_scale(w, at);
+                    const float sc = scale_value(words, w.scale_words);
+                    const E8 cw = weights_of<E>(code[s], zero_value(words, w.scale_words));
+                    const int k = c * kW4Ins + s * 32 + quad * 8;
                     E8 x[N];
-                    operands_of_any<T>(x, load_x<T>(xr[r] + c * kW4Ins + s * 32, c * kW4Ins + s * 32 + quad * 8 < w.n_in));
+                    operands_of_any<T>(x, load_x<T>(x0 + k, k < w.n_in));
                     f32x4 part = {0, 0, 0, 0};
 #pragma unroll
                     for (int n = 0; n < N; ++n) part = mfma(x[n], cw, part);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) again[r][j] = __builtin_fmaf(sc, part[j], again[r][j]);
+                    for (int j = 0; j < 4; ++j) again[j] = __builtin_fmaf(sc, part[j], again[j]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < R * O; ++i)
+                if (i == ro)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (not_finite(tot[i / O][i % O][j])) tot[i / O][i % O][j] = again[j];
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (not_finite(tot[r][j])) tot[r][j] = again[r][j];
     }
+    if (kStaged) __syncthreads();  // x is done with
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_part[(wave * 16 * R + 16 * r + 4 * quad + j) * kPartStride + col] = tot[r][j];
+        for (int o = 0; o < O; ++o)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s_part[(wave * 16 * R + 16 * r + 4 * quad + j) * kStride + kW4Outs * o + col] = tot[r][o][j];
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * kW4Outs; i += 64 * kWaves) {
-        const int r = i / kW4Outs, o = i & (kW4Outs - 1);
+    for (int i = threadIdx.x; i < rows * kW4Outs * O; i += 64 * kWaves) {
+        const int r = i / (kW4Outs * O), out = i % (kW4Outs * O);
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) v += s_part[(k * 16 * R + r) * kPartStride + o];
-        if (tile * kW4Outs + o < w.n_out) put(a, r0 + r, tile * kW4Outs + o, v);
+        for (int k = 0; k < kWaves; ++k) v += s_part[(k * 16 * R + r) * kStride + out];
+        if (tile0 * kW4Outs + out < w.n_out) put(a, r0 + r, tile0 * kW4Outs + out, v);
     }
 }
 
@@ -402,19 +429,21 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
         groups[t] = tile * w.chunks * G * kW4Outs + (col & 15);
     }
     u32x4 code[2][2], next[2][2];
-    uint32_t scale[2][G], zero[2][G], next_scale[2][G], next_zero[2][G];
-    const auto ask_codes = [&](u32x4 (&o)[2][2], uint32_t (&sc)[2][G], uint32_t (&z)[2][G], int c) __attribute__((always_inline)) {
+    u32x2 scale[2][G];
+    const auto ask_codes = [&](u32x4 (&o)[2][2], int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) o[t][e] = *reinterpret_cast<const u32x4*>(tiles[t] + (int64_t)c * kW4TileBytes + e * 512);
+    };
+    const auto ask_scales = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const int64_t at = groups[t] + (c * G + g) * kW4Outs;
-                sc[t][g] = load_scale(w, at);
-                z[t][g] = w.zeros ? w.zeros[at] : 8;
+                scale[t][g] = load_scale(w, at);
             }
-        }
     };
     f32x16 tot[H][2];
 #pragma unroll
@@ -425,27 +454,29 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             for (int j = 0; j < 16; ++j) tot[r][t][j] = 0.0f;
 
     ask_x(0);
-    ask_codes(code, scale, zero, 0);
+    ask_codes(code, 0);
     put_x(0);
     for (int c = 0; c < w.chunks; ++c) {
         __syncthreads();
+        ask_scales(c);  // used behind the first group's products
         if (c + 1 < w.chunks) {
             ask_x(c + 1);
-            ask_codes(next, next_scale, next_zero, c + 1);
+            ask_codes(next, c + 1);
         }
         const E8* const from = s_x + (c & 1) * kBuf + (row0 >> 5) * 8 * N * 64 + h * 32;
         const bf16x8* const sums = s_sum + (c & 1) * G * kRows + row0 + col;
-        f32x16 part[H][2];
 #pragma unroll
-        for (int r = 0; r < H; ++r)
+        for (int g = 0; g < G; ++g) {
+            f32x16 part[H][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int r = 0; r < H; ++r)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[r][t][j] = 0.0f;
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+                    for (int j = 0; j < 16; ++j) part[r][t][j] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int step = g * 8 / G; step < (g + 1) * 8 / G; ++step) {
+                const int s = step >> 1, e = step & 1;
                 E8 cw[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) cw[t] = codes_of<E>(code[t][e][s]);
@@ -453,47 +484,36 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
                 for (int r = 0; r < H; ++r)
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const E8 x = from[((r * 8 + 2 * s + e) * N + n) * 64 + (col ^ (4 * (h + 2 * e)))];
+                        const E8 x = from[((r * 8 + step) * N + n) * 64 + (col ^ (4 * (h + 2 * e)))];
 #pragma unroll
                         for (int t = 0; t < 2; ++t) part[r][t] = mfma(x, cw[t], part[r][t]);
                     }
             }
-            if ((s + 1) * G % 4 == 0) {  // a group ends
-                const int g = s * G / 4;
-                bf16x8 xs8[H];
+            bf16x8 xs8[H];
 #pragma unroll
-                for (int r = 0; r < H; ++r) xs8[r] = sums[g * kRows + 32 * r];
+            for (int r = 0; r < H; ++r) xs8[r] = sums[g * kRows + 32 * r];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float sc = scale_value(scale[t][g], w.scale_dtype);
-                    const float z = (float)zero[t][g];
-                    const uint32_t zb = h ? 0u : __float_as_uint(-z);  // whole numbers up to 15: the upper half is bf16
-                    const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{zb >> 16 | zb, zb >> 16, 0, 0});
+            for (int t = 0; t < 2; ++t) {
+                const float sc = scale_value(scale[t][g], w.scale_words), z = (float)zero_value(scale[t][g], w.scale_words);
+                const uint32_t zb = h ? 0u : __float_as_uint(-z);  // whole numbers up to 15: the upper half is bf16
+                const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{zb >> 16 | zb, zb >> 16, 0, 0});
 #pragma unroll
-                    for (int r = 0; r < H; ++r) {
-                        part[r][t] = mfma(xs8[r], minus, part[r][t]);
+                for (int r = 0; r < H; ++r) {
+                    part[r][t] = mfma(xs8[r], minus, part[r][t]);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
-                            part[r][t][j] = 0.0f;
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j) tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
+                    // Here: the compiler moves these behind the next stores, and all groups' sums wait for them.
+                    if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(tot[r][t]));
                 }
-                if (G > 1) __builtin_amdgcn_sched_barrier(0);  // two groups' sums at a time would not fit
             }
+            if (G > 1) __builtin_amdgcn_sched_barrier(0);
         }
         if (c + 1 < w.chunks) {
             put_x(c + 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) code[t][e] = next[t][e];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    scale[t][g] = next_scale[t][g];
-                    zero[t][g] = next_zero[t][g];
-                }
-            }
         }
     }
     bool odd = false;
@@ -524,8 +544,9 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
                         for (int s = 0; s < 4; ++s) {
                             const int g = s * G / 4, k = c * kW4Ins + s * 32 + q * 8;
                             const int64_t at = ((tile * w.chunks + c) * G + g) * kW4Outs + (col & 15);
-                            const float sc = scale_value(load_scale(w, at), w.scale_dtype);
-                            const E8 cw = weights_of<E>(cd[s], w.zeros ? w.zeros[at] : 8);
+                            const u32x2 words = load_scale(w, at);
+                            const float sc = scale_value(words, w.scale_words);
+                            const E8 cw = weights_of<E>(cd[s], zero_value(words, w.scale_words));
                             E8 x[N];
                             operands_of_any<T>(x, load_x<T>(x0 + k, k < w.n_in));
                             f32x16 part;
@@ -581,21 +602,66 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4PackArgs a) {
         const int out = (int)(at / all) * kW4Outs + (int)(i % kW4Outs), k = (int)(at % all) * (kW4Ins / a.per_chunk);
         const bool in = out < a.n_out && k < a.n_in;
         const int64_t from = (int64_t)out * a.groups + k / a.group;
-        if (a.scale_bytes == 4) static_cast<uint32_t*>(a.scales_out)[i] = in ? static_cast<const uint32_t*>(a.scales)[from] : 0;
-        else static_cast<uint16_t*>(a.scales_out)[i] = in ? static_cast<const uint16_t*>(a.scales)[from] : 0;
-        if (a.zeros) a.zeros_out[i] = in ? a.zeros[from] & 15 : 0;
+        const uint32_t z = !in ? 0 : a.zeros ? a.zeros[from] & 15 : 8;
+        if (a.scale_dtype == 0) {
+            a.scales_out[2 * i] = in ? static_cast<const uint32_t*>(a.scales)[from] : 0;
+            a.scales_out[2 * i + 1] = z;
+        } else {
+            const uint16_t raw = in ? static_cast<const uint16_t*>(a.scales)[from] : 0;
+            const uint32_t v = a.scale_dtype == 1 ? (uint32_t)raw << 16 : __float_as_uint((float)__builtin_bit_cast(_Float16, raw));
+            a.scales_out[i] = (v & ~15u) | z;
+        }
     }
 }
 
-// LDS for x of one workgroup of k_w4_rows, split (fp32); at most this much of it is used.
-constexpr int kStageBytes = 96 * 1024;
-int stage_bytes(const W4Args& a) { return (int)std::min<int64_t>(1 << 30, a.rows * (a.w.chunks * kW4Ins + 8) * 3 * 2); }
+// LDS of k_w4_rows: for x, split (fp32), of which it uses at most kStageBytes, then for the waves' results.
+constexpr int kStageBytes = 80 * 1024;  // half of a compute unit's
+int64_t stage_bytes(const W4Args& a) { return a.rows * (a.w.chunks * kW4Ins + 8) * 3 * 2; }
+template <int R, int O>
+constexpr int kPartLds = kWaves * 16 * R * (kW4Outs * O + 1) * 4;
 
-template <typename T, int R, int U, int G>
+// Output tiles of a workgroup, at most, and chunks on their way at a time: what the registers hold of two workgroups a compute
+// unit (R = 1) or one.
+template <typename T, int R, bool kStaged, int G>
+constexpr int kMostO = sizeof(T) == 2 ? (R == 4 || (R == 1 && G > 1) ? 2 : 4) : R == 4 ? 1 : kStaged && G < 4 ? 4 : 2;
+template <typename T, int R, int O, bool kStaged, int G>
+constexpr int kAhead = sizeof(T) == 4 ? (kStaged && O == 1 ? 2 : 1)
+                       : R == 1       ? (O == 4 ? 1 : O == 2 ? (G == 4 ? 1 : 2) : G == 4 ? 2 : 3)
+                       : R == 2       ? (O == 4 ? 1 : 2)
+                                      : (O == 1 ? 2 : 1);
+// As many as leave one workgroup of 64 rows or less for every compute unit.
+template <typename T, int R, bool kStaged, int G>
+int rows_o(const W4Args& a) {
+    return std::min(a.w.out_tiles < 512 ? 1 : a.w.out_tiles < 1024 ? 2 : 4, kMostO<T, R, kStaged, G>);
+}
+template <typename T, int R, int O, bool kStaged, int G>
+constexpr auto* kRowsKernel = k_w4_rows<T, R, O, kAhead<T, R, O, kStaged, G>, kStaged, G>;
+template <typename T, int R, int O, bool kStaged, int G>
 hipError_t rows_as(const W4Args& a, hipStream_t s) {
-    const dim3 grid(a.w.out_tiles, (unsigned)((a.rows + 16 * R - 1) / (16 * R)));
-    k_w4_rows<T, R, U, false, G><<<grid, 64 * kWaves, 0, s>>>(a);
+    const dim3 grid((a.w.out_tiles + O - 1) / O, (unsigned)((a.rows + 16 * R - 1) / (16 * R)));
+    const int lds = kStaged ? std::max(kPartLds<R, O>, (int)stage_bytes(a)) : kPartLds<R, O>;
+    kRowsKernel<T, R, O, kStaged, G><<<grid, 64 * kWaves, lds, s>>>(a);
     return hipGetLastError();
+}
+template <typename T, int R, bool kStaged, int G>
+hipError_t rows_of(const W4Args& a, hipStream_t s) {
+    const int o = rows_o<T, R, kStaged, G>(a);
+    if constexpr (kMostO<T, R, kStaged, G> >= 4)
+        if (o == 4) return rows_as<T, R, 4, kStaged, G>(a, s);
+    if constexpr (kMostO<T, R, kStaged, G> >= 2)
+        if (o == 2) return rows_as<T, R, 2, kStaged, G>(a, s);
+    return rows_as<T, R, 1, kStaged, G>(a, s);
+}
+template <typename T, int R, bool kStaged, int G>
+hipError_t rows_prepare() {
+    const auto allow = [](const void* f, int bytes) { return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes); };
+    constexpr int M = kMostO<T, R, kStaged, G>, least = kStaged ? kStageBytes : 0;
+    hipError_t e = allow(reinterpret_cast<const void*>(kRowsKernel<T, R, 1, kStaged, G>), std::max(least, kPartLds<R, 1>));
+    if constexpr (M >= 2)
+        if (e == hipSuccess) e = allow(reinterpret_cast<const void*>(kRowsKernel<T, R, 2, kStaged, G>), std::max(least, kPartLds<R, 2>));
+    if constexpr (M >= 4)
+        if (e == hipSuccess) e = allow(reinterpret_cast<const void*>(kRowsKernel<T, R, 4, kStaged, G>), std::max(least, kPartLds<R, 4>));
+    return e;
 }
 
 template <typename T>
@@ -606,14 +672,17 @@ constexpr int kTileLds = 2 * (2 * kTileH<T> * 8 * Kind<T>::kTerms * 1024 + G * 6
 template <typename T, int G>
 hipError_t w4_as(const W4Args& a, hipStream_t s) {
     if constexpr (sizeof(T) == 4) {
-        if (a.rows <= 16 && stage_bytes(a) <= kStageBytes) {
-            k_w4_rows<T, 1, 4, true, G><<<dim3(a.w.out_tiles, 1), 64 * kWaves, stage_bytes(a), s>>>(a);
-            return hipGetLastError();
-        }
+        if (a.rows <= 16 && stage_bytes(a) <= kStageBytes) return rows_of<T, 1, true, G>(a, s);
     }
-    if (a.rows <= 16) return rows_as<T, 1, sizeof(T) == 2 ? 4 : 2, G>(a, s);
-    if (a.rows <= 32) return rows_as<T, 2, sizeof(T) == 2 ? 2 : 1, G>(a, s);
-    if (a.rows <= 64) return rows_as<T, 4, sizeof(T) == 2 ? 2 : 1, G>(a, s);
+    if (a.rows <= 16) return rows_of<T, 1, false, G>(a, s);
+    if (a.rows <= 32) return rows_of<T, 2, false, G>(a, s);
+    // While the workgroups of 64 rows are few, the other kernel would leave compute units idle (64 rows x 128 outputs each and more),
+    // and a chunk of it takes 2.1 us whatever they are: 4096 x 11008, bf16, 128 rows 83 us for 182 there, 256 rows 163 for 182, and
+    // from 1,024 workgroups on it is the faster one: 32,000 x 4096, 65 rows 71 us for 98 here. fp32, where a workgroup has one tile:
+    // 4096 x 11008, 128 rows 167 us for 218, and 15,360 x 5120, 64 rows 169 for 101.
+    constexpr int64_t most = sizeof(T) == 2 ? 1024 : 512;
+    const int o = rows_o<T, 4, false, G>(a);
+    if ((a.rows + 63) / 64 * ((a.w.out_tiles + o - 1) / o) <= most) return rows_of<T, 4, false, G>(a, s);
     constexpr int H = kTileH<T>;
     const int row_blocks = (int)((a.rows + 64 * H - 1) / (64 * H)), out_blocks = (a.w.n_out + kTileOuts - 1) / kTileOuts;
     const unsigned grid = (unsigned)((out_blocks + 7) / 8 * 8) * row_blocks;
@@ -627,12 +696,15 @@ hipError_t w4_any(const W4Args& a, hipStream_t s) {
 
 template <typename T, int G>
 hipError_t prepare() {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_w4_tile<T, kTileH<T>, G>), hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds<T, G>);
+    const auto allow = [](const void* f, int bytes) { return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes); };
     if constexpr (sizeof(T) == 4) {
-        if (e == hipSuccess)
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_w4_rows<T, 1, 4, true, G>), hipFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
+        const hipError_t e = rows_prepare<T, 1, true, G>();
+        if (e != hipSuccess) return e;
     }
-    return e;
+    for (hipError_t e : {allow(reinterpret_cast<const void*>(k_w4_tile<T, kTileH<T>, G>), kTileLds<T, G>), rows_prepare<T, 1, false, G>(),
+                         rows_prepare<T, 2, false, G>(), rows_prepare<T, 4, false, G>()})
+        if (e != hipSuccess) return e;
+    return hipSuccess;
 }
 template <typename T>
 hipError_t prepare_all() {

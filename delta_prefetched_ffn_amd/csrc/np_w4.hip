@@ -11,12 +11,10 @@ struct np_w4 {
     np_w4_desc desc{};
     W4View view{};
     uint8_t* tiles = nullptr;
-    uint8_t* scales = nullptr;
-    uint8_t* zeros = nullptr;
+    uint32_t* scales = nullptr;
     ~np_w4() {
         if (tiles) (void)hipFree(tiles);
         if (scales) (void)hipFree(scales);
-        if (zeros) (void)hipFree(zeros);
     }
 };
 
@@ -57,23 +55,21 @@ np_status create(const np_w4_desc* desc, np_w4** out) {
     v.out_tiles = (D.n_out + kW4Outs - 1) / kW4Outs;
     v.chunks = (D.n_in + kW4Ins - 1) / kW4Ins;
     v.per_chunk = D.group < kW4Ins ? kW4Ins / D.group : 1;
-    v.scale_dtype = D.scale_dtype;
-    const size_t all = (size_t)v.out_tiles * v.chunks, held = all * v.per_chunk * kW4Outs;
-    if (hipMalloc((void**)&w->tiles, all * kW4TileBytes) != hipSuccess || hipMalloc((void**)&w->scales, held * sb) != hipSuccess ||
-        (D.zeros && hipMalloc((void**)&w->zeros, held) != hipSuccess)) {
+    v.scale_words = D.scale_dtype == NP_F32 ? 2 : 1;
+    const size_t all = (size_t)v.out_tiles * v.chunks, code_bytes = all * kW4TileBytes;
+    const size_t scale_bytes = (all * v.per_chunk * kW4Outs * v.scale_words + 1) * sizeof(uint32_t);  // read two at a time
+    if (hipMalloc((void**)&w->tiles, code_bytes) != hipSuccess || hipMalloc((void**)&w->scales, scale_bytes) != hipSuccess) {
         (void)hipGetLastError();
-        return fail(NP_ENOMEM, "cannot allocate %zu bytes of weights", all * kW4TileBytes + held * (sb + (D.zeros ? 1 : 0)));
+        return fail(NP_ENOMEM, "cannot allocate %zu bytes of weights", code_bytes + scale_bytes);
     }
     v.tiles = w->tiles;
     v.scales = w->scales;
-    v.zeros = w->zeros;
     W4PackArgs a;
     a.codes = static_cast<const uint8_t*>(D.codes);
     a.scales = D.scales;
     a.zeros = D.zeros;
     a.tiles = w->tiles;
     a.scales_out = w->scales;
-    a.zeros_out = w->zeros;
     a.n_out = D.n_out;
     a.n_in = D.n_in;
     a.out_tiles = v.out_tiles;
@@ -81,7 +77,7 @@ np_status create(const np_w4_desc* desc, np_w4** out) {
     a.per_chunk = v.per_chunk;
     a.group = D.group;
     a.groups = (D.n_in + D.group - 1) / D.group;
-    a.scale_bytes = sb;
+    a.scale_dtype = D.scale_dtype;
     NP_HIP(w4_prepare());
     NP_HIP(hipDeviceSynchronize());  // whatever stream filled the sources
     NP_HIP(launch_w4_pack(a, nullptr));

@@ -15,12 +15,13 @@ constexpr int kW4TileBytes = kW4Outs * kW4Ins / 2;
 
 struct W4View {
     const uint8_t* tiles;   // [out tiles][chunks][1024]
-    const void* scales;     // [out tiles][chunks * per_chunk][16] of scale_dtype
-    const uint8_t* zeros;   // the same shape, or nullptr: 8
+    // [out tiles][chunks * per_chunk][16] groups of scale_words dwords: the scale as fp32, and the zero point in the low 4 bits of the last
+    // dword. A 16-bit scale leaves those bits of its fp32 value free, so one dword holds both; an fp32 scale takes two.
+    const uint32_t* scales;
     int32_t n_out, n_in;
     int32_t out_tiles, chunks;
     int32_t per_chunk;      // groups of a chunk: 1, 2 or 4
-    int32_t scale_dtype;
+    int32_t scale_words;
 };
 
 struct W4Args {
@@ -37,11 +38,10 @@ struct W4PackArgs {
     const void* scales;     // [n_out][groups]
     const uint8_t* zeros;   // the same shape, or nullptr
     uint8_t* tiles;
-    void* scales_out;
-    uint8_t* zeros_out;
+    uint32_t* scales_out;
     int32_t n_out, n_in, out_tiles, chunks, per_chunk;
     int32_t group, groups;  // inputs of a group, groups of a row, as given
-    int32_t scale_bytes;
+    int32_t scale_dtype;
 };
 
 hipError_t launch_w4_pack(const W4PackArgs& a, hipStream_t s);
