@@ -324,10 +324,15 @@ __global__ __launch_bounds__(64 * kWaves, R == 1 ? 4 : 2) void k_w4_rows(W4Args 
     }
 }
 
-// Many rows: one workgroup of four waves per (64 H rows, 128 outputs), two by two; a wave has 32 H rows x 64 outputs, in products
-// of 32x32x16. The workgroup's x of a chunk of 128 inputs is in LDS as operands (two chunks: one is read while the next one's
+// Many rows: one workgroup of four waves per (64 H rows, 128 outputs); a wave has all the rows x 32 outputs, in products of
+// 32x32x16. The workgroup's x of a chunk of 128 inputs is in LDS as operands (two chunks: one is read while the next one's
 // loads are on their way), with the sums of each row and group, three bf16 terms of them, that take the zero points out: one
-// more product per group, with -z as the other operand. Each wave widens the codes of its outputs itself.
+// more product per group, with -z as the other operand. Each wave widens the codes of its outputs itself, no two the same ones.
+//
+// Bound by the instructions around the matrix products: per chunk and wave 32 of them need 1,024 cycles, the loads, widening,
+// staging and folds beside them some 400 instructions. 1,500 rows x 5120 x 15,360: 329 us in bf16 (716 TFLOP/s), with groups of
+// 32 428 us, fp32 (six times the products) 1,315 us; with waves of half the rows x 64 outputs, which widen all codes twice, 345,
+// 481 and 1,239 us, fp32 with groups of 32 2,265 us (registers) for 1,330.
 //
 // Operand slots: step (s, e) of a chunk, lane half h: inputs 32 s + 8 (h + 2 e) + j, so that a lane's 16 bytes of quad h + 2 e of a
 // tile are its operands of four steps.
@@ -362,7 +367,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
     typedef Kind<T> Kd;
     typedef typename Kd::E E;
     typedef typename Vec8<E>::t E8;
-    constexpr int N = Kd::kTerms, kRows = 64 * H;
+    constexpr int N = Kd::kTerms, kRows = 64 * H, RT = 2 * H, TT = 1;
     const W4View& w = a.w;
     // Workgroups go to the 8 dies in turn: a die takes its own outputs, with all rows one after the other.
     const int die = blockIdx.x & 7, nth = blockIdx.x >> 3;
@@ -371,7 +376,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
     const int64_t r0 = (int64_t)rb * kRows;
     const int rows = (int)min((int64_t)kRows, a.rows - r0);
-    const int row0 = (wave & 1) * 32 * H, tile0 = ob * 8 + (wave >> 1) * 4;
+    const int tile0 = ob * 8 + wave * 2;
     extern __shared__ __attribute__((aligned(128))) uint8_t s_dyn[];
     E8* const s_x = reinterpret_cast<E8*>(s_dyn);  // [2][2 H row tiles][8 steps][N][2 halves][32 rows, changed places]
     constexpr int kBuf = 2 * H * 8 * N * 64;
@@ -420,36 +425,36 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
         }
     };
     // Codes of outputs 32 t + col: quads h and h + 2 of the tile.
-    const uint8_t* tiles[2];
-    int64_t groups[2];
+    const uint8_t* tiles[TT];
+    int64_t groups[TT];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < TT; ++t) {
         const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);  // past the last: not stored
         tiles[t] = w.tiles + tile * w.chunks * kW4TileBytes + (h * 16 + (col & 15)) * 16;
         groups[t] = tile * w.chunks * G * kW4Outs + (col & 15);
     }
-    u32x4 code[2][2], next[2][2];
-    u32x2 scale[2][G];
-    const auto ask_codes = [&](u32x4 (&o)[2][2], int c) __attribute__((always_inline)) {
+    u32x4 code[TT][2], next[TT][2];
+    u32x2 scale[TT][G];
+    const auto ask_codes = [&](u32x4 (&o)[TT][2], int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) o[t][e] = *reinterpret_cast<const u32x4*>(tiles[t] + (int64_t)c * kW4TileBytes + e * 512);
     };
     const auto ask_scales = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const int64_t at = groups[t] + (c * G + g) * kW4Outs;
                 scale[t][g] = load_scale(w, at);
             }
     };
-    f32x16 tot[H][2];
+    f32x16 tot[RT][TT];
 #pragma unroll
-    for (int r = 0; r < H; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) tot[r][t][j] = 0.0f;
 
@@ -463,42 +468,42 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             ask_x(c + 1);
             ask_codes(next, c + 1);
         }
-        const E8* const from = s_x + (c & 1) * kBuf + (row0 >> 5) * 8 * N * 64 + h * 32;
-        const bf16x8* const sums = s_sum + (c & 1) * G * kRows + row0 + col;
+        const E8* const from = s_x + (c & 1) * kBuf + h * 32;
+        const bf16x8* const sums = s_sum + (c & 1) * G * kRows + col;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            f32x16 part[H][2];
+            f32x16 part[RT][TT];
 #pragma unroll
-            for (int r = 0; r < H; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[r][t][j] = 0.0f;
 #pragma unroll
             for (int step = g * 8 / G; step < (g + 1) * 8 / G; ++step) {
                 const int s = step >> 1, e = step & 1;
-                E8 cw[2];
+                E8 cw[TT];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) cw[t] = codes_of<E>(code[t][e][s]);
+                for (int t = 0; t < TT; ++t) cw[t] = codes_of<E>(code[t][e][s]);
 #pragma unroll
-                for (int r = 0; r < H; ++r)
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
                         const E8 x = from[((r * 8 + step) * N + n) * 64 + (col ^ (4 * (h + 2 * e)))];
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) part[r][t] = mfma(x, cw[t], part[r][t]);
+                        for (int t = 0; t < TT; ++t) part[r][t] = mfma(x, cw[t], part[r][t]);
                     }
             }
-            bf16x8 xs8[H];
+            bf16x8 xs8[RT];
 #pragma unroll
-            for (int r = 0; r < H; ++r) xs8[r] = sums[g * kRows + 32 * r];
+            for (int r = 0; r < RT; ++r) xs8[r] = sums[g * kRows + 32 * r];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < TT; ++t) {
                 const float sc = scale_value(scale[t][g], w.scale_words), z = (float)zero_value(scale[t][g], w.scale_words);
                 const uint32_t zb = h ? 0u : __float_as_uint(-z);  // whole numbers up to 15: the upper half is bf16
                 const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{zb >> 16 | zb, zb >> 16, 0, 0});
 #pragma unroll
-                for (int r = 0; r < H; ++r) {
+                for (int r = 0; r < RT; ++r) {
                     part[r][t] = mfma(xs8[r], minus, part[r][t]);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
@@ -511,25 +516,25 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
         if (c + 1 < w.chunks) {
             put_x(c + 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) code[t][e] = next[t][e];
         }
     }
     bool odd = false;
 #pragma unroll
-    for (int r = 0; r < H; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) odd |= not_finite(tot[r][t][j]);
     if (__any(odd)) {
         // The wave's products again, one at a time, x from memory.
 #pragma unroll 1
-        for (int r = 0; r < H; ++r) {
+        for (int r = 0; r < RT; ++r) {
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(row0 + 32 * r + col, rows - 1)) * a.x_row;
+            for (int t = 0; t < TT; ++t) {
+                const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(32 * r + col, rows - 1)) * a.x_row;
                 const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);
                 f32x16 again;
 #pragma unroll
@@ -560,9 +565,9 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
                     }
                 }
 #pragma unroll
-                for (int rr = 0; rr < H; ++rr)
+                for (int rr = 0; rr < RT; ++rr)
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt)
+                    for (int tt = 0; tt < TT; ++tt)
                         if (rr == r && tt == t)
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
@@ -571,12 +576,12 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
         }
     }
 #pragma unroll
-    for (int r = 0; r < H; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const int row = row0 + 32 * r + 8 * (j >> 2) + 4 * h + (j & 3), tile = tile0 + 2 * t + (col >> 4), out = tile * kW4Outs + (col & 15);
+                const int row = 32 * r + 8 * (j >> 2) + 4 * h + (j & 3), tile = tile0 + 2 * t + (col >> 4), out = tile * kW4Outs + (col & 15);
                 if (row < rows && out < w.n_out) put(a, r0 + row, out, tot[r][t][j]);
             }
 }
@@ -678,7 +683,7 @@ hipError_t w4_as(const W4Args& a, hipStream_t s) {
     if (a.rows <= 32) return rows_of<T, 2, false, G>(a, s);
     // While the workgroups of 64 rows are few, the other kernel would leave compute units idle (64 rows x 128 outputs each and more),
     // and a chunk of it takes 2.1 us whatever they are: 4096 x 11008, bf16, 128 rows 83 us for 182 there, 256 rows 163 for 182, and
-    // from 1,024 workgroups on it is the faster one: 32,000 x 4096, 65 rows 71 us for 98 here. fp32, where a workgroup has one tile:
+    // from 1,024 workgroups on it is the faster one: 32,000 x 4096 takes 71 us there with 65 rows and 74 here with 64. fp32, where a workgroup has one tile:
     // 4096 x 11008, 128 rows 167 us for 218, and 15,360 x 5120, 64 rows 169 for 101.
     constexpr int64_t most = sizeof(T) == 2 ? 1024 : 512;
     const int o = rows_o<T, 4, false, G>(a);
