@@ -6,8 +6,6 @@
 // for pair i = (a, b) of the first `rot` values, t = 2 pi p F_i. F_i, a fraction of a turn, is held in 64 bits, so p F_i
 // mod 1 is the low half of an integer product: exact for every position, where a float product p F_i loses the angle of far
 // ones. What is left is a quarter of a turn at most, whose sine and cosine come from their power series in fp32.
-#include <atomic>
-
 #include "kv_quant.hpp"
 #include "rope_internal.hpp"
 
@@ -82,12 +80,12 @@ struct Turner {
         }
     }
     template <typename T>
-    __device__ void load(float* x, const T* head) const {
+    __device__ void load(float* x, const T* head, bool real) const {
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (has[k]) load_row<8>(x + 8 * k, head + d[k]);
+            if (real && has[k]) load_row<8>(x + 8 * k, head + d[k]);
     }
     // x = x * weight / sqrt(mean(x^2) + eps). Every lane of the wave takes part in the sum; w nullptr: x stays.
     __device__ void norm(const RopeView& r, float* x, const float* w) const {
@@ -158,7 +156,7 @@ struct Turner {
     }
 };
 
-constexpr int kWg = 256;
+constexpr int kWg = 256, kAppendWg = 512;
 
 // Heads [g0, g1) * (64 / lanes) of one row, queries first, by one wave.
 template <typename T, int MODE>
@@ -175,9 +173,7 @@ __device__ inline void turn_heads(const RopeView& r, const RopeTensor* x, int n_
         const RopeTensor& y = x[second ? 1 : 0];
         if (second) h -= x[0].heads;
         float v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-        if (real) t.load(v, static_cast<const T*>(y.in) + row * y.in_row + h * y.in_head);
+        t.load(v, static_cast<const T*>(y.in) + row * y.in_row + h * y.in_head, real);
         if (norms) t.norm(r, v, real ? y.weight : nullptr);
         t.turn(r, v, lds + slot * lanes * 16, p);
         if (real) t.store(v, static_cast<T*>(y.out) + row * y.out_row + h * y.out_head);
@@ -212,65 +208,104 @@ __device__ inline int find_row(const RopeBatch& b, int row) {
     return __builtin_amdgcn_readfirstlane(c);
 }
 
-// A step's queries, keys and values in one launch: workgroups [0, 2 * pages * kv heads) take one block of the cache each
-// (K or V of a page and head, as k_kv_append does), the others the queries. K's rows are normalised and turned into LDS
-// first, a head per group of lanes as above, and quantised from there in the cache's tile order.
+// K of one page, heads [h0, h1), one block of the cache after the other: a thread holds 16 values of each of CPT new tokens
+// from their load to their codes, and a token's angles for all the heads: 4,097 tokens x 32 heads of 128 in bf16 with their queries
+// and values 55 us with 8 heads a workgroup (3.0 TB/s), 59 with 4, 63 with 2, 68 with 1; 81 when K went through LDS as fp32, which
+// took the room of other workgroups. Eight waves a SIMD, for which the angles spill a few registers, beat six (58 us), and loading
+// the next head during this one, at five, is worse still (66).
 template <typename T, int CPT, int MODE>
-__global__ __launch_bounds__(kWg) void k_rope_append(RopeAppendArgs a) {
-    extern __shared__ __attribute__((aligned(128))) float s_mem[];
+__device__ inline void append_k(const RopeAppendArgs& a, int page, int h0, int h1, int t0, int lo, int hi, const T* x, float* lds) {
     const KvView& kv = a.kv;
-    const int blocks = a.b.item0[a.b.n] * kv.n_kv * 2;
-    const int lanes = rope_lanes(kv.hd);
-    const int wave = threadIdx.x >> 6;
-    if ((int)blockIdx.x >= blocks) {
-        const int at_once = 64 / lanes, groups = (a.q.heads + at_once - 1) / at_once, shares = (groups + a.per - 1) / a.per;
-        const int64_t item = (int64_t)((int)blockIdx.x - blocks) * (blockDim.x >> 6) + wave;
-        const int64_t row = item / shares;
+    const int pt = 1 << kv.page_shift, nt = blockDim.x, wave = threadIdx.x >> 6, own = threadIdx.x & 63;
+    const int lanes = append_lanes(kv.hd, kv.slabs), at_once = 64 / lanes, slot = own / lanes;
+    Turner<MODE> t[CPT];
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) {
+        t[u].place(a.rope, own - slot * lanes, lanes);
+        t[u].at(a.rope, t0 + lo + (u * (nt >> 6) + wave) * at_once + slot);
+    }
+    for (int h = h0; h < h1; ++h) {
+        int8_t* const ep = kv.exps + (((int64_t)a.layer * kv.n_pages + page) * kv.n_kv + h) * 2;
+        uint8_t* const block = kv.codes + a.layer * kv.layer_bytes + page * kv.page_bytes + (int64_t)(h * 2) * (pt * kv.slabs * kTileDims);
+        const int e0 = lo > 0 ? *ep : -128;
+        float v[CPT][16];
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            const int tok = lo + (u * (nt >> 6) + wave) * at_once + slot;
+            t[u].load(v[u], x + h * a.head_stride[0] + tok * a.row_stride[0], tok < hi);
+        }
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            if (a.k_weight) t[u].norm(a.rope, v[u], a.k_weight);
+            t[u].turn(a.rope, v[u], lds + (wave * 64 + slot * lanes) * 16, t0 + lo + (u * (nt >> 6) + wave) * at_once + slot);
+        }
+        if (h > h0) __syncthreads();  // the last head's maximum has been read
+        const int e = scale_block(v, e0, nt);
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            const int tok = lo + (u * (nt >> 6) + wave) * at_once + slot;
+            if (tok >= hi) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = t[u].d[k];
+                if (d >= kv.slabs * kTileDims) continue;
+                const float* const y = v[u] + 8 * k;
+                // Chunk of 16 values: 64 of them to a tile, tiles ordered (16 tokens, 64 values).
+                const int at = (((tok >> 4) * kv.slabs + (d >> 6)) * 64 + ((d >> 4) & 3) * 16 + (tok & 15)) * 16 + (d & 8);
+                *reinterpret_cast<u32x2*>(block + at) = u32x2{to_e4m3(y[0], y[1], y[2], y[3]), to_e4m3(y[4], y[5], y[6], y[7])};
+            }
+        }
+        if (lo > 0 && e > e0) {  // the tokens before keep their values
+            const float down = pow2i(max(-126, e0 - e));
+            for (int c = threadIdx.x; c < pt * kv.slabs * 4; c += nt) {
+                if ((c >> 6) / kv.slabs * 16 + (c & 15) >= lo) continue;
+                u32x4 w = reinterpret_cast<const u32x4*>(block)[c];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = rescale_e4m3(w[k], down);
+                reinterpret_cast<u32x4*>(block)[c] = w;
+            }
+        }
+        if (threadIdx.x == 0 && e != e0) *ep = (int8_t)e;
+    }
+}
+
+// A step's queries, keys and values in one launch: first the workgroups for K (a touched page and a.heads of its heads each), then
+// V's (a block of the cache each, as k_kv_append takes them), then the queries'.
+template <typename T, int CPT, int MODE>
+__global__ __launch_bounds__(kAppendWg, CPT == 1 ? 8 : CPT == 2 ? 4 : 2) void k_rope_append(RopeAppendArgs a) {
+    extern __shared__ __attribute__((aligned(128))) float s_mem[];  // kFarPairs: 16 a lane
+    const KvView& kv = a.kv;
+    const int items = a.b.item0[a.b.n], shares = (kv.n_kv + a.heads - 1) / a.heads;
+    int at = blockIdx.x;
+    if (at >= items * (shares + kv.n_kv)) {
+        at -= items * (shares + kv.n_kv);
+        const int wave = threadIdx.x >> 6, lanes = rope_lanes(kv.hd);
+        const int at_once = 64 / lanes, groups = (a.q.heads + at_once - 1) / at_once, q_shares = (groups + a.per - 1) / a.per;
+        const int64_t item = (int64_t)at * (blockDim.x >> 6) + wave;
+        const int64_t row = item / q_shares;
         if (row >= a.rows) return;
-        const int g0 = (int)(item - row * shares) * a.per, g1 = min(g0 + a.per, groups);
+        const int g0 = (int)(item - row * q_shares) * a.per, g1 = min(g0 + a.per, groups);
         const int b = find_row(a.b, (int)row);
         turn_heads<T, MODE>(a.rope, &a.q, 1, lanes, row, a.b.before[b] + ((int)row - a.b.row0[b]), g0, g1, s_mem + wave * 64 * 16);
         return;
     }
-    const int side = blockIdx.x & 1, block = blockIdx.x >> 1;
-    const int item = block / kv.n_kv, h = block - item * kv.n_kv;
+    const int side = at >= items * shares ? 1 : 0;
+    if (side) at -= items * shares;
+    const int of = side ? kv.n_kv : shares, item = at / of, share = at - item * of;
     const int b = find_item(a.b, item);
-    const int pt = 1 << kv.page_shift;
     const int before = a.b.before[b], fresh = a.b.fresh[b];
     const int index = (before >> kv.page_shift) + (item - a.b.item0[b]);
     const int t0 = index << kv.page_shift;
-    const int lo = max(0, before - t0), hi = min(pt, before + fresh - t0);  // new tokens of the page
+    const int lo = max(0, before - t0), hi = min(1 << kv.page_shift, before + fresh - t0);  // new tokens of the page
     const int page = page_of(kv, a.b.seq[b], index);
     if (page < 0) return;
-    const int64_t rs = a.row_stride[side];
-    const T* const x = static_cast<const T*>(a.kx[side]) + (int64_t)h * a.head_stride[side] + (int64_t)(a.b.row0[b] + t0 - before) * rs;
-    const int stride = kv.slabs * kTileDims + 4;  // floats of a token in LDS
+    const T* const x = static_cast<const T*>(a.kx[side]) + (int64_t)(a.b.row0[b] + t0 - before) * a.row_stride[side];
     if (side == 0) {
-        const int own = threadIdx.x & 63, at_once = 64 / lanes, slot = own / lanes;
-        Turner<MODE> t;
-        t.place(a.rope, own - slot * lanes, lanes);
-        float* const far = s_mem + (MODE == kFarPairs ? pt * stride + (wave * 64 + slot * lanes) * 16 : 0);
-        // The waves' turns, the same number for all lanes of a wave (the norm's sum needs them).
-        for (int u = lo + wave * at_once; u < hi; u += (int)(blockDim.x >> 6) * at_once) {
-            const int tok = u + slot;
-            const bool real = tok < hi;
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-            if (real) t.load(v, x + tok * rs);
-            t.at(a.rope, t0 + tok);
-            if (a.k_weight) t.norm(a.rope, v, real ? a.k_weight : nullptr);
-            t.turn(a.rope, v, far, t0 + tok);
-            if (real) t.store(v, s_mem + tok * stride);
-        }
-        __syncthreads();
+        append_k<T, CPT, MODE>(a, page, share * a.heads, min(kv.n_kv, (share + 1) * a.heads), t0, lo, hi, x, s_mem);
+        return;
     }
-    const auto load_k = [&](float* v, int t, int d) {
-        load_row<8>(v, s_mem + t * stride + d);
-        if (d + 8 < kv.hd) load_row<8>(v + 8, s_mem + t * stride + d + 8);
-    };
-    const auto load_v = [&](float* v, int t, int d) { load_row<4>(v, x + t * rs + d); };
-    quantise_block<CPT>(kv, a.layer, page, h, side, lo, hi, load_k, load_v);
+    const auto load_v = [&](float* v, int t, int d) { load_row<4>(v, x + share * a.head_stride[1] + t * a.row_stride[1] + d); };
+    quantise_block<CPT>(kv, a.layer, page, share, 1, lo, hi, load_v, load_v);
 }
 
 int mode_of(const RopeView& r) { return r.layout == 1 ? kPairs : r.rot % 16 == 0 ? kAligned : kFarPairs; }
@@ -288,50 +323,27 @@ hipError_t rope_any(const RopeArgs& a, hipStream_t s) {
     return m == kAligned ? rope_as<T, kAligned>(a, s) : m == kPairs ? rope_as<T, kPairs>(a, s) : rope_as<T, kFarPairs>(a, s);
 }
 
-// LDS of k_rope_append: a page of K in fp32, and for kFarPairs (also the queries') 16 floats a lane.
-size_t append_lds(int pt, int slabs, int mode) {
-    return (size_t)pt * (slabs * kTileDims + 4) * sizeof(float) + (mode == kFarPairs ? kWg * 16 * sizeof(float) : 0);
-}
-
+// A workgroup of k_rope_append holds a block: a thread 16 values of up to four tokens.
 template <typename T, int CPT, int MODE>
 hipError_t append_as(const RopeAppendArgs& a, int nt, hipStream_t s) {
     const int groups = rope_groups(a.kv.hd, a.q.heads), waves = nt / 64;
-    const int64_t items = (int64_t)a.rows * ((groups + a.per - 1) / a.per);
-    const int64_t grid = (int64_t)a.b.item0[a.b.n] * a.kv.n_kv * 2 + (items + waves - 1) / waves;
-    k_rope_append<T, CPT, MODE><<<(unsigned)grid, nt, append_lds(1 << a.kv.page_shift, a.kv.slabs, MODE), s>>>(a);
+    const int64_t rows = (int64_t)a.rows * ((groups + a.per - 1) / a.per);
+    const int64_t grid = (int64_t)a.b.item0[a.b.n] * (a.kv.n_kv + (a.kv.n_kv + a.heads - 1) / a.heads) + (rows + waves - 1) / waves;
+    k_rope_append<T, CPT, MODE><<<(unsigned)grid, nt, MODE == kFarPairs ? nt * 16 * sizeof(float) : 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, int MODE>
 hipError_t append_mode(const RopeAppendArgs& a, hipStream_t s) {
-    const int chunks = (1 << a.kv.page_shift) * a.kv.slabs * 4;  // 64 .. 2048, a multiple of 64
-    const int nt = chunks < kWg ? chunks : kWg;
-    const int per = (chunks + nt - 1) / nt;
-    if (per <= 1) return append_as<T, 1, MODE>(a, nt, s);
-    if (per <= 2) return append_as<T, 2, MODE>(a, nt, s);
-    if (per <= 4) return append_as<T, 4, MODE>(a, nt, s);
-    return append_as<T, 8, MODE>(a, nt, s);
+    const int threads = (1 << a.kv.page_shift) * append_lanes(a.kv.hd, a.kv.slabs);  // 64 .. 2048, a multiple of 64
+    const int nt = threads < kAppendWg ? threads : kAppendWg;
+    if (threads <= nt) return append_as<T, 1, MODE>(a, nt, s);
+    if (threads <= 2 * nt) return append_as<T, 2, MODE>(a, nt, s);
+    return append_as<T, 4, MODE>(a, nt, s);
 }
 template <typename T>
 hipError_t append_any(const RopeAppendArgs& a, hipStream_t s) {
     const int m = mode_of(a.rope);
     return m == kAligned ? append_mode<T, kAligned>(a, s) : m == kPairs ? append_mode<T, kPairs>(a, s) : append_mode<T, kFarPairs>(a, s);
-}
-
-template <typename T, int MODE>
-hipError_t prepare_mode() {
-    const int most = (int)append_lds(kMaxPageTokens, kMaxHeadDim / kTileDims, MODE);
-    for (const void* f : {reinterpret_cast<const void*>(k_rope_append<T, 1, MODE>), reinterpret_cast<const void*>(k_rope_append<T, 2, MODE>),
-                          reinterpret_cast<const void*>(k_rope_append<T, 4, MODE>), reinterpret_cast<const void*>(k_rope_append<T, 8, MODE>)}) {
-        const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-}
-template <typename T>
-hipError_t prepare_all() {
-    for (hipError_t e : {prepare_mode<T, kAligned>(), prepare_mode<T, kPairs>(), prepare_mode<T, kFarPairs>()})
-        if (e != hipSuccess) return e;
-    return hipSuccess;
 }
 
 }  // namespace
@@ -346,17 +358,6 @@ hipError_t launch_rope_append(const RopeAppendArgs& a, int dtype, hipStream_t s)
     if (dtype == kF32) return append_any<float>(a, s);
     if (dtype == kBF16) return append_any<__bf16>(a, s);
     return append_any<_Float16>(a, s);
-}
-
-hipError_t rope_prepare() {
-    static std::atomic<uint64_t> done{0};  // a bit per device
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
-    for (hipError_t x : {prepare_all<float>(), prepare_all<__bf16>(), prepare_all<_Float16>()})
-        if (x != hipSuccess) e = x;
-    if (e == hipSuccess && dev < 64) done.fetch_or(1ull << dev);
-    return e;
 }
 
 }  // namespace np

@@ -12,15 +12,48 @@ __device__ inline int exp_for(float a) {
     return max(-120, min(120, e));
 }
 
-// The maximum over the workgroup (at most 256 threads); `use` numbers the calls of one kernel.
+// The maximum over the workgroup (at most 512 threads); `use` numbers the calls of one kernel.
 __device__ inline float block_max(float x, int threads, int use) {
-    __shared__ float s[2][4];
+    __shared__ float s[2][8];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
     if ((threadIdx.x & 63) == 0) s[use][threadIdx.x >> 6] = x;
     __syncthreads();
     for (int w = 0; w < threads >> 6; ++w) x = fmaxf(x, s[use][w]);
     return x;
+}
+
+// The block's exponent, from its new values v and the one it has (e0; -128: none), by which it then scales v.
+template <int CPT>
+__device__ inline int scale_block(float (&v)[CPT][16], int e0, int nt) {
+    float top = 0.0f;
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]));  // ignores NaN
+    top = block_max(top, nt, 0);
+    const bool infinite = top == __builtin_inff();
+    if (infinite) {  // infinities do not set the scale, and saturate
+        top = 0.0f;
+#pragma unroll
+        for (int u = 0; u < CPT; ++u)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]) < __builtin_inff() ? fabsf(v[u][k]) : 0.0f);
+        top = block_max(top, nt, 1);
+    }
+    const int e = max(exp_for(top), e0);
+    const float unit = pow2i(-e);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[u][k] *= unit;
+    if (infinite) {
+#pragma unroll
+        for (int u = 0; u < CPT; ++u)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[u][k] = sat448(v[u][k]);
+    }
+    return e;
 }
 
 // Stores the new tokens [lo, hi) of block (layer, page, head h, side: 0 K, 1 V). A thread holds CPT chunks of 16
@@ -39,7 +72,6 @@ __device__ inline void quantise_block(const KvView& kv, int layer, int page, int
 
     float v[CPT][16];
     u32x4 old[CPT];
-    float top = 0.0f;
 #pragma unroll
     for (int u = 0; u < CPT; ++u) {
         const int c = threadIdx.x + u * nt;
@@ -60,32 +92,10 @@ __device__ inline void quantise_block(const KvView& kv, int layer, int page, int
                     if (t + k >= lo && t + k < hi) load_v(v[u] + 4 * k, t + k, d);
             }
         }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]));  // ignores NaN
     }
-    top = block_max(top, nt, 0);
-    const bool infinite = top == __builtin_inff();
-    if (infinite) {  // infinities do not set the scale, and saturate
-        top = 0.0f;
-#pragma unroll
-        for (int u = 0; u < CPT; ++u)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k]) < __builtin_inff() ? fabsf(v[u][k]) : 0.0f);
-        top = block_max(top, nt, 1);
-    }
-    const int e = max(exp_for(top), e0);
+    const int e = scale_block(v, e0, nt);
     const bool grown = lo > 0 && e > e0;
-    const float down = pow2i(max(-126, e0 - e)), unit = pow2i(-e);
-#pragma unroll
-    for (int u = 0; u < CPT; ++u)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[u][k] *= unit;
-    if (infinite) {
-#pragma unroll
-        for (int u = 0; u < CPT; ++u)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[u][k] = sat448(v[u][k]);
-    }
+    const float down = pow2i(max(-126, e0 - e));
 
 #pragma unroll
     for (int u = 0; u < CPT; ++u) {

@@ -86,7 +86,6 @@ np_status create(const np_rope_desc* desc, np_rope** out) {
     if (D.device < 0 || D.device >= ndev) return fail(NP_EINVAL, "device %d out of range [0, %d)", D.device, ndev);
     DeviceGuard g(D.device);
     if (!g.ok) return fail(NP_EHIP, "hipSetDevice(%d) failed", D.device);
-    NP_HIP(rope_prepare());
     hold.r->desc = D;
     hold.r->desc.freqs = nullptr;  // read, not kept
     if (hipMalloc((void**)&hold.r->turns, bits.size() * sizeof(uint64_t)) != hipSuccess) {
@@ -150,6 +149,9 @@ RopeTensor tensor(const void* in, void* out, const float* weight, const int64_t*
     return t;
 }
 
+// From twice as many new tokens x key heads on, a workgroup takes several heads of its page and works their angles out once; as many
+// as leave 256 workgroups of 64 tokens.
+constexpr int64_t kFullKeys = 256 * 64;
 // Groups of heads that a wave takes one after the other: all of a row's where rows alone fill the device.
 int32_t groups_per_wave(int64_t rows, int groups) {
     const int64_t shares = std::min<int64_t>(groups, (kFullWaves + rows - 1) / rows);
@@ -232,6 +234,7 @@ np_status append(const np_rope* r, np_kv* kv, int32_t layer, const void* q, void
     });
     const int groups = rope_groups(D.head_dim, D.n_heads);
     a.per = groups_per_wave(rows, groups);
+    a.heads = (int32_t)std::clamp<int64_t>(rows * D.n_kv_heads / kFullKeys, 1, D.n_kv_heads);
     // Workgroups have one wave at least.
     if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads * 2 + rows * ((groups + a.per - 1) / a.per) >= kMaxGroups)
         return fail(NP_EINVAL, "%d pages of %d heads and %lld rows in one call are too many", a.b.item0[a.b.n], D.n_kv_heads, (long long)rows);

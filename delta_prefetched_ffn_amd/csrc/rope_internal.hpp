@@ -50,17 +50,19 @@ struct RopeAppendArgs {
     int32_t layer;
     int32_t rows;
     int32_t per;        // as above, for q
+    int32_t heads;      // of K that a workgroup takes
     RopeBatch b;
 };
 static_assert(sizeof(RopeAppendArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
 // Lanes that hold one head: 16 values each, a power of two.
 constexpr int rope_lanes(int hd) { return hd <= 16 ? 1 : hd <= 32 ? 2 : hd <= 64 ? 4 : hd <= 128 ? 8 : 16; }
+// The same on the way into the cache, whose blocks hold whole slabs of 64 values.
+constexpr int append_lanes(int hd, int slabs) { return rope_lanes(hd) > slabs * 4 ? rope_lanes(hd) : slabs * 4; }
 // Groups of heads in a row (one wave's worth each).
 constexpr int rope_groups(int hd, int heads) { return (heads + 64 / rope_lanes(hd) - 1) / (64 / rope_lanes(hd)); }
 
 hipError_t launch_rope(const RopeArgs& a, int dtype, hipStream_t s);
 hipError_t launch_rope_append(const RopeAppendArgs& a, int dtype, hipStream_t s);
-hipError_t rope_prepare();  // lets the current device's kernels use the LDS they ask for
 
 }  // namespace np
