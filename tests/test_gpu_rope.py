@@ -265,6 +265,42 @@ def test_append_is_rope_then_append(dtype, heads, kv, hd, page, rot, layout, nor
             np.testing.assert_array_equal(c.kv.read_tokens(0, s)[1], plain.kv.read_tokens(0, s)[1], err_msg="V")
 
 
+@pytest.mark.parametrize("kv,hd,page,rot,layout,dtype", [
+    (17, 64, 128, 64, "half", "bf16"), (17, 40, 64, 40, "interleaved", "f16"), (17, 24, 32, 20, "half", "f32"), (17, 64, 16, 0, "half", "f32"), (5, 256, 128, 128, "half", "f16")])
+def test_long_prompts_take_several_heads_at_once(kv, hd, page, rot, layout, dtype):
+    # Two prompts that go on where small tokens lie in their pages already; infinities and NaN (rot 0) stay in their own block.
+    from delta_prefetched_ffn_amd import Rope
+    rng = np.random.default_rng(kv + hd + page)
+    rope = Rope(head_dim=hd, rot_dim=rot, layout=layout)
+    new = [50000 // kv, 7]
+    pages = 2 * (new[0] // page + 4)
+    c, plain = (Cache(heads=kv, kv=kv, hd=hd, page=page, pages=pages) for _ in range(2))
+    w = weights(rng, hd) if rot else np.ones(hd, np.float32)
+    dw = torch.from_numpy(w).cuda()
+    for seqs, n, scale in (([1, 0], [9, page - 3], 1e-3), ([1, 0], new, 1.0)):
+        before = [c.kv.tokens(s) for s in seqs]
+        k, v = rand(rng, (sum(n), kv, hd), dtype, scale), rand(rng, (sum(n), kv, hd), dtype)
+        if not rot:
+            k[3, 1, 5], k[4, 2, 6], k[sum(n) - 1, 0, 7] = float("inf"), float("nan"), -float("inf")
+        dk, dv, out = k.cuda(), v.cuda(), torch.empty_like(k, device="cuda")
+        for x in (c, plain):
+            x.kv.extend(seqs, n, stream())
+        rope.append(c.kv, 0, dk.data_ptr(), out.data_ptr(), dk.data_ptr(), dv.data_ptr(), dtype, k_weight_ptr=dw.data_ptr() if rot else 0, eps=1e-5, stream=stream())
+        plain.kv.append(0, dk.data_ptr(), dv.data_ptr(), dtype, stream=stream())
+        torch.cuda.synchronize()
+        if rot == 0:
+            assert torch.equal(c.codes, plain.codes) and torch.equal(c.exps, plain.exps)
+            continue
+        pos = np.concatenate([np.arange(b, b + m) for b, m in zip(before, n)])
+        want, mag = R.turned(k.double().numpy(), pos, R.freqs(rot), layout, 1.0, w.astype(np.float64), float(np.float32(1e-5)))
+        row = 0
+        for s, m, b in zip(seqs, n, before):
+            if scale == 1.0 or b == 0:
+                check_block(c, c.kv, s, want[row:row + m], mag[row:row + m], b)
+            row += m
+            np.testing.assert_array_equal(c.kv.read_tokens(0, s)[1], plain.kv.read_tokens(0, s)[1], err_msg="V")
+
+
 def test_append_special_values_and_other_layers():
     from delta_prefetched_ffn_amd import Rope
     rng = np.random.default_rng(9)
