@@ -12,6 +12,8 @@
 namespace np {
 namespace {
 
+// 2 pi / 2^32, and what fp32 leaves out of it.
+constexpr float kTurn = 1.46291807926715968e-9f, kTurnRest = (float)(1.46291807926715968105e-9 - (double)kTurn);
 // cos and sin of the angle of pair i at position p, times the amplitude.
 __device__ inline f32x2 turn_of(uint64_t f, int p) {
     const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), u = (uint32_t)p;
@@ -19,17 +21,21 @@ __device__ inline f32x2 turn_of(uint64_t f, int p) {
     const uint32_t t = __umulhi(lo, u) + hi * u - (p < 0 ? lo : 0u);
     // t = q quarters + r, r in [-1/8, 1/8) turns
     const uint32_t q = (t + 0x20000000u) >> 30;
-    const float x = (float)(int32_t)(t - (q << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32: |x| <= pi / 4
-    const float z = x * x;
-    // Taylor series: what is left out is below 2^-29 of the sine and 2^-25 of the cosine.
+    // x + e = r 2 pi / 2^32, |x| <= pi / 4: the upper bits of r are exact in fp32, and so is what the product with them leaves out.
+    const int32_t r = (int32_t)(t - (q << 30)), r0 = r & ~255;
+    const float u0 = (float)r0, x = u0 * kTurn;
+    const float e = __builtin_fmaf((float)(r - r0), kTurn, __builtin_fmaf(u0, kTurnRest, __builtin_fmaf(u0, kTurn, -x)));
+    const float z = __builtin_fmaf(x, x, 2.0f * x * e);
+    // Taylor series: what is left out is below 2^-29 of the sine and of the cosine, whose 1 - z / 2 keeps what its rounding leaves out.
     float s = __builtin_fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
     s = __builtin_fmaf(z, s, 8.33333333e-3f);
     s = __builtin_fmaf(z, s, -1.66666667e-1f);
-    s = __builtin_fmaf(z * x, s, x);
-    float c = __builtin_fmaf(z, 2.48015873e-5f, -1.38888889e-3f);
+    s = x + __builtin_fmaf(z * x, s, e);
+    float c = __builtin_fmaf(z, -2.75573192e-7f, 2.48015873e-5f);
+    c = __builtin_fmaf(z, c, -1.38888889e-3f);
     c = __builtin_fmaf(z, c, 4.16666667e-2f);
-    c = __builtin_fmaf(z, c, -0.5f);
-    c = __builtin_fmaf(z, c, 1.0f);
+    const float h = __builtin_fmaf(z, -0.5f, 1.0f);
+    c = h + __builtin_fmaf(z * z, c, __builtin_fmaf(z, -0.5f, 1.0f - h));
     // a quarter turn on: (c, s) -> (-s, c)
     const float a = q & 1 ? s : c, b = q & 1 ? c : s;
     return f32x2{(q + 1) & 2 ? -a : a, q & 2 ? -b : b};
