@@ -214,13 +214,13 @@ __device__ inline int find_row(const RopeBatch& b, int row) {
     return __builtin_amdgcn_readfirstlane(c);
 }
 
-// K of one page, heads [h0, h1), one block of the cache after the other: a thread holds 16 values of each of CPT new tokens
+// K of one page, every `step`th head from h0 on, one block of the cache after the other: a thread holds 16 values of each of CPT new tokens
 // from their load to their codes, and a token's angles for all the heads: 4,097 tokens x 32 heads of 128 in bf16 with their queries
 // and values 55 us with 8 heads a workgroup (3.0 TB/s), 59 with 4, 63 with 2, 68 with 1; 81 when K went through LDS as fp32, which
 // took the room of other workgroups. Eight waves a SIMD, for which the angles spill a few registers, beat six (58 us), and loading
 // the next head during this one, at five, is worse still (66).
 template <typename T, int CPT, int MODE>
-__device__ inline void append_k(const RopeAppendArgs& a, int page, int h0, int h1, int t0, int lo, int hi, const T* x, float* lds) {
+__device__ inline void append_k(const RopeAppendArgs& a, int page, int h0, int step, int t0, int lo, int hi, const T* x, float* lds) {
     const KvView& kv = a.kv;
     const int pt = 1 << kv.page_shift, nt = blockDim.x, wave = threadIdx.x >> 6, own = threadIdx.x & 63;
     const int lanes = append_lanes(kv.hd, kv.slabs), at_once = 64 / lanes, slot = own / lanes;
@@ -230,7 +230,7 @@ __device__ inline void append_k(const RopeAppendArgs& a, int page, int h0, int h
         t[u].place(a.rope, own - slot * lanes, lanes);
         t[u].at(a.rope, t0 + lo + (u * (nt >> 6) + wave) * at_once + slot);
     }
-    for (int h = h0; h < h1; ++h) {
+    for (int h = h0; h < kv.n_kv; h += step) {
         int8_t* const ep = kv.exps + (((int64_t)a.layer * kv.n_pages + page) * kv.n_kv + h) * 2;
         uint8_t* const block = kv.codes + a.layer * kv.layer_bytes + page * kv.page_bytes + (int64_t)(h * 2) * (pt * kv.slabs * kTileDims);
         const int e0 = lo > 0 ? *ep : -128;
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kAppendWg, CPT == 1 ? 8 : CPT == 2 ? 4 : 2) void k_
     if (page < 0) return;
     const T* const x = static_cast<const T*>(a.kx[side]) + (int64_t)(a.b.row0[b] + t0 - before) * a.row_stride[side];
     if (side == 0) {
-        append_k<T, CPT, MODE>(a, page, share * a.heads, min(kv.n_kv, (share + 1) * a.heads), t0, lo, hi, x, s_mem);
+        append_k<T, CPT, MODE>(a, page, share, shares, t0, lo, hi, x, s_mem);
         return;
     }
     const auto load_v = [&](float* v, int t, int d) { load_row<4>(v, x + share * a.head_stride[1] + t * a.row_stride[1] + d); };
