@@ -398,6 +398,11 @@ __device__ inline int sequence_of(const PrefixArgs& a, const int* cum, int t, in
 template <typename T, int NS>
 constexpr int kTiles = run_tiles(sizeof(T) == 4 ? kF32 : kBF16, NS);
 
+// Bound by vector instructions (216 of them and 136 scalar ones a wave and piece of 32 tokens x 32 rows, the vector pipes three
+// quarters busy, the matrix units 0.37): 90 sequences of 3 new tokens behind two prompts of up to 30 Ki tokens, 32 over 8 heads of 128 in
+// bf16, 205 us with the join's 10 (634 TFLOP/s). Few rows are latency: 32 sequences behind one prompt of 8,011 tokens 24.8 us, of
+// which the join takes 6.6.
+//
 // Workgroups of a kv head's items are 8 apart where 8 divides the heads, so a head's tiles over one run share a die's cache.
 template <typename T, int NS>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(run_eu(sizeof(T) == 4 ? kF32 : kBF16, NS)))) void k_prefix(PrefixArgs a) {

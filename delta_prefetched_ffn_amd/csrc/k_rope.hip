@@ -5,7 +5,11 @@
 //     y = x * w / sqrt(mean(x^2) + eps),   (y_a, y_b) -> A (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
 // for pair i = (a, b) of the first `rot` values, t = 2 pi p F_i. F_i, a fraction of a turn, is held in 64 bits, so p F_i
 // mod 1 is the low half of an integer product: exact for every position, where a float product p F_i loses the angle of far
-// ones. What is left is a quarter of a turn at most, whose sine and cosine come from their power series in fp32.
+// ones. What is left is an eighth of a turn at most, whose sine and cosine come from their power series in fp32 (off by
+// 4.5e-8 at most, of which their rounding to fp32 is 3.0e-8).
+//
+// Bound by memory where there are many rows: 4,099 rows of 40 heads of 128 in fp16, 64 values of each turned, 17.1 us (4.9 TB/s, a large
+// copy's rate), one row of 64 heads 4.6 us in the trace, of which an empty launch is 3.4.
 #include "kv_quant.hpp"
 #include "rope_internal.hpp"
 
