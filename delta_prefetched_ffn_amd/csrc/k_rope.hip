@@ -166,7 +166,7 @@ struct Turner {
     }
 };
 
-constexpr int kWg = 256, kAppendWg = 512;
+constexpr int kWg = 256;
 
 // Heads [g0, g1) * (64 / lanes) of one row, queries first, by one wave.
 template <typename T, int MODE>
@@ -333,19 +333,15 @@ hipError_t rope_any(const RopeArgs& a, hipStream_t s) {
     return m == kAligned ? rope_as<T, kAligned>(a, s) : m == kPairs ? rope_as<T, kPairs>(a, s) : rope_as<T, kFarPairs>(a, s);
 }
 
-// A workgroup of k_rope_append holds a block: a thread 16 values of up to four tokens.
 template <typename T, int CPT, int MODE>
 hipError_t append_as(const RopeAppendArgs& a, int nt, hipStream_t s) {
-    const int groups = rope_groups(a.kv.hd, a.q.heads), waves = nt / 64;
-    const int64_t rows = (int64_t)a.rows * ((groups + a.per - 1) / a.per);
-    const int64_t grid = (int64_t)a.b.item0[a.b.n] * (a.kv.n_kv + (a.kv.n_kv + a.heads - 1) / a.heads) + (rows + waves - 1) / waves;
-    k_rope_append<T, CPT, MODE><<<(unsigned)grid, nt, MODE == kFarPairs ? nt * 16 * sizeof(float) : 0, s>>>(a);
+    k_rope_append<T, CPT, MODE><<<(unsigned)append_grid(a), nt, MODE == kFarPairs ? nt * 16 * sizeof(float) : 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, int MODE>
 hipError_t append_mode(const RopeAppendArgs& a, hipStream_t s) {
     const int threads = (1 << a.kv.page_shift) * append_lanes(a.kv.hd, a.kv.slabs);  // 64 .. 2048, a multiple of 64
-    const int nt = threads < kAppendWg ? threads : kAppendWg;
+    const int nt = append_threads(a.kv.page_shift, a.kv.hd, a.kv.slabs);
     if (threads <= nt) return append_as<T, 1, MODE>(a, nt, s);
     if (threads <= 2 * nt) return append_as<T, 2, MODE>(a, nt, s);
     return append_as<T, 4, MODE>(a, nt, s);

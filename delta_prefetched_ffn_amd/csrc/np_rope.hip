@@ -23,7 +23,7 @@ namespace {
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 // Enough waves to fill the device: below, a row's heads go to several waves (each works out the angles again).
 constexpr int64_t kFullWaves = 256 * 16;
-// A launch has at most 2^32 - 1 threads along x, in workgroups of 256.
+// A launch has at most 2^32 - 1 threads along x, np_rope_apply's in workgroups of 256.
 constexpr int64_t kMaxGroups = (int64_t)1 << 24;
 
 // What pair i turns by per position, in radians.
@@ -235,8 +235,7 @@ np_status append(const np_rope* r, np_kv* kv, int32_t layer, const void* q, void
     const int groups = rope_groups(D.head_dim, D.n_heads);
     a.per = groups_per_wave(rows, groups);
     a.heads = (int32_t)std::clamp<int64_t>(rows * D.n_kv_heads / kFullKeys, 1, D.n_kv_heads);
-    // Workgroups have one wave at least.
-    if ((int64_t)a.b.item0[a.b.n] * D.n_kv_heads * 2 + rows * ((groups + a.per - 1) / a.per) >= kMaxGroups)
+    if (append_grid(a) * append_threads(kv->page_shift, D.head_dim, kv->slabs) >> 32)
         return fail(NP_EINVAL, "%d pages of %d heads and %lld rows in one call are too many", a.b.item0[a.b.n], D.n_kv_heads, (long long)rows);
     std::optional<DeviceGuard> g;
     if ((st = make_current(kv, g)) != NP_OK) return st;

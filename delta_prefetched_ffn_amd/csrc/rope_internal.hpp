@@ -59,8 +59,20 @@ static_assert(sizeof(RopeAppendArgs) <= 4096, "kernel arguments are limited to 4
 constexpr int rope_lanes(int hd) { return hd <= 16 ? 1 : hd <= 32 ? 2 : hd <= 64 ? 4 : hd <= 128 ? 8 : 16; }
 // The same on the way into the cache, whose blocks hold whole slabs of 64 values.
 constexpr int append_lanes(int hd, int slabs) { return rope_lanes(hd) > slabs * 4 ? rope_lanes(hd) : slabs * 4; }
+// Threads of a workgroup there: 16 values each of a page's tokens, up to four tokens' where 512 do not reach.
+constexpr int kAppendWg = 512;
+constexpr int append_threads(int page_shift, int hd, int slabs) {
+    return (append_lanes(hd, slabs) << page_shift) < kAppendWg ? append_lanes(hd, slabs) << page_shift : kAppendWg;
+}
 // Groups of heads in a row (one wave's worth each).
 constexpr int rope_groups(int hd, int heads) { return (heads + 64 / rope_lanes(hd) - 1) / (64 / rope_lanes(hd)); }
+
+// Workgroups of a call.
+inline int64_t append_grid(const RopeAppendArgs& a) {
+    const int groups = rope_groups(a.kv.hd, a.q.heads), waves = append_threads(a.kv.page_shift, a.kv.hd, a.kv.slabs) / 64;
+    const int64_t rows = (int64_t)a.rows * ((groups + a.per - 1) / a.per);
+    return (int64_t)a.b.item0[a.b.n] * (a.kv.n_kv + (a.kv.n_kv + a.heads - 1) / a.heads) + (rows + waves - 1) / waves;
+}
 
 hipError_t launch_rope(const RopeArgs& a, int dtype, hipStream_t s);
 hipError_t launch_rope_append(const RopeAppendArgs& a, int dtype, hipStream_t s);

@@ -98,8 +98,7 @@ hipError_t launch_rope(const RopeArgs& a, int, hipStream_t) {
 }
 hipError_t launch_rope_append(const RopeAppendArgs& a, int, hipStream_t) {
     g_append = a;
-    const uint64_t items = (uint64_t)a.rows * ((rope_groups(a.kv.hd, a.q.heads) + a.per - 1) / a.per);
-    return launch(((uint64_t)a.b.item0[a.b.n] * a.kv.n_kv * 2 + items) * 256);
+    return launch((uint64_t)append_grid(a) * append_threads(a.kv.page_shift, a.kv.hd, a.kv.slabs));
 }
 hipError_t launch_w4_pack(const W4PackArgs&, hipStream_t) { return launch(256); }
 hipError_t launch_w4(const W4Args& a, int, hipStream_t) {

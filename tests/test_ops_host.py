@@ -252,6 +252,22 @@ def test_rope_refusals(B):
     r.close()
 
 
+def test_the_largest_prompts_fit_a_launch_or_are_refused(B):
+    # Workgroups of up to 512 threads, of which a launch takes less than 2^32.
+    for heads, kv, hd, page, pages in ((64, 64, 256, 128, 62000), (64, 64, 256, 128, 120000), (64, 64, 8, 16, 130000), (1, 1, 256, 128, 65000), (128, 128, 8, 16, 62000), (128, 128, 8, 16, 70000), (64, 64, 256, 128, 130000), (128, 128, 8, 16, 600000)):
+        c = cache(B, n_heads=heads, n_kv_heads=kv, head_dim=hd, page_tokens=page, n_pages=pages, max_pages=pages, max_seqs=2)
+        rope = B.Rope(head_dim=hd, device=1)
+        c.extend([0], [pages * page])
+        launches = B.stub.stub_launches()
+        try:
+            rope.append(c, 0, P, P << 22, P << 23, P << 24, "bf16")
+        except B.NPError as e:
+            assert e.status == B.NP_EINVAL and "too many" in str(e), (heads, hd, page, pages, str(e))
+            assert B.stub.stub_launches() == launches
+        else:
+            assert B.stub.stub_launches() == launches + 1
+
+
 def test_failed_allocations_reach_the_caller(B):
     for make in (lambda: B.Rope(head_dim=64, device=1), lambda: B.W4(n_out=16, n_in=128, group=128, codes_ptr=P, scales_ptr=P, scale_dtype="f16", device=1)):
         for after in range(20):
