@@ -324,15 +324,16 @@ __global__ __launch_bounds__(64 * kWaves, R == 1 ? 4 : 2) void k_w4_rows(W4Args 
     }
 }
 
-// Many rows: one workgroup of four waves per (64 H rows, 128 outputs); a wave has all the rows x 32 outputs, in products of
-// 32x32x16. The workgroup's x of a chunk of 128 inputs is in LDS as operands (two chunks: one is read while the next one's
-// loads are on their way), with the sums of each row and group, three bf16 terms of them, that take the zero points out: one
-// more product per group, with -z as the other operand. Each wave widens the codes of its outputs itself, no two the same ones.
+// Many rows: one workgroup of 4 S waves per (64 H rows, 128 outputs); a wave has all the rows x 32 outputs, in products of
+// 32x32x16, S = 2 of them half of each chunk's inputs each, joined in LDS behind the last one. The workgroup's x of a chunk of 128 inputs
+// is in LDS as operands (two chunks: one is read while the next one's loads are on their way), with the sums of each row and group (or half
+// of one), three bf16 terms of them, that take the zero points out: one more product per group, with -z as the other operand. Each wave
+// widens the codes of its outputs itself, no two the same ones.
 //
-// Bound by the instructions around the matrix products: per chunk and wave 32 of them need 1,024 cycles, the loads, widening,
-// staging and folds beside them some 400 instructions. 1,500 rows x 5120 x 15,360: 329 us in bf16 (716 TFLOP/s), with groups of
-// 32 428 us, fp32 (six times the products) 1,315 us; with waves of half the rows x 64 outputs, which widen all codes twice, 345,
-// 481 and 1,239 us, fp32 with groups of 32 2,265 us (registers) for 1,330.
+// Bound by the instructions around the matrix products: per chunk, 128 rows and wave 32 of them need 1,024 cycles, the loads,
+// widening, staging and folds beside them 331 vector instructions. 1,500 rows x 5120 x 15,360 (H = 2, S = 1): 327 us in bf16 (721 TFLOP/s),
+// with groups of 32 429 us; with waves of half the rows x 64 outputs, which widen all codes twice, 345 and 481 us. fp32 (H = 1, S = 2; three
+// products for each) 1,058 us.
 //
 // Operand slots: step (s, e) of a chunk, lane half h: inputs 32 s + 8 (h + 2 e) + j, so that a lane's 16 bytes of quad h + 2 e of a
 // tile are its operands of four steps.
@@ -362,12 +363,13 @@ __device__ inline float quad_sum(float x) {
     return x;
 }
 
-template <typename T, int H, int G>
-__global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, int out_blocks) {
+template <typename T, int H, int S, int G>
+__global__ __launch_bounds__(256 * S, S == 1 ? 2 : sizeof(T) == 2 && G < 4 ? 4 : 2) void k_w4_tile(W4Args a, int row_blocks, int out_blocks) {
     typedef Kind<T> Kd;
     typedef typename Kd::E E;
     typedef typename Vec8<E>::t E8;
-    constexpr int N = Kd::kTerms, kRows = 64 * H, RT = 2 * H, TT = 1;
+    constexpr int N = Kd::kTerms, kRows = 64 * H, RT = 2 * H, TT = 1, SG = G < S ? S : G;
+    static_assert(H * S <= 2, "a wave stages whole rows or half chunks of them");
     const W4View& w = a.w;
     // Workgroups go to the 8 dies in turn: a die takes its own outputs, with all rows one after the other.
     const int die = blockIdx.x & 7, nth = blockIdx.x >> 3;
@@ -376,44 +378,51 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
     const int64_t r0 = (int64_t)rb * kRows;
     const int rows = (int)min((int64_t)kRows, a.rows - r0);
-    const int tile0 = ob * 8 + wave * 2;
+    const int part_of = wave >> 2, tile0 = ob * 8 + (wave & 3) * 2;
     extern __shared__ __attribute__((aligned(128))) uint8_t s_dyn[];
     E8* const s_x = reinterpret_cast<E8*>(s_dyn);  // [2][2 H row tiles][8 steps][N][2 halves][32 rows, changed places]
     constexpr int kBuf = 2 * H * 8 * N * 64;
-    bf16x8* const s_sum = reinterpret_cast<bf16x8*>(s_dyn + 2 * kBuf * 16);  // [2][G][rows]
+    bf16x8* const s_sum = reinterpret_cast<bf16x8*>(s_dyn + 2 * kBuf * 16);  // [2][SG][rows]
 
     // Staging: a wave brings 16 H rows in units of 16 rows x 32 inputs: lane 4 r + q has quad q of row r. Places in LDS: row r of (step,
     // half) at r ^ 4 q, so that a unit's 64 stores meet no bank twice.
-    XRaw<T> stage[H][4];
+    constexpr int kSteps = 4 / S;  // of 32 inputs, that a wave brings
+    XRaw<T> stage[H][kSteps];
     const int sr = lane >> 2, sq = lane & 3;
     const T* xs[H];
 #pragma unroll
-    for (int u = 0; u < H; ++u) xs[u] = static_cast<const T*>(a.x) + (r0 + min(wave * 16 * H + u * 16 + sr, rows - 1)) * a.x_row + sq * 8;
+    for (int u = 0; u < H; ++u) xs[u] = static_cast<const T*>(a.x) + (r0 + min((wave & 3) * 16 * H + u * 16 + sr, rows - 1)) * a.x_row + part_of * kSteps * 32 + sq * 8;
     const auto ask_x = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < H; ++u)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) stage[u][s] = load_x<T>(xs[u] + c * kW4Ins + s * 32, c * kW4Ins + s * 32 + sq * 8 < w.n_in);
+            for (int s = 0; s < kSteps; ++s)
+                stage[u][s] = load_x<T>(xs[u] + c * kW4Ins + s * 32, c * kW4Ins + (part_of * kSteps + s) * 32 + sq * 8 < w.n_in);
     };
     const auto put_x = [&](int c) __attribute__((always_inline)) {
         E8* const to = s_x + (c & 1) * kBuf;
-        bf16x8* const sums = s_sum + (c & 1) * G * kRows;
+        bf16x8* const sums = s_sum + (c & 1) * SG * kRows;
 #pragma unroll
         for (int u = 0; u < H; ++u) {
-            const int row = wave * 16 * H + u * 16 + sr;
-            float part[4];
+            const int row = (wave & 3) * 16 * H + u * 16 + sr;
+            float part[kSteps];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
+            for (int s = 0; s < kSteps; ++s) {
                 E8 o[N];
                 operands<T>(o, stage[u][s]);
 #pragma unroll
                 for (int n = 0; n < N; ++n)
-                    to[((((row >> 5) * 8 + 2 * s + (sq >> 1)) * N + n) * 2 + (sq & 1)) * 32 + ((row & 31) ^ (4 * sq))] = o[n];
+                    to[((((row >> 5) * 8 + 2 * (part_of * kSteps + s) + (sq >> 1)) * N + n) * 2 + (sq & 1)) * 32 + ((row & 31) ^ (4 * sq))] = o[n];
                 part[s] = quad_sum(sum8<T>(stage[u][s]));
             }
-            // Lane q writes group q's sum.
-            float v = G == 4 ? (sq == 0 ? part[0] : sq == 1 ? part[1] : sq == 2 ? part[2] : part[3])
-                             : G == 2 ? (sq ? part[2] + part[3] : part[0] + part[1]) : (part[0] + part[1]) + (part[2] + part[3]);
+            // Lane q writes the sum of the wave's group q.
+            constexpr int kSums = SG / S;
+            float v = part[0];
+            if constexpr (kSums == 4) v = sq == 0 ? part[0] : sq == 1 ? part[1] : sq == 2 ? part[2] : part[3];
+            else if constexpr (kSums == kSteps) v = sq ? part[1] : part[0];
+            else if constexpr (kSums == 2) v = sq ? part[2] + part[3] : part[0] + part[1];
+            else if constexpr (kSteps == 2) v = part[0] + part[1];
+            else v = (part[0] + part[1]) + (part[2] + part[3]);
             u32x4 t = {0, 0, 0, 0};
             const uint32_t t0 = __float_as_uint(v) & 0xffff0000u;
             v -= __uint_as_float(t0);
@@ -421,7 +430,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             v -= __uint_as_float(t1);
             t[0] = t0 >> 16 | t1;
             t[1] = __float_as_uint(v) >> 16;
-            if (sq < G) sums[sq * kRows + row] = __builtin_bit_cast(bf16x8, t);
+            if (sq < kSums) sums[(part_of * kSums + sq) * kRows + row] = __builtin_bit_cast(bf16x8, t);
         }
     };
     // Codes of outputs 32 t + col: quads h and h + 2 of the tile.
@@ -430,27 +439,32 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);  // past the last: not stored
-        tiles[t] = w.tiles + tile * w.chunks * kW4TileBytes + (h * 16 + (col & 15)) * 16;
+        tiles[t] = w.tiles + tile * w.chunks * kW4TileBytes + (h * 16 + (col & 15)) * 16 + part_of * kSteps * 4;
         groups[t] = tile * w.chunks * G * kW4Outs + (col & 15);
     }
-    u32x4 code[TT][2], next[TT][2];
-    u32x2 scale[TT][G];
-    const auto ask_codes = [&](u32x4 (&o)[TT][2], int c) __attribute__((always_inline)) {
+    // Of a chunk's SG parts (groups, or halves of one) a wave takes kParts, and the dwords of its steps.
+    constexpr int kParts = SG / S;
+    struct Codes {
+        alignas(4 * kSteps) uint32_t s[kSteps];
+    };
+    Codes code[TT][2], next[TT][2];
+    u32x2 scale[TT][kParts];
+    const auto ask_codes = [&](Codes (&o)[TT][2], int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) o[t][e] = *reinterpret_cast<const u32x4*>(tiles[t] + (int64_t)c * kW4TileBytes + e * 512);
+            for (int e = 0; e < 2; ++e) o[t][e] = *reinterpret_cast<const Codes*>(tiles[t] + (int64_t)c * kW4TileBytes + e * 512);
     };
     const auto ask_scales = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int64_t at = groups[t] + (c * G + g) * kW4Outs;
+            for (int g = 0; g < kParts; ++g) {
+                const int64_t at = groups[t] + (c * G + (part_of * kParts + g) * G / SG) * kW4Outs;
                 scale[t][g] = load_scale(w, at);
             }
     };
-    f32x16 tot[RT][TT];
+    float tot[RT][TT][16];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -469,9 +483,9 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             ask_codes(next, c + 1);
         }
         const E8* const from = s_x + (c & 1) * kBuf + h * 32;
-        const bf16x8* const sums = s_sum + (c & 1) * G * kRows + col;
+        const bf16x8* const sums = s_sum + (c & 1) * SG * kRows + col;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+        for (int g = 0; g < kParts; ++g) {
             f32x16 part[RT][TT];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -480,11 +494,11 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[r][t][j] = 0.0f;
 #pragma unroll
-            for (int step = g * 8 / G; step < (g + 1) * 8 / G; ++step) {
-                const int s = step >> 1, e = step & 1;
+            for (int at = 0; at < 8 / SG; ++at) {
+                const int own = g * (8 / SG) + at, step = part_of * 2 * kSteps + own, s = own >> 1, e = own & 1;
                 E8 cw[TT];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) cw[t] = codes_of<E>(code[t][e][s]);
+                for (int t = 0; t < TT; ++t) cw[t] = codes_of<E>(code[t][e].s[s]);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -496,7 +510,7 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             }
             bf16x8 xs8[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) xs8[r] = sums[g * kRows + 32 * r];
+            for (int r = 0; r < RT; ++r) xs8[r] = sums[(part_of * kParts + g) * kRows + 32 * r];
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const float sc = scale_value(scale[t][g], w.scale_words), z = (float)zero_value(scale[t][g], w.scale_words);
@@ -506,9 +520,11 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
                 for (int r = 0; r < RT; ++r) {
                     part[r][t] = mfma(xs8[r], minus, part[r][t]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
-                    // Here: the compiler moves these behind the next stores, and all groups' sums wait for them.
-                    if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(tot[r][t]));
+                    for (int j = 0; j < 16; ++j) {
+                        tot[r][t][j] = __builtin_fmaf(sc, part[r][t][j], tot[r][t][j]);
+                        // Here: the compiler moves these behind the next stores, and all groups' sums wait for them.
+                        if constexpr (sizeof(T) == 2) asm volatile("" : "+v"(tot[r][t][j]));
+                    }
                 }
             }
             if (G > 1) __builtin_amdgcn_sched_barrier(0);
@@ -530,9 +546,9 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
             for (int j = 0; j < 16; ++j) odd |= not_finite(tot[r][t][j]);
     if (__any(odd)) {
         // The wave's products again, one at a time, x from memory.
-#pragma unroll 1
+#pragma unroll
         for (int r = 0; r < RT; ++r) {
-#pragma unroll 1
+#pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const T* const x0 = static_cast<const T*>(a.x) + (r0 + min(32 * r + col, rows - 1)) * a.x_row;
                 const int64_t tile = min(tile0 + 2 * t + (col >> 4), w.out_tiles - 1);
@@ -544,9 +560,9 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
 #pragma unroll 1
                     for (int e = 0; e < 2; ++e) {
                         const int q = h + 2 * e;
-                        const u32x4 cd = *reinterpret_cast<const u32x4*>(w.tiles + (tile * w.chunks + c) * kW4TileBytes + (q * 16 + (col & 15)) * 16);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
+                        const uint32_t* const cd = reinterpret_cast<const uint32_t*>(w.tiles + (tile * w.chunks + c) * kW4TileBytes + (q * 16 + (col & 15)) * 16);
+#pragma unroll 1
+                        for (int s = part_of * kSteps; s < (part_of + 1) * kSteps; ++s) {
                             const int g = s * G / 4, k = c * kW4Ins + s * 32 + q * 8;
                             const int64_t at = ((tile * w.chunks + c) * G + g) * kW4Outs + (col & 15);
                             const u32x2 words = load_scale(w, at);
@@ -565,15 +581,27 @@ __global__ __launch_bounds__(256, 2) void k_w4_tile(W4Args a, int row_blocks, in
                     }
                 }
 #pragma unroll
-                for (int rr = 0; rr < RT; ++rr)
-#pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
-                        if (rr == r && tt == t)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (not_finite(tot[rr][tt][j])) tot[rr][tt][j] = again[j];
+                for (int j = 0; j < 16; ++j)
+                    if (not_finite(tot[r][t][j])) tot[r][t][j] = again[j];
             }
         }
+    }
+    if constexpr (S > 1) {  // the other half's sums, through LDS
+        float* const s_part = reinterpret_cast<float*>(s_dyn);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float* const at = s_part + ((wave & 3) * RT * 16 + r * 16 + j) * 64 + lane;
+                if (part_of) *at = tot[r][0][j];
+            }
+        __syncthreads();
+        if (part_of) return;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) tot[r][0][j] += s_part[(wave * RT * 16 + r * 16 + j) * 64 + lane];
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -669,10 +697,15 @@ hipError_t rows_prepare() {
     return e;
 }
 
-template <typename T>
-constexpr int kTileH = sizeof(T) == 2 ? 2 : 1;  // what two chunks of LDS hold
-template <typename T, int G>
-constexpr int kTileLds = 2 * (2 * kTileH<T> * 8 * Kind<T>::kTerms * 1024 + G * 64 * kTileH<T> * 16);
+template <typename T, int H, int S, int G>
+constexpr int kTileLds = std::max(2 * (2 * H * 8 * Kind<T>::kTerms * 1024 + (G < S ? S : G) * 64 * H * 16), S == 1 ? 0 : 4 * 2 * H * 16 * 64 * 4);
+template <typename T, int H, int S, int G>
+hipError_t tile_as(const W4Args& a, hipStream_t s) {
+    const int row_blocks = (int)((a.rows + 64 * H - 1) / (64 * H)), out_blocks = (a.w.n_out + kTileOuts - 1) / kTileOuts;
+    const unsigned grid = (unsigned)((out_blocks + 7) / 8 * 8) * row_blocks;
+    k_w4_tile<T, H, S, G><<<grid, 256 * S, kTileLds<T, H, S, G>, s>>>(a, row_blocks, out_blocks);
+    return hipGetLastError();
+}
 
 template <typename T, int G>
 hipError_t w4_as(const W4Args& a, hipStream_t s) {
@@ -681,18 +714,18 @@ hipError_t w4_as(const W4Args& a, hipStream_t s) {
     }
     if (a.rows <= 16) return rows_of<T, 1, false, G>(a, s);
     if (a.rows <= 32) return rows_of<T, 2, false, G>(a, s);
-    // While the workgroups of 64 rows are few, the other kernel would leave compute units idle (64 rows x 128 outputs each and more),
-    // and a chunk of it takes 2.1 us whatever they are: 4096 x 11008, bf16, 128 rows 83 us for 182 there, 256 rows 163 for 182, and
-    // from 1,024 workgroups on it is the faster one: 32,000 x 4096 takes 71 us there with 65 rows and 74 here with 64. fp32, where a workgroup has one tile:
-    // 4096 x 11008, 128 rows 167 us for 218, and 15,360 x 5120, 64 rows 169 for 101.
-    constexpr int64_t most = sizeof(T) == 2 ? 1024 : 512;
+    // While the workgroups of 64 rows are few, the tiles' would leave compute units idle (64 rows x 128 outputs each), and a chunk takes
+    // one of those 1.3 us: 4096 x 11008, 128 rows 82 us for 110 (512 workgroups), 192 rows 123 for 110; fp32 64 rows 85 for 181
+    // (256), 128 rows 167 for 180, but 15,360 x 5120, 64 rows 168 for 87 (960).
     const int o = rows_o<T, 4, false, G>(a);
-    if ((a.rows + 63) / 64 * ((a.w.out_tiles + o - 1) / o) <= most) return rows_of<T, 4, false, G>(a, s);
-    constexpr int H = kTileH<T>;
-    const int row_blocks = (int)((a.rows + 64 * H - 1) / (64 * H)), out_blocks = (a.w.n_out + kTileOuts - 1) / kTileOuts;
-    const unsigned grid = (unsigned)((out_blocks + 7) / 8 * 8) * row_blocks;
-    k_w4_tile<T, H, G><<<grid, 256, kTileLds<T, G>, s>>>(a, row_blocks, out_blocks);
-    return hipGetLastError();
+    if ((a.rows + 63) / 64 * ((a.w.out_tiles + o - 1) / o) <= (sizeof(T) == 2 ? 512 : 256)) return rows_of<T, 4, false, G>(a, s);
+    // Eight waves of 64 rows while two such workgroups a compute unit hold all of them; four of 128 rows beyond, which widen the codes
+    // half as often: 15,360 x 5120, 256 rows (480 workgroups) 70 us for 93, 512 rows 134 for 112. In fp32 the smaller one is always
+    // ahead (1,500 rows 1,058 us; four waves of 64 rows 1,307, and 128 rows do not fit LDS).
+    if constexpr (sizeof(T) == 2) {
+        if ((a.rows + 63) / 64 * ((a.w.n_out + kTileOuts - 1) / kTileOuts) > 512) return tile_as<T, 2, 1, G>(a, s);
+    }
+    return tile_as<T, 1, 2, G>(a, s);
 }
 template <typename T>
 hipError_t w4_any(const W4Args& a, hipStream_t s) {
@@ -706,7 +739,11 @@ hipError_t prepare() {
         const hipError_t e = rows_prepare<T, 1, true, G>();
         if (e != hipSuccess) return e;
     }
-    for (hipError_t e : {allow(reinterpret_cast<const void*>(k_w4_tile<T, kTileH<T>, G>), kTileLds<T, G>), rows_prepare<T, 1, false, G>(),
+    if constexpr (sizeof(T) == 2) {
+        const hipError_t e = allow(reinterpret_cast<const void*>(k_w4_tile<T, 2, 1, G>), kTileLds<T, 2, 1, G>);
+        if (e != hipSuccess) return e;
+    }
+    for (hipError_t e : {allow(reinterpret_cast<const void*>(k_w4_tile<T, 1, 2, G>), kTileLds<T, 1, 2, G>), rows_prepare<T, 1, false, G>(),
                          rows_prepare<T, 2, false, G>(), rows_prepare<T, 4, false, G>()})
         if (e != hipSuccess) return e;
     return hipSuccess;

@@ -110,8 +110,8 @@ np_status matvec(const np_w4* w, int64_t rows, const void* x, int32_t x_dtype, i
         const int64_t step = x_row * xb, off = step ? ((y0 - x0) % step + step) % step : 0;
         if (step != y_row * yb || off < (int64_t)D.n_in * xb || off + (int64_t)D.n_out * yb > step) return fail(NP_EINVAL, "x and y must not overlap");
     }
-    // A launch has at most 2^32 - 1 threads along x: workgroups of 256 for 64 rows x 128 outputs each, at the least.
-    if ((rows + 63) / 64 * ((D.n_out + 1023) / 1024 * 8) >= 1 << 24) return fail(NP_EINVAL, "%lld rows of %d outputs in one call are too many", (long long)rows, D.n_out);
+    // A launch has at most 2^32 - 1 threads along x: workgroups of 512 for 64 rows x 128 outputs each, at the most.
+    if ((rows + 63) / 64 * ((D.n_out + 1023) / 1024 * 8) >= 1 << 23) return fail(NP_EINVAL, "%lld rows of %d outputs in one call are too many", (long long)rows, D.n_out);
     np_status st;
     if ((st = check_io_ptr(x, D.device, "x", "weights")) != NP_OK) return st;
     if ((st = check_io_ptr(y, D.device, "y", "weights")) != NP_OK) return st;

@@ -103,7 +103,7 @@ hipError_t launch_rope_append(const RopeAppendArgs& a, int, hipStream_t) {
 hipError_t launch_w4_pack(const W4PackArgs&, hipStream_t) { return launch(256); }
 hipError_t launch_w4(const W4Args& a, int, hipStream_t) {
     g_w4 = a;
-    return launch((uint64_t)((a.rows + 63) / 64) * ((a.w.out_tiles + 63) / 64 * 8) * 256);
+    return launch((uint64_t)((a.rows + 63) / 64) * ((a.w.out_tiles + 63) / 64 * 8) * 512);
 }
 hipError_t w4_prepare() { return hipSuccess; }
 }  // namespace np

@@ -123,7 +123,8 @@ def kernel_of(m, xd, rows):
     from tests import test_gpu_kv as K
     K.torch = torch
     x, y = torch.zeros((rows, m.n_in), dtype=tdt(xd), device="cuda"), torch.zeros((rows, m.n_out), device="cuda")
-    got = {("k_w4_tile" if "k_w4_tile" in n else "k_w4_rows") for n in K.kernels_of(lambda s: m.w.matvec(rows, x.data_ptr(), xd, y.data_ptr(), "f32", stream=s)) if "k_w4" in n}
+    names = [n for n in K.kernels_of(lambda s: m.w.matvec(rows, x.data_ptr(), xd, y.data_ptr(), "f32", stream=s)) if "k_w4" in n]
+    got = {"rows" if "k_w4_rows" in n else "eight waves" if "Li1ELi2ELi" in n else "four waves" for n in names}
     assert len(got) == 1
     return got.pop()
 
@@ -139,25 +140,28 @@ def test_many_outputs(xd, n_out, n_in, group, scales):
 
 
 @pytest.mark.parametrize("xd", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("n_out,rows,n_in,group,scales", [(130, 7301, 72, 32, "f16"), (1050, 1111, 264, 64, "f32"), (265, 4000, 392, 128, "bf16"), (16390, 129, 520, 256, "f16"), (2060, 640, 128, 32, "bf16")])
+@pytest.mark.parametrize("n_out,rows,n_in,group,scales", [(130, 7301, 72, 32, "f16"), (1050, 1111, 264, 64, "f32"), (265, 4000, 392, 128, "bf16"), (16390, 129, 520, 256, "f16"), (2060, 640, 128, 32, "bf16"),
+                                                            (1050, 3700, 72, 32, "f32"), (16390, 260, 392, 64, "f16"), (2060, 2000, 264, 128, "bf16")])
 def test_many_rows_and_outputs(xd, n_out, rows, n_in, group, scales):
     rng = np.random.default_rng(rows)
     m = Matrix(rng, n_out, n_in, group, scales)
-    assert kernel_of(m, xd, rows) == "k_w4_tile"
+    many = -(-rows // 64) * -(-n_out // 128) > 512
+    assert kernel_of(m, xd, rows) == ("four waves" if many and xd != "f32" else "eight waves")
     run(m, rng.standard_normal((rows, n_in)), xd, "f32", rows, accumulate=True)
     run(m, rng.standard_normal((rows, n_in)), xd, "bf16", rows, pad=1)
 
 
 @pytest.mark.parametrize("xd", ["f32", "bf16", "f16"])
-def test_infinities_and_nan_in_many_rows(xd):
+@pytest.mark.parametrize("n_out,rows,n_in,group", [(265, 3900, 200, 64), (20, 33000, 136, 32), (265, 3900, 264, 128)])
+def test_infinities_and_nan_in_many_rows(xd, n_out, rows, n_in, group):
     rng = np.random.default_rng(11)
-    m = Matrix(rng, 265, 200, 64)
-    x = rng.standard_normal((3900, 200))
-    x[3, 7], x[4, 150], x[5, 0], x[5, 199], x[3899, 199], x[640, 64] = -np.inf, np.nan, np.inf, -np.inf, np.inf, np.inf
+    m = Matrix(rng, n_out, n_in, group)
+    x = rng.standard_normal((rows, n_in))
+    x[3, 7], x[4, 130], x[5, 0], x[5, n_in - 1], x[rows - 1, n_in - 1], x[640, 64] = -np.inf, np.nan, np.inf, -np.inf, np.inf, np.inf
     x[8] = 0.0
-    assert kernel_of(m, xd, 3900) == "k_w4_tile"
-    assert bool((run(m, x, xd, "f32", 3900)[8] == 0).all())
-    run(m, rng.standard_normal((3900, 200)) * (2.0 ** 12 if xd == "f16" else 2.0 ** 100), xd, "f32", 3900)
+    assert kernel_of(m, xd, rows) == ("four waves" if rows > 4000 and xd != "f32" else "eight waves")
+    assert bool((run(m, x, xd, "f32", rows)[8] == 0).all())
+    run(m, rng.standard_normal((rows, n_in)) * (2.0 ** 12 if xd == "f16" else 2.0 ** 100), xd, "f32", rows)
 
 
 def test_small_values_and_exact_products():
@@ -194,7 +198,7 @@ def test_small_values_and_exact_products():
 def test_the_same_from_run_to_run_on_streams_and_in_graphs():
     rng = np.random.default_rng(4)
     m = Matrix(rng, 1000, 1024, 128)
-    for rows in (1, 12, 64, 200, 1700):   # the last one takes the tiles of many rows
+    for rows in (1, 12, 64, 200, 1700, 5000):   # the last two take the tiles of many rows
         x = torch.from_numpy(rng.standard_normal((rows, 1024)).astype(np.float32)).bfloat16().cuda()
         want, y = torch.empty((rows, 1000), device="cuda"), torch.zeros((rows, 1000), device="cuda")
         m.w.matvec(rows, x.data_ptr(), "bf16", want.data_ptr(), "f32", stream=stream())
