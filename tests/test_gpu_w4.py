@@ -240,6 +240,31 @@ def test_columns_of_one_buffer_and_weights_past_4_gib_of_offsets():
     check(y, want, slack, "f32")
 
 
+def test_weights_past_4_gib():
+    # 2^20 outputs x 8,200 inputs: the last outputs' tiles lie past 2^32 bytes.
+    from delta_prefetched_ffn_amd import W4
+    n_out, n_in, last = 1 << 20, 8200, 40
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 256, (n_out, n_in // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    groups = -(-n_in // 4096)
+    sc = (torch.rand((n_out, groups), device="cuda", generator=gen) + 0.5).bfloat16()
+    w = W4(n_out=n_out, n_in=n_in, group=4096, codes_ptr=codes.data_ptr(), scales_ptr=sc.data_ptr(), scale_dtype="bf16")
+    tail = codes[-last:].cpu().numpy().astype(np.int64)
+    m = Matrix.__new__(Matrix)
+    m.c = np.empty((last, n_in), np.int64)
+    m.c[:, 0::2], m.c[:, 1::2] = tail & 15, tail >> 4
+    m.z, m.s = np.full((last, groups), 8), sc[-last:].double().cpu().numpy()
+    m.n_out, m.n_in, m.group, m.groups = last, n_in, 4096, groups
+    del codes
+    for rows in (1, 20, 70):
+        x = torch.randn((rows, n_in), device="cuda", generator=gen).bfloat16()
+        y = torch.empty((rows, n_out), device="cuda")
+        w.matvec(rows, x.data_ptr(), "bf16", y.data_ptr(), "f32", stream=stream())
+        want, slack = m.product(x.double().cpu().numpy())
+        check(y[:, -last:], want, slack, "f32")
+    w.close()
+
+
 def test_refusals():
     from delta_prefetched_ffn_amd import W4, NPError
     from delta_prefetched_ffn_amd import binding as B
