@@ -351,7 +351,7 @@ class KVCache:
 
     def append(self, layer: int, k_ptr: int, v_ptr: int, dtype: str, strides=None, stream: int = 0) -> None:
         """Stores the current tokens' k, v [rows][n_kv_heads][head_dim]; strides (elements): k row, k head, v row, v head."""
-        if layer >> 31 > 0:
+        if layer >> 31:   # negative or too large
             _i32(layer)
         rc = self._append(self.h, layer, k_ptr, v_ptr, DTYPES[dtype], self._stride_array(strides), stream or None)
         if rc:
@@ -372,7 +372,7 @@ class KVCache:
                sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
         """Attention of the current tokens: q, out [rows][n_heads][head_dim]; strides (elements): q row, q head, out row,
         out head; window 0: every earlier token, else the last `window` and the first `sinks`."""
-        if (layer | window | sinks) >> 31 > 0:
+        if (layer | window | sinks) >> 31:   # one of them negative or too large
             for x in (layer, window, sinks):
                 _i32(x)
         rc = self._attend(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
@@ -383,7 +383,7 @@ class KVCache:
     def attend_shared(self, layer: int, q_ptr: int, out_ptr: int, dtype: str, strides=None, *, scale: float, window: int = 0,
                       sinks: int = 0, lse_ptr: int = 0, stream: int = 0) -> None:
         """attend(), with first pages that several sequences of the step share (fork) read once for all of them."""
-        if (layer | window | sinks) >> 31 > 0:
+        if (layer | window | sinks) >> 31:   # one of them negative or too large
             for x in (layer, window, sinks):
                 _i32(x)
         rc = lib().np_attend_shared(self.h, layer, q_ptr, out_ptr, lse_ptr or None, DTYPES[dtype], self._stride_array(strides), scale,
@@ -538,7 +538,7 @@ class Rope:
                q_weight_ptr: int = 0, k_weight_ptr: int = 0, eps: float = 1e-6, stream: int = 0) -> None:
         """The cache's current tokens: q normalised and turned into q_out; k, normalised and turned, and v stored in the cache;
         strides (elements): row and head of q, q_out, k, v."""
-        if layer >> 31 > 0:
+        if layer >> 31:   # negative or too large
             _i32(layer)
         rc = self._append(self.h, kv.h, layer, q_ptr, q_out_ptr, k_ptr, v_ptr, q_weight_ptr or None, k_weight_ptr or None, eps,
                           DTYPES[dtype], self._strides(strides), stream or None)
