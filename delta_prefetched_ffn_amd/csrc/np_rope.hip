@@ -21,6 +21,8 @@ struct np_rope {
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
+// What a pair may turn by per position, in radians: of more, turn_bits() would lose bits behind the point.
+constexpr double kMostTurn = 1099511627776.0;
 // Enough waves to fill the device: below, a row's heads go to several waves (each works out the angles again).
 constexpr int64_t kFullWaves = 256 * 16;
 // A launch has at most 2^32 - 1 threads along x, np_rope_apply's in workgroups of 256.
@@ -47,7 +49,7 @@ np_status check_desc(const np_rope_desc& D) {
     if (!(std::isfinite(D.amplitude) && D.amplitude > 0.0f)) return fail(NP_EINVAL, "amplitude=%g must be positive and finite", D.amplitude);
     if (D.freqs) {
         for (int i = 0; i < D.rot_dim / 2; ++i)
-            if (!std::isfinite(D.freqs[i])) return fail(NP_EINVAL, "freqs[%d]=%g must be finite", i, D.freqs[i]);
+            if (!(std::fabs(D.freqs[i]) <= kMostTurn)) return fail(NP_EINVAL, "freqs[%d]=%g must be at most 2^40", i, D.freqs[i]);
         return NP_OK;
     }
     if (!(std::isfinite(D.base) && D.base > 0.0)) return fail(NP_EINVAL, "base=%g must be positive and finite", D.base);
@@ -58,15 +60,18 @@ np_status check_desc(const np_rope_desc& D) {
     if (D.scaling == NP_ROPE_BLEND && !(D.context > 0 && std::isfinite(D.low) && std::isfinite(D.high) && D.low < D.high))
         return fail(NP_EINVAL, "context=%lld must be positive and low=%g below high=%g", (long long)D.context, D.low, D.high);
     for (int i = 0; i < D.rot_dim / 2; ++i)
-        if (!std::isfinite(freq_of(D, i))) return fail(NP_EINVAL, "pair %d turns by %g a position: not finite", i, freq_of(D, i));
+        if (!(std::fabs(freq_of(D, i)) <= kMostTurn)) return fail(NP_EINVAL, "pair %d turns by %g a position: more than 2^40", i, freq_of(D, i));
     return NP_OK;
 }
 
-// f radians as a fraction of a turn, in 2^-64 (whole turns do not count).
+// 1 / (2 pi): its first 64 bits, and 64 of what they leave out.
+constexpr long double kTurns = 0xa2f9836e4e44152ap-66L, kTurnsRest = -0xf62a0b82b2c88fc9p-136L;
+// f radians as a fraction of a turn, to the nearest 2^-64 (whole turns do not count), for |f| <= kMostTurn.
 uint64_t turn_bits(double f) {
-    const long double t = (long double)f / 6.283185307179586476925286766559005768L;
-    const long double part = (t - std::floor(t)) * 18446744073709551616.0L;
-    return part >= 18446744073709551616.0L ? 0 : (uint64_t)part;
+    const long double a = std::fabs(f), t = a * kTurns, rest = std::fma(a, kTurns, -t) + a * kTurnsRest;  // t + rest turns
+    const long double part = (t - std::floor(t)) * 18446744073709551616.0L, whole = std::floor(part);
+    const uint64_t bits = (uint64_t)whole + (uint64_t)std::llround(part - whole + rest * 18446744073709551616.0L);
+    return f < 0.0 ? 0 - bits : bits;
 }
 
 np_status create(const np_rope_desc* desc, np_rope** out) {

@@ -603,8 +603,8 @@ typedef struct np_rope_desc {
     double factor;       /* positive; not used by PLAIN                      */
     int64_t context;     /* BLEND: positions of the trained context          */
     double low, high;    /* BLEND, low < high                                */
-    const double* freqs; /* host [rot_dim / 2]: f_i themselves, any finite
-                            numbers (the fields above are then not used); or
+    const double* freqs; /* host [rot_dim / 2]: f_i themselves, of either
+                            sign (the fields above are then not used); or
                             NULL. Read, not kept.                            */
     float amplitude;     /* positive; 1 unless the scaling asks for another  */
     int32_t device;      /* HIP device ordinal                               */
@@ -614,7 +614,8 @@ typedef struct np_rope_desc {
  * device is not looked at. */
 np_status np_rope_freqs(const np_rope_desc* desc, double* freqs);
 
-/* Errors: NP_EINVAL, NP_ENOMEM, NP_EHIP; *out is NULL on any error. destroy
+/* Errors: NP_EINVAL (also where a pair turns by more than 2^40 a position),
+ * NP_ENOMEM, NP_EHIP; *out is NULL on any error. destroy
  * synchronizes the device. A rope may be used from several threads and streams
  * at once. */
 np_status np_rope_create(const np_rope_desc* desc, np_rope** out);
