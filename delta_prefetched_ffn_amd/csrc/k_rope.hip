@@ -3,10 +3,10 @@
 //
 // For a head x of `hd` values at position p, with w the norm's weights (none: x as it is):
 //     y = x * w / sqrt(mean(x^2) + eps),   (y_a, y_b) -> A (y_a cos t - y_b sin t, y_a sin t + y_b cos t)
-// for pair i = (a, b) of the first `rot` values, t = 2 pi p F_i. F_i, a fraction of a turn, is held in 64 bits, so p F_i
-// mod 1 is the low half of an integer product: exact for every position, where a float product p F_i loses the angle of far
-// ones. What is left is an eighth of a turn at most, whose sine and cosine come from their power series in fp32 (off by
-// 4.5e-8 at most, of which their rounding to fp32 is 3.0e-8).
+// for pair i = (a, b) of the first `rot` values, t = 2 pi p F_i. F_i, a fraction of a turn, is held to the nearest 2^-64, so p F_i
+// mod 1 is the low half of an integer product, off by |p| 2^-65 (2^-34 at the farthest positions), where a float product p F_i
+// loses the angle of far ones. What is left is an eighth of a turn at most, whose sine and cosine come from their power series in
+// fp32 (off by 4.5e-8 at most, of which their rounding to fp32 is 3.0e-8).
 //
 // Bound by memory where there are many rows: 4,099 rows of 40 heads of 128 in fp16, 64 values of each turned, 17.1 us (4.9 TB/s, a large
 // copy's rate), one row of 64 heads 4.6 us in the trace, of which an empty launch is 3.4.
@@ -21,16 +21,19 @@ constexpr float kTurn = 1.46291807926715968e-9f, kTurnRest = (float)(1.462918079
 // cos and sin of the angle of pair i at position p, times the amplitude.
 __device__ inline f32x2 turn_of(uint64_t f, int p) {
     const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), u = (uint32_t)p;
-    // the upper word of (f * p) mod 2^64, p sign-extended
-    const uint32_t t = __umulhi(lo, u) + hi * u - (p < 0 ? lo : 0u);
+    // (f * p) mod 2^64, p sign-extended: its upper word t, and the lower one
+    const uint64_t prod = (uint64_t)lo * u;
+    const uint32_t t = (uint32_t)(prod >> 32) + hi * u - (p < 0 ? lo : 0u), below = (uint32_t)prod;
     // t = q quarters + r, r in [-1/8, 1/8) turns
     const uint32_t q = (t + 0x20000000u) >> 30;
-    // x + e = r 2 pi / 2^32, |x| <= pi / 4: the upper bits of r are exact in fp32, and so is what the product with them leaves out.
+    // x + e = (r + below / 2^32) 2 pi / 2^32, |x| <= pi / 4: the upper bits of r are exact in fp32, and so is what the product with
+    // them leaves out.
     const int32_t r = (int32_t)(t - (q << 30)), r0 = r & ~255;
     const float u0 = (float)r0, x = u0 * kTurn;
-    const float e = __builtin_fmaf((float)(r - r0), kTurn, __builtin_fmaf(u0, kTurnRest, __builtin_fmaf(u0, kTurn, -x)));
+    const float rest = __builtin_fmaf((float)below, 0x1p-32f, (float)(r - r0));
+    const float e = __builtin_fmaf(rest, kTurn, __builtin_fmaf(u0, kTurnRest, __builtin_fmaf(u0, kTurn, -x)));
     const float z = __builtin_fmaf(x, x, 2.0f * x * e);
-    // Taylor series: what is left out is below 2^-29 of the sine and of the cosine, whose 1 - z / 2 keeps what its rounding leaves out.
+    // Taylor series: what is left out is below 2^-28 of the sine and 2^-32 of the cosine, whose 1 - z / 2 keeps what its rounding leaves out.
     float s = __builtin_fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
     s = __builtin_fmaf(z, s, 8.33333333e-3f);
     s = __builtin_fmaf(z, s, -1.66666667e-1f);
