@@ -121,13 +121,16 @@ np_status check_call(const np_rope* r, int32_t dtype, float eps) {
     return NP_OK;
 }
 
+// Without rows a tensor may have no address.
+const void* address(const void* p, int64_t rows) { return p || rows > 0 ? p : reinterpret_cast<const void*>(16); }
+
 // The heads of `rows` rows: addresses, strides, and that the results do not overlap each other.
 np_status check_tensor(const np_rope* r, int64_t rows, int32_t heads, const void* in, const void* out, const float* weight, const int64_t* S,
                        int32_t dtype, const char* what) {
     const int hd = r->desc.head_dim, dev = r->desc.device;
     np_status st;
-    if ((st = check_rows(nullptr, in, S[0], S[1], dtype, what)) != NP_OK) return st;
-    if ((st = check_rows(nullptr, out, S[2], S[3], dtype, "the result")) != NP_OK) return st;
+    if ((st = check_rows(nullptr, address(in, rows), S[0], S[1], dtype, what)) != NP_OK) return st;
+    if ((st = check_rows(nullptr, address(out, rows), S[2], S[3], dtype, "the result")) != NP_OK) return st;
     const __int128 row = S[2], head = S[3];
     if (!((head >= hd || heads == 1) && (row >= (heads - 1) * head + hd || rows <= 1)) &&
         !((row >= hd || rows <= 1) && (head >= (rows - 1) * row + hd || heads == 1)))
@@ -135,8 +138,8 @@ np_status check_tensor(const np_rope* r, int64_t rows, int32_t heads, const void
     if (in == out && (S[0] != S[2] || S[1] != S[3]) && rows > 0)
         return fail(NP_EINVAL, "%s: in place, the result must have the input's strides", what);
     if (weight && !aligned16(weight)) return fail(NP_EINVAL, "%s: the weights must be 16-byte aligned", what);
-    if ((st = check_io_ptr(in, dev, what, "rope")) != NP_OK) return st;
-    if ((st = check_io_ptr(out, dev, "the result", "rope")) != NP_OK) return st;
+    if (in && (st = check_io_ptr(in, dev, what, "rope")) != NP_OK) return st;
+    if (out && (st = check_io_ptr(out, dev, "the result", "rope")) != NP_OK) return st;
     if (weight && (st = check_io_ptr(weight, dev, "the weights", "rope")) != NP_OK) return st;
     return NP_OK;
 }

@@ -98,14 +98,15 @@ np_status matvec(const np_w4* w, int64_t rows, const void* x, int32_t x_dtype, i
     if (x_row == 0) x_row = D.n_in;
     if (y_row == 0) y_row = D.n_out;
     const int xb = elem_bytes(x_dtype), yb = elem_bytes(y_dtype);
-    if (!x || !aligned16(x) || x_row < D.n_in || x_row > (int64_t)1 << 36 || x_row * xb % 16)
+    const bool some = rows > 0;  // without rows a tensor may have no address
+    if ((some && !x) || !aligned16(x) || x_row < D.n_in || x_row > (int64_t)1 << 36 || x_row * xb % 16)
         return fail(NP_EINVAL, "x must be a 16-byte aligned device pointer, its stride %lld a multiple of 16 bytes of at least n_in=%d", (long long)x_row, D.n_in);
-    if (!y || (uintptr_t)y % yb || y_row < D.n_out || y_row > (int64_t)1 << 36)
+    if ((some && !y) || (uintptr_t)y % yb || y_row < D.n_out || y_row > (int64_t)1 << 36)
         return fail(NP_EINVAL, "y must be a device pointer aligned to its type, its stride %lld at least n_out=%d", (long long)y_row, D.n_out);
     if (accumulate != 0 && accumulate != 1) return fail(NP_EINVAL, "accumulate=%d must be 0 or 1", accumulate);
     const uint8_t* const x0 = static_cast<const uint8_t*>(x);
     const uint8_t* const y0 = static_cast<const uint8_t*>(y);
-    if (rows > 0 && x0 < y0 + ((rows - 1) * y_row + D.n_out) * yb && y0 < x0 + ((rows - 1) * x_row + D.n_in) * xb) {
+    if (some && x0 < y0 + ((rows - 1) * y_row + D.n_out) * yb && y0 < x0 + ((rows - 1) * x_row + D.n_in) * xb) {
         // Columns of the same rows may belong to both.
         const int64_t step = x_row * xb, off = step ? ((y0 - x0) % step + step) % step : 0;
         if (step != y_row * yb || off < (int64_t)D.n_in * xb || off + (int64_t)D.n_out * yb > step) return fail(NP_EINVAL, "x and y must not overlap");
@@ -113,9 +114,9 @@ np_status matvec(const np_w4* w, int64_t rows, const void* x, int32_t x_dtype, i
     // A launch has at most 2^32 - 1 threads along x: workgroups of 512 for 64 rows x 128 outputs each, at the most.
     if ((rows + 63) / 64 * ((D.n_out + 1023) / 1024 * 8) >= 1 << 23) return fail(NP_EINVAL, "%lld rows of %d outputs in one call are too many", (long long)rows, D.n_out);
     np_status st;
-    if ((st = check_io_ptr(x, D.device, "x", "weights")) != NP_OK) return st;
-    if ((st = check_io_ptr(y, D.device, "y", "weights")) != NP_OK) return st;
-    if (rows == 0) return NP_OK;
+    if (x && (st = check_io_ptr(x, D.device, "x", "weights")) != NP_OK) return st;
+    if (y && (st = check_io_ptr(y, D.device, "y", "weights")) != NP_OK) return st;
+    if (!some) return NP_OK;
     W4Args a;
     a.w = w->view;
     a.x = x;

@@ -628,7 +628,7 @@ np_status np_rope_destroy(np_rope* rope);
  * norm. strides (host, in elements, multiples of 16 bytes; NULL: contiguous): row
  * and head stride of q, q_out, k, k_out. A result may be its input itself (same
  * address and strides), and must not overlap any input in another way, nor
- * itself or the other result. rows 0 enqueues nothing.
+ * itself or the other result. rows 0 enqueues nothing (tensors may be NULL).
  * Errors: NP_EINVAL (also rows above 2^28, or more waves than a launch holds: 2^26). */
 np_status np_rope_apply(const np_rope* rope, int64_t rows, const int32_t* positions, int32_t first, const void* q, void* q_out,
                         int32_t n_heads, const float* q_weight, const void* k, void* k_out, int32_t n_kv_heads,
@@ -687,7 +687,7 @@ np_status np_w4_destroy(np_w4* w);
  * of x_dtype, 16-byte aligned, its row stride (elements; 0: n_in) a multiple of 16
  * bytes; y [rows][n_out] of y_dtype, its row stride 0 (n_out) or at least n_out. x
  * and y must not overlap (columns of the same rows may be either's). rows 0 enqueues
- * nothing. Allocates nothing.
+ * nothing (x and y may be NULL). Allocates nothing.
  * Errors: NP_EINVAL (also rows above 2^20, or workgroups beyond a launch). */
 np_status np_w4_matvec(const np_w4* w, int64_t rows, const void* x, int32_t x_dtype, int64_t x_row, void* y, int32_t y_dtype,
                        int64_t y_row, int32_t accumulate, void* stream);
