@@ -398,8 +398,8 @@ __device__ inline int sequence_of(const PrefixArgs& a, const int* cum, int t, in
 template <typename T, int NS>
 constexpr int kTiles = run_tiles(sizeof(T) == 4 ? kF32 : kBF16, NS);
 
-// Bound by vector instructions (216 of them and 136 scalar ones a wave and piece of 32 tokens x 32 rows, the vector pipes three
-// quarters busy, the matrix units 0.37): 90 sequences of 3 new tokens behind two prompts of up to 30 Ki tokens, 32 over 8 heads of 128 in
+// Bound by vector issue: vector instructions take 0.71 of a SIMD's time, the matrix products among them keep their units busy for 0.37 of
+// it, and a wave waits for its turn to issue for 0.36 of its time, for data and barriers for 0.23. 90 sequences of 3 new tokens behind two prompts of up to 30 Ki tokens, 32 over 8 heads of 128 in
 // bf16, 205 us with the join's 10 (634 TFLOP/s). Few rows are latency: 32 sequences behind one prompt of 8,011 tokens 24.8 us, of
 // which the join takes 6.6.
 //

@@ -8,7 +8,7 @@
 // loses the angle of far ones. What is left is an eighth of a turn at most, whose sine and cosine come from their power series in
 // fp32 (off by 4.5e-8 at most, of which their rounding to fp32 is 3.0e-8).
 //
-// Bound by memory where there are many rows: 4,099 rows of 40 heads of 128 in fp16, 64 values of each turned, 17.1 us (4.9 TB/s, a large
+// Bound by memory where there are many rows: 4,099 rows of 40 heads of 128 in fp16, 64 values of each turned, 17.2 us (4.9 TB/s, a large
 // copy's rate), one row of 64 heads 4.6 us in the trace, of which an empty launch is 3.4.
 #include "kv_quant.hpp"
 #include "rope_internal.hpp"
@@ -223,9 +223,9 @@ __device__ inline int find_row(const RopeBatch& b, int row) {
 
 // K of one page, every `step`th head from h0 on, one block of the cache after the other: a thread holds 16 values of each of CPT new tokens
 // from their load to their codes, and a token's angles for all the heads: 4,097 tokens x 32 heads of 128 in bf16 with their queries
-// and values 55 us with 8 heads a workgroup (3.0 TB/s), 59 with 4, 63 with 2, 68 with 1; 81 when K went through LDS as fp32, which
-// took the room of other workgroups. Eight waves a SIMD, for which the angles spill a few registers, beat six (58 us), and loading
-// the next head during this one, at five, is worse still (66).
+// and values 58 us with 8 heads a workgroup (2.9 TB/s). Measured when it was 55, before the angles' last bits cost it 2: 59 with 4
+// heads, 63 with 2, 68 with 1; 81 when K went through LDS as fp32, which took the room of other workgroups. Eight waves a SIMD, for
+// which the angles spill some 14 registers, beat six (58 us), and loading the next head during this one, at five, was worse still (66).
 template <typename T, int CPT, int MODE>
 __device__ inline void append_k(const RopeAppendArgs& a, int page, int h0, int step, int t0, int lo, int hi, const T* x, float* lds) {
     const KvView& kv = a.kv;

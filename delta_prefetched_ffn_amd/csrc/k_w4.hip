@@ -140,8 +140,9 @@ constexpr int kWaves = 8;
 // their way at a time.
 //
 // Bound by the weights' way from memory at first: one row of 4096 x 11008 takes 7.6 us (3.1 TB/s), of 32,000 x 4096 13.3 us (5.1 TB/s;
-// 25 us before O went up to 4, since every workgroup reads all of x), with the empty launch's 3.5. From 16 rows on the widening and
-// the folds of the groups' sums bound it, with 4096 outputs' 256 workgroups one wave or two a SIMD: 64 rows of 4096 x 4096 18 us.
+// 25 us before O went up to 4, since every workgroup reads all of x), with the empty launch's 3.5. With more rows x itself comes first:
+// every workgroup reads all its rows of it from the caches, 64 rows of 4096 x 4096 134 MB in 18 us, 128 rows of 4096 x 11008 0.72 GB
+// in 82 us (8.8 TB/s).
 template <typename T, int R, int O, int U, bool kStaged, int G>
 __global__ __launch_bounds__(64 * kWaves, R == 1 ? 4 : 2) void k_w4_rows(W4Args a) {
     typedef Kind<T> Kd;
@@ -330,10 +331,10 @@ __global__ __launch_bounds__(64 * kWaves, R == 1 ? 4 : 2) void k_w4_rows(W4Args 
 // of one), three bf16 terms of them, that take the zero points out: one more product per group, with -z as the other operand. Each wave
 // widens the codes of its outputs itself, no two the same ones.
 //
-// Bound by the instructions around the matrix products: per chunk, 128 rows and wave 32 of them need 1,024 cycles, the loads,
-// widening, staging and folds beside them 331 vector instructions. 1,500 rows x 5120 x 15,360 (H = 2, S = 1): 327 us in bf16 (721 TFLOP/s),
-// with groups of 32 429 us; with waves of half the rows x 64 outputs, which widen all codes twice, 345 and 481 us. fp32 (H = 1, S = 2; three
-// products for each) 1,058 us.
+// Bound by waiting, at two waves a SIMD: a wave waits for data and barriers for 0.43 of its time and for its turn to issue for 0.21; the
+// matrix units are busy for 0.36 of theirs, other vector instructions (302 a wave and chunk beside 36 products) take 0.38. 1,500 rows x 5120 x
+// 15,360 (H = 2, S = 1): 325 us in bf16 (726 TFLOP/s), with groups of 32 429 us; with waves of half the rows x 64 outputs, which widen all
+// codes twice, 345 and 481 us. fp32 (H = 1, S = 2; three products for each) 1,058 us.
 //
 // Operand slots: step (s, e) of a chunk, lane half h: inputs 32 s + 8 (h + 2 e) + j, so that a lane's 16 bytes of quad h + 2 e of a
 // tile are its operands of four steps.

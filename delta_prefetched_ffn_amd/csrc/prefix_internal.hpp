@@ -46,8 +46,8 @@ struct PrefixArgs {
 static_assert(sizeof(PrefixArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
 // Row tiles of 16 that a workgroup takes over a run (or over a sequence's own tokens, where it has more than 16 rows), and the
-// waves that a SIMD then holds. A wave issues an instruction about every 8 clocks, a SIMD takes one every 2: more waves of
-// fewer rows are ahead of few of many as long as nothing is spilled. Measured in bf16 at head_dim 128 and 8 kv heads, two tiles at
+// waves that a SIMD then holds. A wave issues an instruction about every 11 clocks, a SIMD takes a vector one every 4: more
+// waves of fewer rows are ahead of few of many (also at 128 values a head, where three waves leave 2 registers to be spilled). Measured in bf16 at head_dim 128 and 8 kv heads, two tiles at
 // three waves against four tiles at two: 32 sequences behind 8,011 tokens 24.8 us for 29, 8 sequences of 31 rows x 4 behind
 // 8,000 tokens 58 for 66; only very long runs of many rows go the other way (two of 30 Ki tokens at most for 540 rows each, 205 for 181).
 constexpr int run_tiles(int dtype, int slabs) { return slabs <= 2 ? 2 : 1; }

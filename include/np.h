@@ -455,8 +455,10 @@ typedef struct np_kv_desc {
 np_status np_kv_bytes(const np_kv_desc* desc, int64_t* out2);
 
 /* A cache of empty sequences. The contents of the pool are kept. desc is
- * copied. Errors: NP_EINVAL (a limit above, a pointer that the device cannot
- * reach), NP_ENOMEM, NP_EHIP; *out is NULL on any error. */
+ * copied. Allocates on the device, besides 4 bytes an entry of the page table,
+ * scratch for 65,536 partial results of (head_dim rounded up to 64) + 2 fp32
+ * values: 17, 34, 51 or 68 MB. Errors: NP_EINVAL (a limit above, a pointer that
+ * the device cannot reach), NP_ENOMEM, NP_EHIP; *out is NULL on any error. */
 np_status np_kv_create(const np_kv_desc* desc, np_kv** out);
 
 /* Synchronizes the device and frees what the cache allocated (not the pool). */
@@ -562,11 +564,19 @@ np_status np_kv_info(const np_kv* kv, int32_t* out4);
  * whole pages of earlier tokens that several sequences of the step have in common, from their
  * first page on, is read once for the rows of all of them instead of once for each;
  * runs may branch (a conversation forked from a conversation). What is shared is
- * seen from the page lists; the caller says nothing. Where too little is shared
- * for that to pay, or a sequence has many new tokens, it is np_kv_attend itself.
- * Results are those of np_kv_attend up to the order of the fp32 sums, and the
- * same from run to run. Two launches; a captured call replays with the runs of the
- * capture (as np_kv_attend with its sequences and lengths). */
+ * seen from the page lists; the caller says nothing. Where a host estimate of both
+ * says that too little is shared for that to pay, or a sequence has many new
+ * tokens (128 or more rows of a key/value head), it is np_kv_attend itself; near
+ * the estimate's break-even the other one may be the faster.
+ * Results are those of np_kv_attend up to the order of the fp32 sums and the
+ * roundings of the weights, and the same from run to run. V scales that lie more
+ * than 2^40 below the largest may vanish, as there; with a window the largest
+ * counts among the shared tokens that up to 32 rows see, which may be rows of
+ * several sequences. Two launches; the first call after np_kv_extend (of a
+ * dtype, window and sinks) also divides the work, on the host: some 10 us for 32
+ * sequences, 35 for 127. A captured call replays with the runs of the capture, whose
+ * pages it looks up in the list of one of the sequences that share them: all of
+ * these must hold them still (np_kv_compact may have moved them). */
 np_status np_attend_shared(np_kv* kv, int32_t layer, const void* q, void* out, float* lse, int32_t dtype,
                            const int64_t* strides, float scale, int32_t window, int32_t sinks, void* stream);
 
