@@ -1136,7 +1136,9 @@ np_status np_layer_create(const np_layer_desc* desc, np_layer** out) {
 np_status np_layer_destroy(np_layer* L) {
     if (!L) return fail(NP_EINVAL, "layer must not be NULL");
     DeviceGuard g(L->desc.device);
-    (void)hipDeviceSynchronize();
+    CaptureGuard c;
+    (void)hipFree(L->buf);  // waits for the device
+    L->buf = nullptr;
     drop_plans_with(L);
     free_layer(L);
     return NP_OK;

@@ -38,4 +38,17 @@ struct DeviceGuard {
     }
 };
 
+// What a handle's destruction does within this scope leaves streams alone that are being captured: Python's collector may
+// drop a handle at any time. hipDeviceSynchronize would end the capture nevertheless; hipFree waits for the device as well, and does
+// not. (The runtime has the call; a host build over a stand-in for it may lack it.)
+extern "C" hipError_t hipThreadExchangeStreamCaptureMode(hipStreamCaptureMode*) __attribute__((weak));
+struct CaptureGuard {
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    static void exchange(hipStreamCaptureMode* m) {
+        if (hipThreadExchangeStreamCaptureMode) (void)hipThreadExchangeStreamCaptureMode(m);
+    }
+    CaptureGuard() { exchange(&mode); }
+    ~CaptureGuard() { exchange(&mode); }
+};
+
 }  // namespace np

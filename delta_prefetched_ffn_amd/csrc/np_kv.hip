@@ -574,8 +574,8 @@ np_status np_kv_destroy(np_kv* kv) {
         return NP_OK;
     }
     DeviceGuard g(kv->desc.device);
-    (void)hipDeviceSynchronize();
-    delete kv;
+    CaptureGuard c;
+    delete kv;  // its first hipFree waits for the device
     return NP_OK;
 }
 

@@ -270,8 +270,8 @@ np_status np_rope_create(const np_rope_desc* desc, np_rope** out) {
 np_status np_rope_destroy(np_rope* rope) {
     if (!rope) return fail(NP_EINVAL, "rope must not be NULL");
     DeviceGuard g(rope->desc.device);
-    (void)hipDeviceSynchronize();
-    delete rope;
+    CaptureGuard c;
+    delete rope;  // hipFree waits for the device
     return NP_OK;
 }
 

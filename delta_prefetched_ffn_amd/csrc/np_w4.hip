@@ -143,8 +143,8 @@ np_status np_w4_create(const np_w4_desc* desc, np_w4** out) {
 np_status np_w4_destroy(np_w4* w) {
     if (!w) return fail(NP_EINVAL, "w must not be NULL");
     DeviceGuard g(w->desc.device);
-    (void)hipDeviceSynchronize();
-    delete w;
+    CaptureGuard c;
+    delete w;  // its first hipFree waits for the device
     return NP_OK;
 }
 

@@ -461,7 +461,9 @@ np_status np_kv_bytes(const np_kv_desc* desc, int64_t* out2);
  * the device cannot reach), NP_ENOMEM, NP_EHIP; *out is NULL on any error. */
 np_status np_kv_create(const np_kv_desc* desc, np_kv** out);
 
-/* Synchronizes the device and frees what the cache allocated (not the pool). */
+/* Synchronizes the device and frees what the cache allocated (not the pool). This
+ * and the other handles' destroy calls may be made while a stream is captured: the
+ * capture goes on. */
 np_status np_kv_destroy(np_kv* kv);
 
 /* Every sequence empty, every page free. Enqueues nothing. */
