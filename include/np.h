@@ -591,7 +591,7 @@ np_status np_attend_shared(np_kv* kv, int32_t layer, const void* q, void* out, f
  * values from rot_dim on stay as they are. Computed in fp32 and rounded once;
  * the angle is exact to 2^-34 turns at any 32-bit position (f_i is held as a
  * 64-bit fraction of a turn). Squares are summed in fp32: a norm of values
- * above 2^59 overflows. Not-a-number and infinite values spread as in the
+ * above 2^59 overflows, and with eps 0 one of values below 2^-60 underflows. Not-a-number and infinite values spread as in the
  * formulas (within their head). */
 typedef struct np_rope np_rope; /* opaque: one rotation, read-only after create */
 
@@ -662,8 +662,8 @@ np_status np_rope_append(const np_rope* rope, np_kv* kv, int32_t layer, const vo
  * The dense projections next to the sparse FFNs, at a quarter of their bf16
  * bytes. A weight is a code c in 0 .. 15 with its group's scale and zero point,
  *   w[o][i] = scale[o][i / group] * (c[o][i] - zero[o][i / group]),
- * and y[r][o] = sum_i w[o][i] x[r][i]. Codes, zero points and x enter exactly;
- * per group, the fp32 sums of c x and of x are joined to sum (c - zero) x and times
+ * and y[r][o] = sum_i w[o][i] x[r][i]. Codes, zero points and x enter exactly (of
+ * an fp32 x, what lies above 2^-133: all of a value from 2^-110 on); per group, the fp32 sums of c x and of x are joined to sum (c - zero) x and times
  * the scale in fp32, groups are summed in fp32, and y is rounded once. Sums of
  * c x above fp32's range overflow even where the scale would bring them back. Results are
  * the same from run to run; a row's bits may differ between calls with other

@@ -98,3 +98,23 @@ def test_subnormal_fp16_inputs(rows, n_out, n_in, takes):
     w.matvec(rows, xt.data_ptr(), "f16", y.data_ptr(), "f32", stream=torch.cuda.current_stream().cuda_stream)
     want = x @ ((c - np.repeat(z, 64, 1)[:, :n_in]) * 0.5).T
     assert np.array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("rows,n_out,n_in,takes", [(3, 70, 264, ("rows", 1)), (60, 70, 264, ("rows", 4)), (260, 8200, 264, ("tile", 8)), (4100, 1100, 264, ("tile", 4))])
+def test_tiny_inputs(rows, n_out, n_in, takes):
+    # bf16 numbers below 2^-126, and fp32 ones down to where bf16 summands end (2^-133); large scales make them visible.
+    rng = np.random.default_rng(rows)
+    groups = -(-n_in // 64)
+    c = 1 << rng.integers(0, 4, (n_out, n_in))
+    w = matrix(c, np.full((n_out, groups), 2.0 ** 60), np.zeros((n_out, groups), np.int64), 64, "f32")
+    assert kernel(w, rows, n_in, n_out, "bf16") == takes
+    at = rng.integers(0, n_in, rows)
+    for xd, lowest, bits in (("bf16", -133, 0), ("bf16", -130, 3), ("bf16", -126, 7), ("f32", -110, 23), ("f32", -120, 23)):
+        x = np.zeros((rows, n_in))
+        x[np.arange(rows), at] = ((1 << bits) + rng.integers(0, 1 << bits, rows)) * 2.0 ** (lowest - bits) * rng.choice([-1, 1], rows)
+        xt, y = torch.from_numpy(x.astype(np.float32)).to(tdt(xd)).cuda(), torch.empty((rows, n_out), device="cuda")
+        assert np.array_equal(xt.double().cpu().numpy(), x)
+        w.matvec(rows, xt.data_ptr(), xd, y.data_ptr(), "f32", stream=torch.cuda.current_stream().cuda_stream)
+        cx = c[:, at].T * 2.0 ** 60
+        err = np.abs(y.double().cpu().numpy() - x[np.arange(rows), at][:, None] * cx)
+        assert (err <= (2.0 ** -133 * cx if lowest < -110 and xd == "f32" else 0)).all(), (xd, lowest)
